@@ -83,6 +83,7 @@ typedef enum { MTP_F32 = 0, MTP_BF16 = 1 } mtp_dtype;
 #define MTP_ERR_TIMEOUT    0x20u /* a bounded wait inside a kernel gave up */
 #define MTP_ERR_MODE       0x40u /* mode > 2, or mode 2 while relaxed_topk is 0 (decided greedily) */
 #define MTP_ERR_TREE       0x80u /* malformed parents list (that request is treated as a chain) */
+#define MTP_ERR_SCALE      0x100u /* scale of a partly filled 8-bit block is not positive and finite */
 
 /* ------------------------------------------------------------------------ */
 /* 1. Verify attention with KV append.
@@ -380,6 +381,135 @@ typedef struct {
 int kv_rollback(const mtp_rollback_args* args, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* 4. The cache in 8 bits, and attention behind a window.
+ *
+ * The pages give neither; both follow from the verify step's own cost: its
+ * attention is bound by reading the cache, so a cache of half the bytes, or
+ * one of which only a window is read, is read in half the time or less.
+ *
+ * 4a. Append to an 8-bit cache.
+ *
+ * The cache holds e4m3 bytes (value = byte * scale) with one float scale for
+ * each block and KV head, K and V apart. Request b appends the tokens
+ * starts[b] .. starts[b+1]-1 of k_new / v_new at slots ctx_lens[b] and up;
+ * any number of them, none included (a prefill chunk, the tokens of a step).
+ * With a the largest finite magnitude that the call writes into a block's
+ * head, its scale becomes
+ *   2^e, the smallest e >= -100 with a <= 448 * 2^e,  where the call writes
+ *        the block's first slot (what the block held before is forgotten);
+ *   the old scale doubled until a <= 448 * scale,     otherwise. The slots
+ *        before the first written one are rounded again to the new scale
+ *        (exact unless a byte becomes subnormal); slots behind the last
+ *        written one keep their bytes, which no row sees.
+ * A written byte is e4m3(x / scale), to nearest even; x that is not finite
+ * is stored as NaN and reaches the rows that see it. No two requests' slots
+ * may share a block that is written.
+ *   k_new, v_new [T, Hkv, d] dtype (MTP_F32 or MTP_BF16), d 64 or 128
+ *   starts       [B+1] int32, not decreasing, within [0, T]
+ *   k_cache, v_cache [num_blocks, 64, Hkv, d] e4m3 bytes
+ *   k_scale, v_scale [num_blocks, Hkv] float
+ *   block_table [B, max_blocks] int32;  ctx_lens [B] int32
+ * k_new, v_new and the caches must be 16-byte aligned. Errors: a request with
+ * bad starts or slots beyond max_blocks sets MTP_ERR_LENGTH, a block id
+ * outside [0, num_blocks) MTP_ERR_BLOCK_ID, an old scale that is needed and
+ * not positive and finite MTP_ERR_SCALE; that request's (block's, head's)
+ * tokens are not written. */
+typedef struct {
+  const void* k_new;
+  const void* v_new;
+  const int32_t* starts;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  int32_t T, B, Hkv, d;
+  int32_t block_size, max_blocks, num_blocks;
+  int32_t dtype;             /* mtp_dtype of k_new, v_new */
+} mtp_kv8_append_args;
+
+int mtp_kv8_append(const mtp_kv8_append_args* args, void* stream);
+
+/* 4b. Verify attention over the 8-bit cache, and behind a window.
+ *
+ * mtp_verify_attention's append and attention for chains of drafts, with two
+ * changes. mtp_verify_attention_kv8 keeps the cache as in 4a: the R verify
+ * tokens' K/V are quantised into it first, and every row reads the quantised
+ * values, its own token's included. And row j of request b, at position
+ * p = ctx + j, sees slot t <= p iff
+ *   window == 0, or t > p - window, or t < sinks:
+ * the last `window` positions, its own among them, and the first `sinks`
+ * tokens. mtp_verify_attention_window is the same over the cache of
+ * mtp_verify_attention (K/V in `dtype`, k_scale and v_scale NULL) and needs
+ * window >= 1. A block no row sees is not read, and its table entry may be
+ * anything (kv_window_release sets it to -1). Sums and softmax statistics are
+ * fp32; with bf16 rows the probabilities of a tile are rounded to 16 bits
+ * before they meet V.
+ *   q, out       [B, R, Hq, d] dtype (MTP_F32 or MTP_BF16), d 64 or 128
+ *   k_new, v_new [B, R, Hkv, d] dtype
+ *   k_cache, v_cache [num_blocks, 64, Hkv, d] e4m3 bytes (kv8) or dtype
+ *   k_scale, v_scale [num_blocks, Hkv] float (kv8) or NULL
+ * R = D+1 <= 16, Hq % Hkv == 0. q, out, k_new, v_new and the caches must be
+ * 16-byte aligned. Errors are those of the append and of
+ * mtp_verify_attention: a request of bad length is skipped (its rows of out
+ * stay as they were), a block with a bad id takes no part. Trees of drafts and MLA are not
+ * provided in these forms. */
+typedef struct {
+  const void* q;
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  void* out;
+  int32_t B, D, Hq, Hkv, d;
+  int32_t block_size, max_blocks, num_blocks;
+  int32_t window, sinks;
+  float sm_scale;
+  int32_t dtype;             /* mtp_dtype */
+  void* workspace;           /* device, >= the entry's *_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* timing_events[2];    /* as in mtp_attn_args */
+} mtp_window_attn_args;
+
+size_t mtp_attention_kv8_workspace_size(const mtp_window_attn_args* args);
+int mtp_verify_attention_kv8(const mtp_window_attn_args* args, void* stream);
+size_t mtp_attention_window_workspace_size(const mtp_window_attn_args* args);
+int mtp_verify_attention_window(const mtp_window_attn_args* args, void* stream);
+
+/* 4c. Giving back the blocks that have left the window.
+ *
+ * With seq_lens[b] = L tokens kept (kv_rollback's result), the next rows sit
+ * at positions >= L, and block i holds nothing they see iff
+ * ceil(sinks/64) <= i < (L - window + 1) / 64. Every such block whose table
+ * entry is >= 0 is appended to free_list from position *free_count on
+ * (request-major, block index ascending), its entry becomes -1, and
+ * *free_count is advanced. A request is released whole or not at all: as in
+ * kv_rollback, one whose blocks do not fit after those of every earlier
+ * request stays as it was and sets MTP_ERR_FREE_LIST. L < 0 or beyond
+ * max_blocks sets MTP_ERR_LENGTH and skips the request.
+ *   block_table [B, max_blocks] int32 (in/out); seq_lens [B] int32
+ *   free_list [free_capacity] int32; free_count [1] int32 (in/out)
+ *   workspace: device, >= mtp_window_release_workspace_size(B) bytes, 256-byte aligned */
+typedef struct {
+  int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t* free_list;
+  int32_t* free_count;
+  int32_t B, block_size, max_blocks, free_capacity;
+  int32_t window, sinks;
+  void* workspace;
+  size_t workspace_bytes;
+} mtp_window_release_args;
+
+size_t mtp_window_release_workspace_size(int32_t B);
+int kv_window_release(const mtp_window_release_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Bounded-wait check (validation only, not on the verify path).
  *
  * The tensor-core kernels wait on shared-memory mbarriers (TMA copies, MMA
@@ -442,7 +572,8 @@ int mtp_last_launch_count(void);
 
 /* ABI version (MTP_ABI_VERSION) and sizeof of the argument structs
  * (0 = mtp_attn_args, 1 = mtp_lmhead_args, 2 = mtp_rollback_args,
- * 3 = mtp_draft_args, 4 = mtp_kv_compact_args), for
+ * 3 = mtp_draft_args, 4 = mtp_kv_compact_args, 5 = mtp_kv8_append_args,
+ * 6 = mtp_window_attn_args, 7 = mtp_window_release_args), for
  * bindings to check their struct layouts against. */
 int mtp_abi_version(void);
 size_t mtp_abi_struct_size(int which);

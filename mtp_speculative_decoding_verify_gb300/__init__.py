@@ -7,10 +7,14 @@ seeded synthetic-workload generators used by the tests and the benchmark.
 from ._binding import (  # noqa: F401
     MtpError,
     kv_rollback,
+    kv_window_release,
     lib,
     mtp_draft_argmax,
+    mtp_kv8_append,
     mtp_tree_kv_compact,
     mtp_verify_attention,
+    mtp_verify_attention_kv8,
+    mtp_verify_attention_window,
     mtp_verify_logits_accept,
     mtp_verify_logits_accept_noalloc,
     sync_status,

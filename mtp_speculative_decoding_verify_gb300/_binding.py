@@ -5,6 +5,7 @@ contiguity, their raw pointers go into the C argument structs, and every step
 of the verify path runs in the library's CUDA kernels. There is no CPU
 fallback: if the library is missing, loading it raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -60,6 +61,26 @@ class RollbackArgs(ctypes.Structure):
                 ("free_capacity", _I)]
 
 
+class Kv8AppendArgs(ctypes.Structure):
+    _fields_ = [("k_new", _P), ("v_new", _P), ("starts", _P), ("k_cache", _P), ("v_cache", _P), ("k_scale", _P),
+                ("v_scale", _P), ("block_table", _P), ("ctx_lens", _P), ("T", _I), ("B", _I), ("Hkv", _I), ("d", _I),
+                ("block_size", _I), ("max_blocks", _I), ("num_blocks", _I), ("dtype", _I)]
+
+
+class WindowAttnArgs(ctypes.Structure):
+    _fields_ = [("q", _P), ("k_new", _P), ("v_new", _P), ("k_cache", _P), ("v_cache", _P), ("k_scale", _P),
+                ("v_scale", _P), ("block_table", _P), ("ctx_lens", _P), ("out", _P), ("B", _I), ("D", _I), ("Hq", _I),
+                ("Hkv", _I), ("d", _I), ("block_size", _I), ("max_blocks", _I), ("num_blocks", _I), ("window", _I),
+                ("sinks", _I), ("sm_scale", ctypes.c_float), ("dtype", _I), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("timing_events", _P * 2)]
+
+
+class WindowReleaseArgs(ctypes.Structure):
+    _fields_ = [("block_table", _P), ("seq_lens", _P), ("free_list", _P), ("free_count", _P), ("B", _I),
+                ("block_size", _I), ("max_blocks", _I), ("free_capacity", _I), ("window", _I), ("sinks", _I),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
 class MtpError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__("mtp status %d: %s" % (code, msg))
@@ -108,6 +129,18 @@ def lib():
         L.mtp_draft_argmax.restype = ctypes.c_int
         L.mtp_tree_kv_compact.argtypes = [ctypes.POINTER(KvCompactArgs), _P]
         L.mtp_tree_kv_compact.restype = ctypes.c_int
+        L.mtp_kv8_append.argtypes = [ctypes.POINTER(Kv8AppendArgs), _P]
+        L.mtp_kv8_append.restype = ctypes.c_int
+        for name in ("kv8", "window"):
+            size, call = getattr(L, "mtp_attention_%s_workspace_size" % name), getattr(L, "mtp_verify_attention_" + name)
+            size.argtypes = [ctypes.POINTER(WindowAttnArgs)]
+            size.restype = ctypes.c_size_t
+            call.argtypes = [ctypes.POINTER(WindowAttnArgs), _P]
+            call.restype = ctypes.c_int
+        L.mtp_window_release_workspace_size.argtypes = [ctypes.c_int32]
+        L.mtp_window_release_workspace_size.restype = ctypes.c_size_t
+        L.kv_window_release.argtypes = [ctypes.POINTER(WindowReleaseArgs), _P]
+        L.kv_window_release.restype = ctypes.c_int
         L.mtp_hbm_read_probe.argtypes = [_P, ctypes.c_size_t, _P, ctypes.c_int32, ctypes.c_int32, _P]
         L.mtp_hbm_read_probe.restype = ctypes.c_int
         L.mtp_abi_version.argtypes = []
@@ -116,7 +149,8 @@ def lib():
         L.mtp_abi_struct_size.restype = ctypes.c_size_t
         if L.mtp_abi_version() != ABI_VERSION:
             raise RuntimeError("library ABI version %d, binding expects %d" % (L.mtp_abi_version(), ABI_VERSION))
-        for which, st in enumerate((AttnArgs, LmArgs, RollbackArgs, DraftArgs, KvCompactArgs)):
+        for which, st in enumerate((AttnArgs, LmArgs, RollbackArgs, DraftArgs, KvCompactArgs, Kv8AppendArgs,
+                                    WindowAttnArgs, WindowReleaseArgs)):
             if L.mtp_abi_struct_size(which) != ctypes.sizeof(st):
                 raise RuntimeError("ABI mismatch for %s" % st.__name__)
         _lib = L
@@ -372,6 +406,145 @@ def kv_rollback(block_table, seq_lens, num_accepted, free_list, free_count, *, D
     """Truncate each request to ctx + n + 1 slots and release blocks holding only rejected drafts."""
     a = rollback_args(block_table, seq_lens, num_accepted, free_list, free_count, D=D)
     _check(lib().kv_rollback(ctypes.byref(a), _stream_handle(stream)))
+
+
+def _same_device(first, *tensors):
+    """The CUDA device that all the tensors are on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError("tensors on %s and %s in one call" % (dev, t.device))
+    return dev
+
+
+def _launch(dev, stream, call):
+    """call(stream handle) with the tensors' device current, on `stream` or that device's current one.
+    The workspace that a call allocates meanwhile belongs to that stream, so that no other call shares it."""
+    with contextlib.ExitStack() as stack:
+        if torch.cuda.current_device() != dev.index:
+            stack.enter_context(torch.cuda.device(dev))
+        if stream is not None:
+            stack.enter_context(torch.cuda.stream(stream))
+        else:
+            stream = torch.cuda.current_stream(dev)
+        _check(call(stream.cuda_stream))
+
+
+def mtp_kv8_append(k_new, v_new, starts, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, *, stream=None):
+    """Quantise a ragged batch of new K/V into the 8-bit paged cache.
+
+    k_new, v_new [T, Hkv, d] (float32 or bfloat16, d 64 or 128); starts [B+1] int32: request b appends tokens
+    starts[b] .. starts[b+1]-1 at slots ctx_lens[b] and up; k_cache, v_cache [blocks, 64, Hkv, d] float8_e4m3fn;
+    k_scale, v_scale [blocks, Hkv] float32 (both updated); block_table [B, max_blocks] int32, ctx_lens [B] int32.
+    """
+    T, Hkv, d = k_new.shape
+    B, max_blocks = block_table.shape
+    dt, nb = k_new.dtype, k_cache.shape[0]
+    dev = _same_device(k_new, v_new, starts, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens)
+    _dev(k_new, "k_new")
+    _dev(v_new, "v_new", dt, (T, Hkv, d))
+    _dev(starts, "starts", torch.int32, (B + 1,))
+    _kv8_cache(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(ctx_lens, "ctx_lens", torch.int32, (B,))
+    a = Kv8AppendArgs(k_new.data_ptr(), v_new.data_ptr(), starts.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                      k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(), T, B, Hkv,
+                      d, BLOCK_SIZE, max_blocks, nb, _dtype_code(k_new))
+    _launch(dev, stream, lambda s: lib().mtp_kv8_append(ctypes.byref(a), s))
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d):
+    _dev(k_cache, "k_cache", torch.float8_e4m3fn, (nb, BLOCK_SIZE, Hkv, d))
+    _dev(v_cache, "v_cache", torch.float8_e4m3fn, (nb, BLOCK_SIZE, Hkv, d))
+    _dev(k_scale, "k_scale", torch.float32, (nb, Hkv))
+    _dev(v_scale, "v_scale", torch.float32, (nb, Hkv))
+
+
+def _window_attention(name, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, window,
+                      sinks, sm_scale, workspace, stream):
+    B, R, Hq, d = q.shape
+    nb, _, Hkv, _ = k_cache.shape
+    dt = q.dtype
+    dev = _same_device(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, out)
+    if k_scale is None:
+        _dev(k_cache, "k_cache", dt, (nb, BLOCK_SIZE, Hkv, d))
+        _dev(v_cache, "v_cache", dt, (nb, BLOCK_SIZE, Hkv, d))
+    else:
+        _same_device(q, k_scale, v_scale)
+        _kv8_cache(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d)
+    _dev(q, "q")
+    _dev(k_new, "k_new", dt, (B, R, Hkv, d))
+    _dev(v_new, "v_new", dt, (B, R, Hkv, d))
+    _dev(out, "out", dt, (B, R, Hq, d))
+    _dev(block_table, "block_table", torch.int32)
+    _dev(ctx_lens, "ctx_lens", torch.int32, (B,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must have shape (%d, max_blocks), got %s" % (B, tuple(block_table.shape)))
+    a = WindowAttnArgs(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                       None if k_scale is None else k_scale.data_ptr(), None if v_scale is None else v_scale.data_ptr(),
+                       block_table.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), B, R - 1, Hq, Hkv, d, BLOCK_SIZE,
+                       block_table.shape[1], nb, min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1),
+                       d ** -0.5 if sm_scale is None else float(sm_scale), _dtype_code(q))
+    L, ref = lib(), ctypes.byref(a)
+
+    def call(s):
+        ws = workspace
+        if ws is None:
+            n = getattr(L, "mtp_attention_%s_workspace_size" % name)(ref)
+            if n == 0:
+                _check(MTP_INVALID_ARG)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        return getattr(L, "mtp_verify_attention_" + name)(ref, s)
+
+    _launch(dev, stream, call)
+
+
+def mtp_verify_attention_kv8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, *,
+                             window=0, sinks=0, sm_scale=None, workspace=None, stream=None):
+    """Quantise the verify tokens' K/V into the 8-bit paged cache and run verify attention over it into `out`.
+
+    q, out [B, R, Hq, d], k_new, v_new [B, R, Hkv, d] (float32 or bfloat16, d 64 or 128); k_cache, v_cache
+    [blocks, 64, Hkv, d] float8_e4m3fn, k_scale, v_scale [blocks, Hkv] float32 (as mtp_kv8_append keeps them);
+    block_table [B, max_blocks] int32, ctx_lens [B] int32. window > 0: a row sees the last `window` positions and the
+    first `sinks` tokens; window = 0: all. Chains of drafts only.
+    """
+    _window_attention("kv8", q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, window,
+                      sinks, sm_scale, workspace, stream)
+
+
+def mtp_verify_attention_window(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, out, *, window, sinks=0,
+                                sm_scale=None, workspace=None, stream=None):
+    """mtp_verify_attention for chains in which a row sees the last `window` >= 1 positions, its own among them, and
+    the first `sinks` tokens (GQA/MHA caches [blocks, 64, Hkv, d] of q's type, d 64 or 128). Blocks that no row sees
+    are not read; their table entries may be -1."""
+    _window_attention("window", q, k_new, v_new, k_cache, v_cache, None, None, block_table, ctx_lens, out, window,
+                      sinks, sm_scale, workspace, stream)
+
+
+def kv_window_release(block_table, seq_lens, free_list, free_count, *, window, sinks=0, workspace=None, stream=None):
+    """Return the blocks that no row at a position >= seq_lens sees behind `window` and `sinks` to the free list."""
+    B, max_blocks = block_table.shape
+    dev = _same_device(block_table, seq_lens, free_list, free_count)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32, (B,))
+    _dev(free_list, "free_list", torch.int32)
+    _dev(free_count, "free_count", torch.int32, (1,))
+    L = lib()
+    a = WindowReleaseArgs(block_table.data_ptr(), seq_lens.data_ptr(), free_list.data_ptr(), free_count.data_ptr(), B,
+                          BLOCK_SIZE, max_blocks, free_list.numel(), min(int(window), 2 ** 31 - 1),
+                          min(int(sinks), 2 ** 31 - 1))
+
+    def call(s):
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(L.mtp_window_release_workspace_size(B), dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        return L.kv_window_release(ctypes.byref(a), s)
+
+    _launch(dev, stream, call)
 
 
 def sync_status(stream=None):

@@ -213,6 +213,9 @@ size_t mtp_abi_struct_size(int which) {
     case 2: return sizeof(mtp_rollback_args);
     case 3: return sizeof(mtp_draft_args);
     case 4: return sizeof(mtp_kv_compact_args);
+    case 5: return sizeof(mtp_kv8_append_args);
+    case 6: return sizeof(mtp_window_attn_args);
+    case 7: return sizeof(mtp_window_release_args);
     default: return 0;
   }
 }
@@ -330,11 +333,12 @@ int mtp_sync_status(void* stream) {
   if (word == 0) return MTP_OK;
   e = cudaMemset(c->err, 0, sizeof word);
   if (e != cudaSuccess) return cuda_fail(e, "clearing the error word");
-  return fail(MTP_DEVICE_ERROR, "device range check failed: 0x%x%s%s%s%s%s%s%s%s", word,
+  return fail(MTP_DEVICE_ERROR, "device range check failed: 0x%x%s%s%s%s%s%s%s%s%s", word,
               (word & MTP_ERR_BLOCK_ID) ? " block-id" : "", (word & MTP_ERR_TOKEN_ID) ? " token-id" : "",
               (word & MTP_ERR_LENGTH) ? " length" : "", (word & MTP_ERR_ACCEPTED) ? " num-accepted" : "",
               (word & MTP_ERR_FREE_LIST) ? " free-list" : "", (word & MTP_ERR_TIMEOUT) ? " timeout" : "",
-              (word & MTP_ERR_MODE) ? " mode" : "", (word & MTP_ERR_TREE) ? " tree" : "");
+              (word & MTP_ERR_MODE) ? " mode" : "", (word & MTP_ERR_TREE) ? " tree" : "",
+              (word & MTP_ERR_SCALE) ? " scale" : "");
 }
 
 }  // extern "C"
