@@ -34,7 +34,12 @@ __global__ void __launch_bounds__(128) window_append_kernel(const uint4* __restr
                                                             uint4* __restrict__ v_cache,
                                                             const int32_t* __restrict__ block_table,
                                                             const int32_t* __restrict__ ctx_lens, int R, int vecs,
-                                                            int max_blocks, int num_blocks, unsigned* err) {
+                                                            int max_blocks, int num_blocks, unsigned* err,
+                                                            const WindowSchedule schedule) {
+  if (schedule.prefix != nullptr && blockIdx.x == gridDim.x - 1) {
+    window_schedule<128>(schedule);
+    return;
+  }
   const int b = blockIdx.x / R, j = blockIdx.x % R;
   const int ctx = ctx_lens[b];
   if (ctx < 0 || ctx > max_blocks * kBlock - R) {
@@ -66,13 +71,6 @@ template <typename T> struct KvLoad;
 template <> struct KvLoad<float> {
   __device__ __forceinline__ static float4 get(const void* base, int64_t elem) {
     return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-  }
-};
-template <> struct KvLoad<__nv_bfloat16> {
-  __device__ __forceinline__ static float4 get(const void* base, int64_t elem) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + elem);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
   }
 };
 template <> struct KvLoad<uint8_t> {
@@ -306,7 +304,11 @@ int check_window(const mtp_window_attn_args* a, bool kv8) {
   return MTP_OK;
 }
 
-WindowPlan plan_window(const mtp_window_attn_args& a, int sm_count) {
+// The tensor cores take bf16 rows, the SIMT kernel fp32 ones.
+bool uses_mma(const mtp_window_attn_args& a) { return a.dtype == MTP_BF16; }
+
+WindowPlan plan_window(const mtp_window_attn_args& a, bool kv8, int sm_count) {
+  if (uses_mma(a)) return plan_window_mma(a, kv8, sm_count);
   WindowPlan p{};
   const int rows = a.Hq / a.Hkv * (a.D + 1);
   const long long ctas = (long long)a.B * a.Hkv * ((rows + kSimtRows - 1) / kSimtRows);
@@ -330,10 +332,10 @@ size_t workspace_size(const mtp_window_attn_args* a, bool kv8) {
   unsigned* err = nullptr;
   int sm_count = 0;
   if (device_context(&err, &sm_count) != MTP_OK) return 0;
-  return plan_window(*a, sm_count).ws_bytes;
+  return plan_window(*a, kv8, sm_count).ws_bytes;
 }
 
-cudaError_t append(const mtp_window_attn_args& a, bool kv8, unsigned* err, cudaStream_t s) {
+cudaError_t append(const mtp_window_attn_args& a, bool kv8, const WindowSchedule& sch, unsigned* err, cudaStream_t s) {
   if (kv8) {
     mtp_kv8_append_args k{};
     k.k_new = a.k_new;
@@ -351,12 +353,12 @@ cudaError_t append(const mtp_window_attn_args& a, bool kv8, unsigned* err, cudaS
     k.max_blocks = a.max_blocks;
     k.num_blocks = a.num_blocks;
     k.dtype = a.dtype;
-    return launch_kv8_append(k, a.D + 1, err, s);
+    return launch_kv8_append(k, a.D + 1, sch, err, s);
   }
   const int vecs = a.Hkv * a.d * (a.dtype == MTP_BF16 ? 2 : 4) / 16;
-  window_append_kernel<<<a.B * (a.D + 1), 128, 0, s>>>(
+  window_append_kernel<<<a.B * (a.D + 1) + (sch.prefix ? 1 : 0), 128, 0, s>>>(
       (const uint4*)a.k_new, (const uint4*)a.v_new, (uint4*)a.k_cache, (uint4*)a.v_cache, a.block_table, a.ctx_lens,
-      a.D + 1, vecs, a.max_blocks, a.num_blocks, err);
+      a.D + 1, vecs, a.max_blocks, a.num_blocks, err, sch);
   return cudaGetLastError();
 }
 
@@ -368,7 +370,7 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
   unsigned* err = nullptr;
   int sm_count = 0;
   if ((rc = device_context(&err, &sm_count)) != MTP_OK) return rc;
-  const WindowPlan pl = plan_window(*a, sm_count);
+  const WindowPlan pl = plan_window(*a, kv8, sm_count);
   if (!a->workspace || a->workspace_bytes < pl.ws_bytes) {
     char buf[160];
     snprintf(buf, sizeof buf, "workspace of %zu bytes needed, %zu given", pl.ws_bytes, a->workspace ? a->workspace_bytes : (size_t)0);
@@ -402,12 +404,35 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.ws_partial_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto record = [&](void* ev) { return ev ? cudaEventRecord(static_cast<cudaEvent_t>(ev), s) : cudaSuccess; };
-  cudaError_t e = append(*a, kv8, err, s);
+  WindowSchedule sch{};
+  const bool mma = uses_mma(*a);
+  if (mma) {
+    p.row_tiles = pl.row_tiles;
+    p.row_warps = pl.row_warps;
+    p.key_parts = pl.key_parts;
+    p.stages = pl.stages;
+    sch.prefix = reinterpret_cast<int64_t*>(static_cast<char*>(a->workspace) + pl.ws_prefix);
+    sch.arrived = reinterpret_cast<int32_t*>(static_cast<char*>(a->workspace) + pl.ws_arrived);
+    sch.n_arrived = (int64_t)p.B * p.Hkv * pl.row_tiles * pl.row_warps;
+    sch.ctx_lens = p.ctx_lens;
+    sch.B = p.B;
+    sch.R = p.R;
+    sch.max_blocks = p.max_blocks;
+    sch.window = p.window;
+    sch.sinks = p.sinks;
+    p.prefix = sch.prefix;
+    p.arrived = sch.arrived;
+  }
+  cudaError_t e = append(*a, kv8, sch, err, s);
   if (e != cudaSuccess) return set_cuda_error(e, "kv append launch");
   if ((e = record(a->timing_events[0])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
   int launches = 0;
-  e = a->dtype == MTP_BF16 ? launch_simt<__nv_bfloat16>(p, a->d, kv8, s, &launches)
-                           : launch_simt<float>(p, a->d, kv8, s, &launches);
+  if (mma) {
+    launches = 1;
+    e = launch_window_mma(*a, kv8, pl, p, s);
+  } else {
+    e = launch_simt<float>(p, a->d, kv8, s, &launches);
+  }
   if (e != cudaSuccess) return set_cuda_error(e, "attention launch");
   if ((e = record(a->timing_events[1])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
   set_launch_count(1 + launches);

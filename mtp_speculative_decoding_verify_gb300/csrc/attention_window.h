@@ -1,5 +1,5 @@
-// Launch parameters shared by the kernels of attention_window.cu and
-// attention_window_mma.cu.
+// Launch parameters shared by attention_window.cu, attention_window_mma.cu
+// and the appends that run before them.
 #pragma once
 
 #include "kernels.h"
@@ -7,8 +7,11 @@
 namespace mtp {
 
 struct WindowPlan {
-  int n_splits;            // SIMT: ranges a request's pages are cut into
-  size_t ws_partial_o, ws_partial_lse, ws_bytes;
+  int n_splits;                      // SIMT: ranges a request's pages are cut into
+  int row_tiles, row_warps, key_parts, stages, ctas_per_head, smem;   // tensor cores
+  size_t ws_partial_o, ws_partial_lse;
+  size_t ws_prefix, ws_arrived;
+  size_t ws_bytes;
 };
 
 struct WindowParams {
@@ -17,11 +20,30 @@ struct WindowParams {
   const void *k_cache, *v_cache;
   const float *k_scale, *v_scale;   // [num_blocks, Hkv], nullptr: the cache holds the rows' type
   const int32_t *block_table, *ctx_lens;
-  float *part_o, *part_lse;         // [row][split][d], [row][split] (base 2)
+  float *part_o, *part_lse;         // SIMT: [row][split][d], [row][split] (base 2); tensor cores: see the kernel
+  const int64_t* prefix;            // [B+1] pages of the requests before each (WindowSchedule)
+  int32_t* arrived;                 // [B][Hkv][row blocks] CTAs that have left a partial result
   unsigned* err;
   int B, R, Hq, Hkv, group, rows;   // rows = query rows per (request, KV head)
   int max_blocks, num_blocks, window, sinks, n_splits;
+  int row_tiles, row_warps, key_parts, stages;
   float sm_scale;
 };
+
+// What the append launch prepares for the tensor-core kernel in one more CTA:
+// the prefix sums of the requests' pages, and zeros for the arrival counters.
+struct WindowSchedule {
+  int64_t* prefix;                  // nullptr: nothing to prepare
+  int32_t* arrived;
+  int64_t n_arrived;
+  const int32_t* ctx_lens;
+  int B, R, max_blocks, window, sinks;
+};
+
+WindowPlan plan_window_mma(const mtp_window_attn_args& a, bool kv8, int sm_count);
+cudaError_t launch_window_mma(const mtp_window_attn_args& a, bool kv8, const WindowPlan& pl, const WindowParams& p,
+                              cudaStream_t s);
+cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, const WindowSchedule& sch, unsigned* err,
+                              cudaStream_t s);
 
 }  // namespace mtp

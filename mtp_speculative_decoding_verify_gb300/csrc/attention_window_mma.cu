@@ -1,0 +1,687 @@
+// Windowed and 8-bit verify attention of bf16 rows on the tensor cores.
+//
+// out = softmax(scale Q K^T) V over the slots each row sees, one pass over
+// the cache with a running maximum and sum, fp32 accumulation (mma.sync
+// m16n8k16). Pages arrive by TMA in a ring of shared-memory stages that one
+// warp fills; a page of one KV head (64 keys) is a tile.
+//
+// What bounds it is the read of the cache, so the work is cut into equal
+// numbers of pages, whatever the lengths: the pages that the requests' rows
+// see, request after request, form one line per KV head (its prefix sums
+// come with the append launch), and CTA g of G takes pages [g T / G,
+// (g+1) T / G) of it. A CTA crosses from one request to the next without
+// draining its ring. A request that several CTAs share is joined by the last
+// of them to finish, in the order of the pages, so the result does not depend
+// on who that is. G x KV heads CTAs fill the device once; the KV heads of the
+// same pages run side by side, which keeps their interleaved rows together
+// in DRAM.
+//
+// A warp takes 16 query rows (row warp) and every key_parts-th tile; the
+// parts join in shared memory at the end of a request. Registers hold Q, the
+// scores and the output.
+//
+// The 8-bit cache: e4m3 bytes become f16 in registers, which is exact, and
+// meet Q in f16. A row of Q is scaled by a power of two so that its largest
+// value is near 2^14; bf16's 8 bits then fit f16 exactly except for values
+// 2^-28 below the row's largest. For Q K^T a lane's four consecutive bytes
+// serve as k = 2t, 2t+1, 2t+8, 2t+9 of the product, with Q's fragments loaded
+// in the same order; for P V a transposing load yields pairs of dims, whose
+// even and odd dims become two column tiles. Probabilities are rounded to f16
+// times 2^15 (of f16's range all but the top bit), sums are not rounded. A
+// tile's P V is summed apart and joins the output times the block's scale.
+//
+// Slots that not every row sees occur in the last pages, at the window's edge
+// and behind the sinks. Only those tiles take the masked path: hidden scores
+// become -inf, and values that are not finite are taken out of the product
+// (0 x NaN) and put back into the rows that do see them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "attention_window.h"
+#include "kv8.cuh"
+#include "mma_sync.cuh"
+#include "sm100.cuh"
+
+namespace mtp {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxWarps = 9;              // producer + consumers: up to 224 registers a thread
+constexpr int kMaxStages = 16;
+constexpr int kMaxSmem = 232448;          // 227 KB
+constexpr int kPShift = 15;               // f16 probabilities are kept times 2^15
+
+template <int D, bool KV8>
+struct Tile {
+  static constexpr int kRowBytes = D * (KV8 ? 1 : 2);
+  static constexpr int kBoxes = kRowBytes > 128 ? kRowBytes / 128 : 1;
+  static constexpr int kBytes = kBlock * kRowBytes;      // K or V of a page's head
+  static constexpr int kStage = 2 * kBytes;
+  // byte offset of the 16-byte chunk c of a key's row
+  __device__ __forceinline__ static uint32_t at(int key, int c) {
+    if constexpr (kRowBytes == 64) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);                 // 64-byte swizzle
+    return (c >> 3) * (kBlock * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);                     // 128-byte
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// two e4m3 bytes (the low or high half of w) to f16x2
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return cvt_lo(w >> 16); }
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Take what is not finite out of a pair; true if there was any.
+template <bool KV8>
+__device__ __forceinline__ bool take_out(uint32_t& w) {
+  uint32_t keep;
+  if constexpr (KV8) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&w), z = __hsub2(h, h);
+    keep = __heq2_mask(z, z);
+  } else {
+    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w), z = __hsub2(h, h);
+    keep = __heq2_mask(z, z);
+  }
+  w &= keep;
+  return keep != 0xffffffffu;
+}
+
+// The request that page `pos` of the line belongs to: prefix[b] <= pos < prefix[b+1].
+__device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_t pos, int lane) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + kWarp - 1) / kWarp;
+    const int b = lo + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, lane == 0 || (b < hi && __ldg(prefix + b) <= pos));
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
+    window_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const WindowParams p) {
+  using T = Tile<D, KV8>;
+  constexpr int kVals = D / 2 + 4;        // fp32 values of a lane's partial result: output, two maxima, two sums
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* xchg = reinterpret_cast<float*>(smem + p.stages * T::kStage);     // [row warp][key_parts / 2][kVals][32]
+  uint64_t* full = reinterpret_cast<uint64_t*>(xchg + p.row_warps * (p.key_parts / 2) * kVals * kWarp);
+  uint64_t* empty = full + kMaxStages;
+  float2* stage_scale = reinterpret_cast<float2*>(empty + kMaxStages);     // K and V scale of its block
+  int* stage_valid = reinterpret_cast<int*>(stage_scale + kMaxStages);     // 0: the table named no block
+  int* last_flag = stage_valid + kMaxStages;                               // [row warp]
+  volatile int* abort = last_flag + kMaxWarps;
+
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int heads = p.Hkv * p.row_tiles;
+  const int kvh = blockIdx.x % heads / p.row_tiles, row_tile = blockIdx.x % heads % p.row_tiles;
+  const int64_t total = __ldg(p.prefix + p.B);
+  const int G = (int)min((int64_t)(gridDim.x / heads), total);             // every CTA g < G has a page
+  const int g_cta = blockIdx.x / heads;
+  if (g_cta >= G) return;
+  const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      sm100::mbar_init(&full[s], 1);
+      sm100::mbar_init(&empty[s], p.row_warps);   // a tile is read by one part: a warp of every row warp
+    }
+    *abort = 0;
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+
+  int b = find_request(p.prefix, p.B, t_begin, lane);
+  int stage = 0;             // of tile n (counted over the CTA's life): n % stages
+  uint32_t phase = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    // The warp reads the block ids and scales of 32 pages at a time, one a
+    // lane, so that their latency is paid once for 32 tiles.
+    const uint64_t pol = sm100::l2_policy_evict_first();
+    int last_parity[kMaxStages];
+#pragma unroll
+    for (int s = 0; s < kMaxStages; ++s) last_parity[s] = -1;
+    if (lane == 0) {
+      sm100::tma_prefetch_desc(&tm_k);
+      sm100::tma_prefetch_desc(&tm_v);
+    }
+    bool ok = true;
+    for (int64_t pos = t_begin; pos < t_end && ok;) {
+      while (__ldg(p.prefix + b + 1) <= pos) ++b;
+      const int64_t p0 = __ldg(p.prefix + b), p1 = __ldg(p.prefix + b + 1);
+      const int i1 = (int)(min(t_end, p1) - p0);
+      const PageSpan span = page_span(p.ctx_lens[b], p.R, p.window, p.sinks);
+      for (int i = (int)(pos - p0); i < i1 && ok; i += kWarp) {
+        int blk = -1;
+        float2 sc = make_float2(1.0f, 1.0f);
+        if (i + lane < i1) {
+          blk = p.block_table[(int64_t)b * p.max_blocks + span.page(i + lane)];
+          if (blk < 0 || blk >= p.num_blocks) {
+            raise_error(p.err, MTP_ERR_BLOCK_ID);
+            blk = -1;
+          } else if (KV8) {
+            sc = make_float2(p.k_scale[(int64_t)blk * p.Hkv + kvh], p.v_scale[(int64_t)blk * p.Hkv + kvh]);
+          }
+        }
+        const int n = min(kWarp, i1 - i);
+        for (int x = 0; x < n; ++x) {
+          const int id = __shfl_sync(0xffffffffu, blk, x);
+          const float sk = __shfl_sync(0xffffffffu, sc.x, x), sv = __shfl_sync(0xffffffffu, sc.y, x);
+          int go = 1;
+          if (lane == 0) {
+            go = sm100::mbar_wait(&empty[stage], phase ^ 1u, abort);
+            if (go) {
+              stage_scale[stage] = make_float2(sk, sv);
+              stage_valid[stage] = id >= 0;
+              if (id >= 0) {
+                uint8_t* ks = smem + stage * T::kStage;
+                sm100::mbar_arrive_expect_tx(&full[stage], T::kStage);
+#pragma unroll
+                for (int c = 0; c < T::kBoxes; ++c) {
+                  sm100::tma_load_4d(ks + c * kBlock * 128, &tm_k, &full[stage], c * (KV8 ? D : 64), kvh, 0, id, pol);
+                  sm100::tma_load_4d(ks + T::kBytes + c * kBlock * 128, &tm_v, &full[stage], c * (KV8 ? D : 64), kvh, 0,
+                                     id, pol);
+                }
+                last_parity[stage] = (int)phase;
+              } else {
+                sm100::mbar_arrive(&full[stage]);
+              }
+            } else {
+              *abort = 1;
+              raise_error(p.err, MTP_ERR_TIMEOUT);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+          if (!ok) break;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      pos = p0 + i1;
+    }
+    // Every copy issued lands before the CTA may exit.
+    if (lane == 0) {
+      for (int s = 0; s < p.stages; ++s)
+        if (last_parity[s] >= 0) sm100::mbar_wait_timeout(&full[s], (uint32_t)last_parity[s], sm100::kWaitTimeoutNs);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------- consumers
+  const int cw = warp - 1, rw = cw % p.row_warps, kp = cw / p.row_warps;
+  const int g = lane >> 2, t = lane & 3, mi = lane >> 3;
+  const int r_lo = (row_tile * p.row_warps + rw) * 16 + g, r_hi = r_lo + 8;
+  const int c_lo = min(r_lo, p.rows - 1), c_hi = min(r_hi, p.rows - 1);     // padding rows repeat the last row
+  const int j_lo = c_lo / p.group, j_hi = c_hi / p.group;
+  const int64_t q_lo = (int64_t)j_lo * p.Hq + kvh * p.group + c_lo % p.group;   // + b R Hq: the row of q and out
+  const int64_t q_hi = (int64_t)j_hi * p.Hq + kvh * p.group + c_hi % p.group;
+  const int row_block = row_tile * p.row_warps + rw, row_blocks = p.row_tiles * p.row_warps;
+  const int part_threads = p.key_parts * kWarp;
+  float* my_xchg = xchg + (size_t)rw * (p.key_parts / 2) * kVals * kWarp + lane;
+
+  uint32_t qa[D / 16][4];
+  float o[D / 8][4];
+  float m_lo, m_hi, l_lo, l_hi;           // running maxima (log2 units, scaled) and this lane's part of the sums
+  float f_lo = p.sm_scale * kLog2e, f_hi = f_lo;   // 8-bit: times the power of two taken out of the row of Q
+  int tile = 0;                           // n % key_parts == kp: this part's tiles
+
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    m_lo = m_hi = -INFINITY;
+    l_lo = l_hi = 0.0f;
+  };
+  // Join another partial result (same fragment layout), read through `val`.
+  auto fold = [&](auto&& val) {
+    const float ml = val(D / 2), mh = val(D / 2 + 1);
+    const float nl = fmaxf(m_lo, ml), nh = fmaxf(m_hi, mh);
+    const float al = m_lo == -INFINITY ? 0.0f : ex2(m_lo - nl), bl = ml == -INFINITY ? 0.0f : ex2(ml - nl);
+    const float ah = m_hi == -INFINITY ? 0.0f : ex2(m_hi - nh), bh = mh == -INFINITY ? 0.0f : ex2(mh - nh);
+    l_lo = l_lo * al + val(D / 2 + 2) * bl;
+    l_hi = l_hi * ah + val(D / 2 + 3) * bh;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      o[i][0] = o[i][0] * al + val(4 * i) * bl;
+      o[i][1] = o[i][1] * al + val(4 * i + 1) * bl;
+      o[i][2] = o[i][2] * ah + val(4 * i + 2) * bh;
+      o[i][3] = o[i][3] * ah + val(4 * i + 3) * bh;
+    }
+    m_lo = nl;
+    m_hi = nh;
+  };
+  auto spill = [&](float* to) {
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) to[i * kWarp] = o[i >> 2][i & 3];
+    to[(D / 2) * kWarp] = m_lo;
+    to[(D / 2 + 1) * kWarp] = m_hi;
+    to[(D / 2 + 2) * kWarp] = l_lo;
+    to[(D / 2 + 3) * kWarp] = l_hi;
+  };
+  auto part_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + rw), "r"(part_threads) : "memory"); };
+  // Join the parts of this row warp into part 0, halving their number each time.
+  auto join_parts = [&]() {
+    for (int n = p.key_parts; n > 1;) {
+      const int half = (n + 1) / 2;
+      if (kp >= half && kp < n) spill(my_xchg + (size_t)(kp - half) * kVals * kWarp);
+      part_sync();
+      if (kp < n - half) {
+        const float* from = my_xchg + (size_t)kp * kVals * kWarp;
+        fold([&](int i) { return from[i * kWarp]; });
+      }
+      part_sync();
+      n = half;
+    }
+  };
+
+  auto consume = [&](int page, int ctx, auto masked_c) {
+    constexpr bool kMasked = decltype(masked_c)::value;
+    const uint32_t kbase = sm100::smem_u32(smem + stage * T::kStage), vbase = kbase + T::kBytes;
+    const float2 sc = stage_scale[stage];
+    float s[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    if constexpr (KV8) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t w[4];
+          mma::ldsm_x4(kbase + T::at(n * 8 + (lane & 7), c * 4 + mi), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma_f16_16816(s[n], qa[c * 4 + x], cvt_lo(w[x]), cvt_hi(w[x]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t b0, b1, b2, b3;
+          mma::ldsm_x4(kbase + T::at(np * 16 + (mi >> 1) * 8 + (lane & 7), kk * 2 + (mi & 1)), b0, b1, b2, b3);
+          mma::mma_bf16_16816(s[2 * np], qa[kk], b0, b1);
+          mma::mma_bf16_16816(s[2 * np + 1], qa[kk], b2, b3);
+        }
+      }
+    }
+    // (a factor of 0 would turn a hidden -inf into NaN; scores that small are 0 all the same)
+    const float fl = KV8 ? fmaxf(f_lo * sc.x, 1e-36f) : f_lo, fh = KV8 ? fmaxf(f_hi * sc.x, 1e-36f) : f_hi;
+    if constexpr (kMasked) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int slot = page * kBlock + n * 8 + 2 * t + (e & 1);
+          if (!slot_visible(slot, ctx + (e < 2 ? j_lo : j_hi), p.window, p.sinks)) s[n][e] = -INFINITY;
+        }
+      }
+    }
+    float x_lo = -INFINITY, x_hi = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      x_lo = fmaxf(x_lo, fmaxf(s[n][0], s[n][1]));
+      x_hi = fmaxf(x_hi, fmaxf(s[n][2], s[n][3]));
+    }
+    x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 1));
+    x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 2));
+    x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 1));
+    x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 2));
+    const float n_lo = fmaxf(m_lo, x_lo * fl), n_hi = fmaxf(m_hi, x_hi * fh);
+    const float z_lo = n_lo == -INFINITY ? 0.0f : n_lo, z_hi = n_hi == -INFINITY ? 0.0f : n_hi;
+    const float k_lo = ex2(m_lo - z_lo), k_hi = ex2(m_hi - z_hi);
+    m_lo = n_lo;
+    m_hi = n_hi;
+    constexpr float kUp = KV8 ? (float)kPShift : 0.0f;
+    float t_lo = 0.0f, t_hi = 0.0f;
+    uint32_t pa[4][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float p0 = ex2(fmaf(s[n][0], fl, kUp - z_lo)), p1 = ex2(fmaf(s[n][1], fl, kUp - z_lo));
+      const float p2 = ex2(fmaf(s[n][2], fh, kUp - z_hi)), p3 = ex2(fmaf(s[n][3], fh, kUp - z_hi));
+      t_lo += p0 + p1;
+      t_hi += p2 + p3;
+      pa[n >> 1][(n & 1) * 2] = KV8 ? pack_f16(p0, p1) : mma::pack_bf16(p0, p1);
+      pa[n >> 1][(n & 1) * 2 + 1] = KV8 ? pack_f16(p2, p3) : mma::pack_bf16(p2, p3);
+    }
+    l_lo = l_lo * k_lo + t_lo;
+    l_hi = l_hi * k_hi + t_hi;
+    bool out_of = false;
+    if constexpr (KV8) {
+      const float v = sc.y;
+#pragma unroll
+      for (int c2 = 0; c2 < D / 32; ++c2) {       // two 16-dim chunks at a time
+        float y[4][4];                             // chunk 0 even dims, odd dims, chunk 1 even, odd
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];                           // chunk 0 keys 0-7, 8-15, chunk 1 keys 0-7, 8-15
+          mma::ldsm_x4_trans(vbase + T::at(k * 16 + (mi & 1) * 8 + (lane & 7), c2 * 2 + (mi >> 1)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] = __byte_perm(w[x], 0, 0x3120);   // pairs of keys: even dim, odd dim
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t e0 = cvt_lo(w[2 * x]), e1 = cvt_lo(w[2 * x + 1]), d0 = cvt_hi(w[2 * x]), d1 = cvt_hi(w[2 * x + 1]);
+            if constexpr (kMasked) {
+              out_of |= take_out<true>(e0);
+              out_of |= take_out<true>(e1);
+              out_of |= take_out<true>(d0);
+              out_of |= take_out<true>(d1);
+            }
+            mma_f16_16816(y[2 * x], pa[k], e0, e1);
+            mma_f16_16816(y[2 * x + 1], pa[k], d0, d1);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float(&a)[4] = o[c2 * 4 + i];
+          a[0] = fmaf(a[0], k_lo, y[i][0] * v);
+          a[1] = fmaf(a[1], k_lo, y[i][1] * v);
+          a[2] = fmaf(a[2], k_hi, y[i][2] * v);
+          a[3] = fmaf(a[3], k_hi, y[i][3] * v);
+        }
+      }
+    } else {
+      if (__any_sync(0xffffffffu, k_lo != 1.0f || k_hi != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= k_lo;
+          o[i][1] *= k_lo;
+          o[i][2] *= k_hi;
+          o[i][3] *= k_hi;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+          uint32_t b0, b1, b2, b3;
+          mma::ldsm_x4_trans(vbase + T::at(k * 16 + (mi & 1) * 8 + (lane & 7), dp * 2 + (mi >> 1)), b0, b1, b2, b3);
+          if constexpr (kMasked) {
+            out_of |= take_out<false>(b0);
+            out_of |= take_out<false>(b1);
+            out_of |= take_out<false>(b2);
+            out_of |= take_out<false>(b3);
+          }
+          mma::mma_bf16_16816(o[2 * dp], pa[k], b0, b1);
+          mma::mma_bf16_16816(o[2 * dp + 1], pa[k], b2, b3);
+        }
+      }
+    }
+    if constexpr (kMasked) {
+      if (__any_sync(0xffffffffu, out_of)) {       // rare: a NaN or infinity in V
+        const uint8_t* vt = smem + stage * T::kStage + T::kBytes;
+        for (int key = 0; key < kBlock; ++key) {
+          const bool see_lo = slot_visible(page * kBlock + key, ctx + j_lo, p.window, p.sinks);
+          const bool see_hi = slot_visible(page * kBlock + key, ctx + j_hi, p.window, p.sinks);
+          if (!see_lo && !see_hi) continue;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // the dim of o[i][e] and o[i][e + 2]
+              const int dim = KV8 ? (i >> 1) * 16 + 4 * t + 2 * e + (i & 1) : i * 8 + 2 * t + e;
+              float v;
+              if constexpr (KV8) v = (vt[T::at(key, dim / 16) + dim % 16] & 127) == 127 ? NAN : 0.0f;
+              else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt + T::at(key, dim / 8) + dim % 8 * 2));
+              if (!(fabsf(v) <= FLT_MAX)) {
+                if (see_lo) o[i][e] += v;
+                if (see_hi) o[i][e + 2] += v;
+              }
+            }
+          }
+        }
+      }
+    }
+  };
+
+  for (int64_t pos = t_begin; pos < t_end;) {
+    while (__ldg(p.prefix + b + 1) <= pos) ++b;
+    const int64_t p0 = __ldg(p.prefix + b), p1 = __ldg(p.prefix + b + 1);
+    const int i0 = (int)(pos - p0), i1 = (int)(min(t_end, p1) - p0), n_tiles = (int)(p1 - p0);
+    const int ctx = p.ctx_lens[b];
+    const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
+    const int64_t row0 = (int64_t)b * p.R * p.Hq;
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q);
+    if constexpr (KV8) {
+      uint2 w[2][D / 16];
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        w[0][kk] = __ldg(reinterpret_cast<const uint2*>(qp + (row0 + q_lo) * D + kk * 16 + 4 * t));
+        w[1][kk] = __ldg(reinterpret_cast<const uint2*>(qp + (row0 + q_hi) * D + kk * 16 + 4 * t));
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t v = e == 0 ? w[x][kk].x : w[x][kk].y;
+            const float a = fabsf(__uint_as_float(v << 16)), c = fabsf(__uint_as_float(v & 0xffff0000u));
+            top = fmaxf(top, fmaxf(a <= FLT_MAX ? a : 0.0f, c <= FLT_MAX ? c : 0.0f));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e with the row's largest value in [2^14, 2^15) after division; e >= -100 keeps the factors in range
+        const int e = top > 0.0f ? max(-100, (int)(__float_as_uint(top) >> 23) - 127 - 14) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        (x == 0 ? f_lo : f_hi) = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint2 v = w[x][kk];
+          qa[kk][x] = pack_f16(__uint_as_float(v.x << 16) * down, __uint_as_float(v.x & 0xffff0000u) * down);
+          qa[kk][x + 2] = pack_f16(__uint_as_float(v.y << 16) * down, __uint_as_float(v.y & 0xffff0000u) * down);
+        }
+      }
+    } else {
+      const uint32_t* lo = reinterpret_cast<const uint32_t*>(qp + (row0 + q_lo) * D);
+      const uint32_t* hi = reinterpret_cast<const uint32_t*>(qp + (row0 + q_hi) * D);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qa[kk][0] = __ldg(lo + kk * 8 + t);
+        qa[kk][1] = __ldg(hi + kk * 8 + t);
+        qa[kk][2] = __ldg(lo + kk * 8 + 4 + t);
+        qa[kk][3] = __ldg(hi + kk * 8 + 4 + t);
+      }
+    }
+    clear();
+
+    for (int i = i0; i < i1; ++i) {
+      if (tile == kp) {
+        if (!__all_sync(0xffffffffu, sm100::mbar_wait(&full[stage], phase, abort) ? 1 : 0)) {
+          // the tiles that are left give up at once; the joins below still meet
+          if (lane == 0) {
+            *abort = 1;
+            raise_error(p.err, MTP_ERR_TIMEOUT);
+          }
+        } else {
+          if (stage_valid[stage]) {
+            const int page = span.page(i), first = page * kBlock, last = first + kBlock - 1;
+            const bool whole = last <= ctx && (p.window == 0 || first > ctx + p.R - 1 - p.window || last < p.sinks);
+            if (whole) consume(page, ctx, std::false_type());
+            else consume(page, ctx, std::true_type());
+          }
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&empty[stage]);
+        }
+      }
+      if (++tile == p.key_parts) tile = 0;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    pos = p0 + i1;
+
+    join_parts();
+    if (i0 > 0 || i1 < n_tiles) {
+      // Shared with other CTAs: leave the partial result, and the last to
+      // arrive at this (request, KV head, row block) joins them all. Slot 0
+      // of a CTA is for a request it did not begin, slot 1 for one it began.
+      const int g0 = (int)(((p0 + 1) * G - 1) / total), g1 = (int)((p1 * G - 1) / total);   // CTAs of pages p0, p1 - 1
+      const size_t stride = (size_t)kVals * kWarp;
+      auto slot_of = [&](int gg, int which) {
+        return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * row_blocks + row_block) * stride + lane;
+      };
+      if (kp == 0) {
+        spill(slot_of(g_cta, i0 > 0 ? 0 : 1));
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          const int before = atomicAdd(p.arrived + ((int64_t)b * p.Hkv + kvh) * row_blocks + row_block, 1);
+          last_flag[rw] = before == g1 - g0;
+        }
+        __threadfence();
+      }
+      part_sync();
+      const bool last = *const_cast<volatile int*>(last_flag + rw) != 0;
+      if (!last) {
+        part_sync();       // the flag has been read
+        continue;
+      }
+      __threadfence();
+      clear();
+      for (int gg = g0 + kp; gg <= g1; gg += p.key_parts) {
+        const float* from = slot_of(gg, gg == g0 ? 1 : 0);
+        fold([&](int i) { return __ldcg(from + i * kWarp); });
+      }
+      part_sync();
+      join_parts();
+    }
+    if (kp == 0) {
+      l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
+      l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
+      l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
+      l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
+      const float v_lo = l_lo == 0.0f ? 0.0f : 1.0f / l_lo, v_hi = l_hi == 0.0f ? 0.0f : 1.0f / l_hi;
+      __nv_bfloat16* out_lo = static_cast<__nv_bfloat16*>(p.out) + (row0 + q_lo) * D;
+      __nv_bfloat16* out_hi = static_cast<__nv_bfloat16*>(p.out) + (row0 + q_hi) * D;
+      if constexpr (KV8) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {       // four consecutive dims: even and odd tile interleaved
+          float(&e)[4] = o[2 * c];
+          float(&d)[4] = o[2 * c + 1];
+          if (r_lo < p.rows)
+            *reinterpret_cast<uint2*>(out_lo + c * 16 + 4 * t) =
+                make_uint2(mma::pack_bf16(e[0] * v_lo, d[0] * v_lo), mma::pack_bf16(e[1] * v_lo, d[1] * v_lo));
+          if (r_hi < p.rows)
+            *reinterpret_cast<uint2*>(out_hi + c * 16 + 4 * t) =
+                make_uint2(mma::pack_bf16(e[2] * v_hi, d[2] * v_hi), mma::pack_bf16(e[3] * v_hi, d[3] * v_hi));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          if (r_lo < p.rows)
+            *reinterpret_cast<uint32_t*>(out_lo + i * 8 + 2 * t) = mma::pack_bf16(o[i][0] * v_lo, o[i][1] * v_lo);
+          if (r_hi < p.rows)
+            *reinterpret_cast<uint32_t*>(out_hi + i * 8 + 2 * t) = mma::pack_bf16(o[i][2] * v_hi, o[i][3] * v_hi);
+        }
+      }
+    }
+  }
+}
+
+// The layout of a launch: row warps and key parts of a CTA, stages, CTAs.
+// A page of 64 keys keeps a warp busy for about as long as several pages take
+// to arrive, so a CTA (one per SM: 227 KB of stages) needs around 8 warps;
+// with few rows they come from key parts.
+template <int D, bool KV8>
+void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
+  using T = Tile<D, KV8>;
+  const int blocks = (a.Hq / a.Hkv * (a.D + 1) + 15) / 16;     // of 16 rows
+  pl->row_tiles = (blocks + 7) / 8;
+  pl->row_warps = (blocks + pl->row_tiles - 1) / pl->row_tiles;
+  // Tile n sits in stage n % stages and goes to part n % key_parts. stages is
+  // a multiple of key_parts, so that each stage serves one part, which meets
+  // its phases one after the other, and two stages a part at least, so that
+  // one fills while the other is read.
+  for (pl->key_parts = 8 / pl->row_warps;; --pl->key_parts) {
+    const int fixed = pl->row_warps * (pl->key_parts / 2) * (D / 2 + 4) * kWarp * 4 + kMaxStages * 28 + (kMaxWarps + 1) * 4 + 1024;
+    pl->stages = std::min(kMaxStages, (kMaxSmem - fixed) / T::kStage) / pl->key_parts * pl->key_parts;
+    pl->smem = pl->stages * T::kStage + fixed;
+    if (pl->key_parts == 1 || pl->stages >= 2 * pl->key_parts) break;
+  }
+  const long long heads = (long long)a.Hkv * pl->row_tiles;
+  pl->ctas_per_head = (int)std::max<long long>(1, sm_count / heads);
+}
+
+template <int D, bool KV8>
+cudaError_t launch(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
+  auto encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t elem = KV8 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)kBlock, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[3] = {D * elem, a.Hkv * D * elem, (cuuint64_t)kBlock * a.Hkv * D * elem};
+  const cuuint32_t box[4] = {KV8 ? (cuuint32_t)D : 64u, 1, (cuuint32_t)kBlock, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i) {
+    if (encode(&maps[i], KV8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               i == 0 ? a.k_cache : a.v_cache, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               Tile<D, KV8>::kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)(pl.ctas_per_head * a.Hkv * pl.row_tiles);
+  window_mma_kernel<D, KV8><<<grid, (pl.row_warps * pl.key_parts + 1) * kWarp, pl.smem, s>>>(maps[0], maps[1], p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+WindowPlan plan_window_mma(const mtp_window_attn_args& a, bool kv8, int sm_count) {
+  WindowPlan pl{};
+  if (kv8) a.d == 128 ? layout<128, true>(a, sm_count, &pl) : layout<64, true>(a, sm_count, &pl);
+  else a.d == 128 ? layout<128, false>(a, sm_count, &pl) : layout<64, false>(a, sm_count, &pl);
+  const size_t rows = (size_t)a.Hkv * pl.row_tiles * pl.row_warps;     // row blocks of a request
+  pl.ws_prefix = 0;
+  pl.ws_arrived = ((size_t)(a.B + 1) * sizeof(int64_t) + 255) / 256 * 256;
+  pl.ws_partial_o = pl.ws_arrived + ((size_t)a.B * rows * sizeof(int32_t) + 255) / 256 * 256;
+  pl.ws_bytes = pl.ws_partial_o + (size_t)pl.ctas_per_head * 2 * rows * (a.d / 2 + 4) * kWarp * sizeof(float);
+  pl.ws_bytes = (pl.ws_bytes + 255) / 256 * 256;
+  return pl;
+}
+
+cudaError_t launch_window_mma(const mtp_window_attn_args& a, bool kv8, const WindowPlan& pl, const WindowParams& p,
+                              cudaStream_t s) {
+  if (kv8) return a.d == 128 ? launch<128, true>(a, pl, p, s) : launch<64, true>(a, pl, p, s);
+  return a.d == 128 ? launch<128, false>(a, pl, p, s) : launch<64, false>(a, pl, p, s);
+}
+
+}  // namespace mtp

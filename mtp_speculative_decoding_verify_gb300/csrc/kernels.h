@@ -64,8 +64,4 @@ cudaError_t launch_relaxed_prepass(const mtp_lmhead_args& a, const LmPlan& p, cu
 // ----------------------------------------------------------------- rollback
 cudaError_t launch_rollback(const mtp_rollback_args& a, unsigned* err, cudaStream_t s);
 
-// --------------------------------------------------------------- 8-bit cache
-// uniform > 0: every request appends that many tokens (at most 16; a.starts is not read)
-cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, unsigned* err, cudaStream_t s);
-
 }  // namespace mtp

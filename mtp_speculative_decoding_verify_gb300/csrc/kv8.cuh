@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 #include <float.h>
 
+#include "attention_window.h"
 #include "common.cuh"
 
 namespace mtp {
@@ -77,6 +78,38 @@ __host__ __device__ __forceinline__ PageSpan page_span(int ctx, int R, int windo
   s.n_sink = window == 0 ? 0 : (sink_pages < s.w0 ? sink_pages : s.w0);
   s.n = s.n_sink + pages - s.w0;
   return s;
+}
+
+// The work of one CTA of THREADS threads (a multiple of 32): see WindowSchedule.
+template <int THREADS>
+__device__ void window_schedule(const WindowSchedule& w) {
+  __shared__ int64_t s_warp[THREADS / kWarp];
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < w.B; b0 += THREADS) {
+    const int b = b0 + threadIdx.x;
+    int64_t n = 0;
+    if (b < w.B) {
+      const int ctx = w.ctx_lens[b];      // a bad length has no pages: its rows stay as they were
+      if (ctx >= 0 && ctx <= w.max_blocks * kBlock - w.R) n = page_span(ctx, w.R, w.window, w.sinks).n;
+    }
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += y;
+    }
+    __syncthreads();                       // the last chunk's totals have been read
+    if (lane == kWarp - 1) s_warp[warp] = n;
+    __syncthreads();
+    n += base;
+    for (int i = 0; i < THREADS / kWarp; ++i) {
+      if (i < warp) n += s_warp[i];
+      base += s_warp[i];
+    }
+    if (b < w.B) w.prefix[b + 1] = n;
+  }
+  if (threadIdx.x == 0) w.prefix[0] = 0;
+  for (int64_t i = threadIdx.x; i < w.n_arrived; i += THREADS) w.arrived[i] = 0;
 }
 
 }  // namespace mtp

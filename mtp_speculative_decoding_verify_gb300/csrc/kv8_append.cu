@@ -56,6 +56,7 @@ struct AppendParams {
   int T, B, Hkv, uniform, max_blocks, num_blocks;
   long long units;             // teams of the grid that have work to look for
   unsigned* err;
+  WindowSchedule schedule;     // for the last CTA, when asked for
 };
 
 // The request that slot `piece` of the piece numbering belongs to. A request
@@ -94,6 +95,10 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   __shared__ float s_max[kThreads / kWarp];
   const int tid = threadIdx.x % TEAM;
 
+  if (p.schedule.prefix != nullptr && blockIdx.x == gridDim.x - 1) {
+    window_schedule<kThreads>(p.schedule);
+    return;
+  }
   if (p.starts != nullptr && blockIdx.x == 0) {
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
       const int s0 = p.starts[b], s1 = p.starts[b + 1];
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
 template <typename T, int D>
 cudaError_t run_append(const AppendParams& p, cudaStream_t s) {
   if (p.starts == nullptr) {
-    const long long grid = (p.units + kThreads / kWarp - 1) / (kThreads / kWarp);
+    const long long grid = (p.units + kThreads / kWarp - 1) / (kThreads / kWarp) + (p.schedule.prefix ? 1 : 0);
     kv8_append_kernel<T, D, kWarp><<<(unsigned)grid, kThreads, 0, s>>>(p);
   } else {
     kv8_append_kernel<T, D, kThreads><<<(unsigned)p.units, kThreads, 0, s>>>(p);
@@ -233,7 +238,8 @@ int check_append(const mtp_kv8_append_args* a) {
 
 }  // namespace
 
-cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, unsigned* err, cudaStream_t s) {
+cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, const WindowSchedule& sch, unsigned* err,
+                              cudaStream_t s) {
   AppendParams p;
   p.k_new = a.k_new;
   p.v_new = a.v_new;
@@ -251,6 +257,7 @@ cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, unsigne
   p.max_blocks = a.max_blocks;
   p.num_blocks = a.num_blocks;
   p.err = err;
+  p.schedule = sch;
   const long long pieces = uniform > 0 ? 2ll * a.B : (long long)a.T / kBlock + 2ll * a.B;
   p.units = pieces * a.Hkv * 2;
   if (a.dtype == MTP_BF16)
@@ -268,7 +275,7 @@ extern "C" int mtp_kv8_append(const mtp_kv8_append_args* a, void* stream) {
   unsigned* err = nullptr;
   int sm_count = 0;
   if ((rc = mtp::device_context(&err, &sm_count)) != MTP_OK) return rc;
-  const cudaError_t e = mtp::launch_kv8_append(*a, 0, err, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = mtp::launch_kv8_append(*a, 0, mtp::WindowSchedule{}, err, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return mtp::set_cuda_error(e, "8-bit append launch");
   mtp::set_launch_count(1);
   return MTP_OK;
