@@ -53,7 +53,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxWarps = 9;              // producer + consumers: up to 224 registers a thread
+constexpr int kMaxWarps = 8;              // producer + consumers, two per SM sub-partition: up to 255 registers a thread
 constexpr int kMaxStages = 16;
 constexpr int kMaxSmem = 232448;          // 227 KB
 constexpr int kPShift = 15;               // f16 probabilities are kept times 2^15
@@ -82,12 +82,17 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// two e4m3 bytes (the low or high half of w) to f16x2
-__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 bytes to two f16x2: bytes 0, 1 and bytes 2, 3.
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n"
+      "  .reg .b16 a, b;\n"
+      "  mov.b32 {a, b}, %2;\n"
+      "  cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      "  cvt.rn.f16x2.e4m3x2 %1, b;\n"
+      "}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return cvt_lo(w >> 16); }
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -321,7 +326,11 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
           uint32_t w[4];
           mma::ldsm_x4(kbase + T::at(n * 8 + (lane & 7), c * 4 + mi), w[0], w[1], w[2], w[3]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma_f16_16816(s[n], qa[c * 4 + x], cvt_lo(w[x]), cvt_hi(w[x]));
+          for (int x = 0; x < 4; ++x) {
+            uint32_t b0, b1;
+            cvt_e4m3x4(w[x], b0, b1);
+            mma_f16_16816(s[n], qa[c * 4 + x], b0, b1);
+          }
         }
       }
     } else {
@@ -393,7 +402,9 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
           for (int x = 0; x < 4; ++x) w[x] = __byte_perm(w[x], 0, 0x3120);   // pairs of keys: even dim, odd dim
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            uint32_t e0 = cvt_lo(w[2 * x]), e1 = cvt_lo(w[2 * x + 1]), d0 = cvt_hi(w[2 * x]), d1 = cvt_hi(w[2 * x + 1]);
+            uint32_t e0, e1, d0, d1;
+            cvt_e4m3x4(w[2 * x], e0, d0);
+            cvt_e4m3x4(w[2 * x + 1], e1, d1);
             if constexpr (kMasked) {
               out_of |= take_out<true>(e0);
               out_of |= take_out<true>(e1);
@@ -623,13 +634,13 @@ template <int D, bool KV8>
 void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
   using T = Tile<D, KV8>;
   const int blocks = (a.Hq / a.Hkv * (a.D + 1) + 15) / 16;     // of 16 rows
-  pl->row_tiles = (blocks + 7) / 8;
+  pl->row_tiles = (blocks + kMaxWarps - 2) / (kMaxWarps - 1);
   pl->row_warps = (blocks + pl->row_tiles - 1) / pl->row_tiles;
   // Tile n sits in stage n % stages and goes to part n % key_parts. stages is
   // a multiple of key_parts, so that each stage serves one part, which meets
   // its phases one after the other, and two stages a part at least, so that
   // one fills while the other is read.
-  for (pl->key_parts = 8 / pl->row_warps;; --pl->key_parts) {
+  for (pl->key_parts = (kMaxWarps - 1) / pl->row_warps;; --pl->key_parts) {
     const int fixed = pl->row_warps * (pl->key_parts / 2) * (D / 2 + 4) * kWarp * 4 + kMaxStages * 28 + (kMaxWarps + 1) * 4 + 1024;
     pl->stages = std::min(kMaxStages, (kMaxSmem - fixed) / T::kStage) / pl->key_parts * pl->key_parts;
     pl->smem = pl->stages * T::kStage + fixed;
