@@ -1,0 +1,1012 @@
+// Verify attention of bf16 rows over the 8-bit cache on the 5th-generation
+// tensor cores.
+//
+// out = softmax(scale Q K^T) V over the slots each row sees; work is shared
+// out and joined as in attention_window_mma.cu: every CTA takes an equal
+// number of pages of one KV head's line, crossing from request to request.
+//
+// Both products run on the bytes as TMA brought them (kind::f8f6f4, fp32
+// sums). The other operand is split into e4m3 terms, 4 bits each:
+//   S = Q K^T   a row of Q is scaled by a power of two (largest value in
+//               [2^7, 2^8)) and q = hi + lo holds bf16's 8 bits. What lo
+//               cannot hold (below 2^-18 of the row's largest value) goes
+//               into a third e5m2 term, used only for requests with a row
+//               where these rests pass 2^-19 of the row's sum.
+//   O += P V    p = hi + lo / 16: 8 bits, as bf16 would keep.
+// No operand is converted in shared memory, whose bandwidth is what two
+// products with f16 values of V would run out of (measured: 112 us where this
+// takes half).
+//
+// M = 128 TMEM lanes. Lanes 32 w .. 32 w + 15, of warp w, hold a block of 16
+// query rows as hi, lanes 32 w + 16 .. the same rows as lo: one MMA gives
+// both terms, added after they are read. With fewer than 64 rows several
+// warps hold the same block (row block w % NRB, key group w / NRB) and each
+// takes its own keys of the tile (two pages, 128 keys): P is zero outside a
+// warp's own keys (those columns are written once, at the start), so every
+// row of every warp is an online softmax of its own, and warps exchange
+// nothing until the request ends. The 16x32bx2 form of the TMEM loads and
+// stores gives the threads t and t + 16 of a warp two column ranges of one
+// lane: they share a row and halve its keys (16 NRB each) and output dims,
+// with a shuffle for the common maximum.
+//
+// A row's probabilities are 2^(score + log2(v scale) - ref): the block's
+// scale of V rides along, and the sum, which is kept relative to a maximum of
+// scores alone, divides it out again. e4m3 holds 2^-9 (lo: 2^-13) to 2^8, so
+// ref follows the tiles up and down: when a tile's largest probability would
+// pass 2^8, or was below 2^-2 for three tiles, O is rescaled in TMEM to put
+// it at 2. (Down, so that a few large scores do not cost the rest of the
+// context its bits; O in fp32 has room for the 60 octaves that are allowed.)
+//
+// Two groups of four softmax warps take alternate tiles, each with an S
+// buffer and an O of its own, joined with the rest when the request ends.
+// P lies in the columns of the S it came from: P V of tile g and S of tile
+// g + 2 are issued back to back, in the order in which they use the buffer.
+//
+// Hidden slots: only tiles with a slot that not every row sees are masked.
+// There V's bytes that are NaN become 0 in shared memory (0 x NaN), and a
+// bitmap of (verify token, dim) puts NaN back into the rows that do see them.
+//
+// Warps: 0 MMA issue, 1 TMA (block ids and scales of 32 pages at a time, one
+// a lane), 4-11 softmax and output, 12-15 masked V and the next request's Q.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <limits.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "attention_window.h"
+#include "kv8.cuh"
+#include "sm100.cuh"
+
+namespace mtp {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 512;
+constexpr int kKeys = 128;
+constexpr int kInfo = 8;               // tiles whose scales and pages are held: the TMA warp is at most 6 stages and 2 S buffers ahead
+constexpr int kSegs = 4;               // requests whose row factors are held; the Q warps are at most 3 ahead
+constexpr int kNanSegs = 8;            // requests whose NaN bitmaps are held; their writers are at most 6 stages ahead
+// log2 of a tile's largest probability: the bounds that ref keeps, and where a rescale puts it
+constexpr float kMostP = 8.0f, kLeastP = -2.0f, kNominalP = 1.0f;
+constexpr int kLowTiles = 3;
+constexpr float kDown = 60.0f;         // ref is never further below the largest there was
+constexpr float kLoScale = 16.0f;      // P's second term is held times this
+constexpr uint32_t kColO = 256;        // S (and P) buffers at columns 0 and 128, O at 256 and 384
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = kKeys * D;                 // bytes of K or V of a tile
+  static constexpr int kStages = D == 128 ? 5 : 6;
+  static constexpr int kK = 0, kV = kK + kStages * kTile;
+  static constexpr int kQ = kV + kStages * kTile;         // hi and lo, rest
+  static constexpr int kX = kQ + 2 * kTile;               // join of a row's partial results: [8 warps][16][36] floats
+  static constexpr int kRed = kX + 128 * 36 * 4;          // [8 warps][16] (maximum, sum)
+  static constexpr int kInfoOff = kRed + 128 * 8;         // [kInfo] TileInfo
+  static constexpr int kFac = kInfoOff + kInfo * 32;      // [kSegs][64] factors of the rows' scores
+  static constexpr int kNan = kFac + kSegs * 64 * 4;      // [kNanSegs][16][4] words
+  static constexpr int kBar = kNan + kNanSegs * 16 * 4 * 4;
+  static constexpr int kBars = 5 * kStages + 2 + 2 + 2 + 2 + kInfo + kSegs;
+  static constexpr int kMisc = kBar + kBars * 8;          // rest flags [kSegs][2], join flag, abort, TMEM base
+  static constexpr int kBytes = kMisc + kSegs * 8 + 16 + 1024;
+  // byte offset of 16-byte chunk c of row r of a K-major operand tile, as TMA swizzles it
+  __device__ __forceinline__ static uint32_t at(int r, int c) {
+    if constexpr (D == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return r * 128 + ((c ^ (r & 7)) << 4);
+  }
+};
+static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "227 KB of shared memory");
+
+struct TileInfo {            // of its two pages
+  float sk[2];               // scale of K
+  float lsv[2], isv[2];      // log2 and reciprocal of the scale of V
+  int page[2];               // index in the request, -1: nothing loaded; -2 - index: some row does not see all of it
+};
+
+// ------------------------------------------------------------- instructions
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four probabilities (at most 2^8) as e4m3 terms: hi, and lo = 16 (p - hi).
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  asm("{\n"
+      "  .reg .b16 h0, h1, l0, l1;\n"
+      "  .reg .b32 p0, p1, q0, q1, m, s;\n"
+      "  mov.b32 m, 0xcc00cc00;\n"                        // f16 -16, -16
+      "  mov.b32 s, 0x4c004c00;\n"                        // f16 16, 16
+      "  cvt.rn.f16x2.f32 p0, %3, %2;\n"
+      "  cvt.rn.f16x2.f32 p1, %5, %4;\n"
+      "  cvt.rn.satfinite.e4m3x2.f16x2 h0, p0;\n"
+      "  cvt.rn.satfinite.e4m3x2.f16x2 h1, p1;\n"
+      "  cvt.rn.f16x2.e4m3x2 q0, h0;\n"
+      "  cvt.rn.f16x2.e4m3x2 q1, h1;\n"
+      "  mul.rn.f16x2 p0, p0, s;\n"
+      "  mul.rn.f16x2 p1, p1, s;\n"
+      "  fma.rn.f16x2 p0, q0, m, p0;\n"
+      "  fma.rn.f16x2 p1, q1, m, p1;\n"
+      "  cvt.rn.satfinite.e4m3x2.f16x2 l0, p0;\n"
+      "  cvt.rn.satfinite.e4m3x2.f16x2 l1, p1;\n"
+      "  mov.b32 %0, {h0, h1};\n"
+      "  mov.b32 %1, {l0, l1};\n"
+      "}\n"
+      : "=r"(hi), "=r"(lo)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
+// D[tmem] (+)= A[smem] x B[smem]^T of 8-bit operands, K = 32.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with A from TMEM, four bytes a column.
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// TMEM lanes 0-15 of the warp's quarter: threads t < 16 get lane t's columns
+// col.., threads t >= 16 lane t - 16's columns col + HALF...
+template <int N, int HALF>
+__device__ __forceinline__ void ld_halves(uint32_t addr, float* v) {
+  uint32_t r[32];
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], %17;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr), "n"(HALF));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], %33;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr), "n"(HALF));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int N, int HALF>
+__device__ __forceinline__ void st_halves(uint32_t addr, const uint32_t* r) {
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %1, {%2, %3, %4, %5};" ::"r"(addr), "n"(HALF), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2, %3, %4, %5, %6, %7, %8, %9};" ::"r"(addr), "n"(HALF),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, "
+        "{%2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17};" ::"r"(addr),
+        "n"(HALF), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  }
+}
+
+// K-major operand tile of D-byte rows as TMA swizzles it (128 or 64 bytes).
+template <int D>
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(8 * D >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)(D == 128 ? 2 : 4) << 61;
+}
+
+// The V tile as MN-major operand: D dims of a key are one swizzle row, eight
+// keys a group.
+template <int D>
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t addr) {
+  return desc_kmajor<D>(addr);
+}
+
+// --------------------------------------------------------------- work shares
+__device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_t pos, int lane) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + kWarp - 1) / kWarp;
+    const int b = lo + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, lane == 0 || (b < hi && __ldg(prefix + b) <= pos));
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// The part of a request that this CTA does: pages i0 .. i1-1 of its n.
+struct Seg {
+  int b, i0, i1, n, ctx;
+  int64_t p0;
+  __device__ __forceinline__ int tiles() const { return (i1 - i0 + 1) / 2; }
+};
+
+// Walks the segments of pages [pos, end) in order; every role has one.
+struct Walk {
+  const WindowParams& p;
+  int64_t pos, end;
+  int b;
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (pos >= end) return false;
+    while (__ldg(p.prefix + b + 1) <= pos) ++b;
+    s.b = b;
+    s.p0 = __ldg(p.prefix + b);
+    const int64_t p1 = __ldg(p.prefix + b + 1);
+    s.ctx = __ldg(p.ctx_lens + b);
+    s.i0 = (int)(pos - s.p0);
+    s.i1 = (int)(min(end, p1) - s.p0);
+    s.n = (int)(p1 - s.p0);
+    pos = s.p0 + s.i1;
+    return true;
+  }
+};
+
+// Every row sees the whole page.
+__device__ __forceinline__ bool page_whole(const WindowParams& p, int page, int ctx) {
+  const int first = page * kBlock, last = first + kBlock - 1;
+  return last <= ctx && (p.window == 0 || first > ctx + p.R - 1 - p.window || last < p.sinks);
+}
+
+// Four bytes of V of a tile with hidden slots: a NaN becomes 0, and its dim's
+// bit is set in the row of every verify token that sees the slot (rare).
+__device__ __forceinline__ uint32_t hide_nan(const WindowParams& p, uint32_t w, int slot, int ctx, uint32_t* row_bits, int bit) {
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // 0x80 where a byte is 0x7f or 0xff
+  if (nan != 0) {
+    for (int e = 0; e < 4; ++e) {
+      if (!((nan >> (8 * e + 7)) & 1)) continue;
+      w &= ~(0xffu << (8 * e));
+      for (int j = 0; j < p.R; ++j)
+        if (slot_visible(slot, ctx + j, p.window, p.sinks)) atomicOr(row_bits + j * 4, 1u << (bit + e));
+    }
+  }
+  return w;
+}
+
+// NRB: blocks of 16 query rows (1, 2, 4).
+template <int D, int NRB>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const WindowParams p) {
+  using S = Smem<D>;
+  constexpr int kStages = S::kStages;
+  constexpr int KG = 4 / NRB;            // key groups: warps that share a row block
+  constexpr int NK = 16 * NRB;           // keys of a tile that a lane takes
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* xbuf = reinterpret_cast<float*>(smem + S::kX);
+  float2* red = reinterpret_cast<float2*>(smem + S::kRed);
+  TileInfo* info = reinterpret_cast<TileInfo*>(smem + S::kInfoOff);
+  float* fac = reinterpret_cast<float*>(smem + S::kFac);
+  uint32_t* nanmap = reinterpret_cast<uint32_t*>(smem + S::kNan);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  uint64_t* k_empty = k_full + kStages;
+  uint64_t* v_full = k_empty + kStages;
+  uint64_t* v_ready = v_full + kStages;  // masked bytes have been dealt with
+  uint64_t* v_empty = v_ready + kStages;
+  uint64_t* q_full = v_empty + kStages;  // Q of the next request is in place
+  uint64_t* q_empty = q_full + 1;        // the last S of a request is done
+  uint64_t* s_full = q_full + 2;         // [2] S of tile g is there, and so O of tile g - 2
+  uint64_t* p_full = s_full + 2;         // [2] P of tile g has replaced S
+  uint64_t* pv_done = p_full + 2;        // [2] O holds tile g
+  uint64_t* info_full = pv_done + 2;     // [kInfo]
+  uint64_t* fac_full = info_full + kInfo;   // [kSegs]
+  volatile int* rest = reinterpret_cast<volatile int*>(smem + S::kMisc);   // [kSegs] the third term of Q is needed
+  volatile int* last_flag = rest + kSegs * 2;
+  volatile int* abort = last_flag + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc + kSegs * 8 + 8);
+
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int heads = p.Hkv * p.row_tiles;
+  const int kvh = blockIdx.x % heads / p.row_tiles, row_tile = blockIdx.x % heads % p.row_tiles;
+  const int64_t total = __ldg(p.prefix + p.B);
+  const int G = (int)min((int64_t)(gridDim.x / heads), total);
+  const int g_cta = blockIdx.x / heads;
+  if (g_cta >= G) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      sm100::mbar_init(&k_full[s], 1);
+      sm100::mbar_init(&k_empty[s], 1);
+      sm100::mbar_init(&v_full[s], 1);
+      sm100::mbar_init(&v_ready[s], 4);
+      sm100::mbar_init(&v_empty[s], 1);
+    }
+    sm100::mbar_init(q_full, 128);
+    sm100::mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&s_full[i], 1);
+      sm100::mbar_init(&p_full[i], 4);
+      sm100::mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&info_full[i], 1);
+    for (int i = 0; i < kSegs; ++i) sm100::mbar_init(&fac_full[i], 128);
+    *abort = 0;
+    sm100::fence_barrier_init();
+  }
+  if (warp == 0) {
+    sm100::tmem_alloc(tmem_slot, 512);
+    sm100::tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < kNanSegs * 16 * 4; i += kThreads) nanmap[i] = 0;
+  for (int i = threadIdx.x; i < S::kTile / 16; i += kThreads)   // the rest term has no second one
+    *reinterpret_cast<uint4*>(smem + S::kQ + S::kTile + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = sm100::smem_u32(smem);
+
+  const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
+  // Registers: 128 a thread at launch; the softmax warps take what the others
+  // leave (104 + 2 x 152 + 104 = 4 x 128).
+  Walk walk{p, t_begin, t_end, find_request(p.prefix, p.B, t_begin, lane)};
+  bool ok = true;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0) {
+    // ----------------------------------------------------------------- MMA
+    // The whole warp walks the tiles, so that the descriptors stay uniform,
+    // and one elected lane issues. It polls: S of tile g + 1 as soon as its
+    // keys are there (it runs during the softmax of tile g), P V of tile g as
+    // soon as its probabilities and values are.
+    constexpr uint32_t kShape = (1u << 4) | ((uint32_t)(128 >> 4) << 24);   // fp32 D, M = 128
+    constexpr uint32_t idesc_qk = kShape | ((uint32_t)(kKeys >> 3) << 17);              // e4m3 x e4m3
+    constexpr uint32_t idesc_rest = idesc_qk | (1u << 7);                               // e5m2 x e4m3
+    constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // V MN-major
+    const uint64_t qd = desc_kmajor<D>(sbase + S::kQ), kd0 = desc_kmajor<D>(sbase + S::kK);
+    const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV);
+    Seg seg, qseg;
+    Walk qwalk = walk;                   // the tile whose S is issued next
+    bool have = walk.next(seg), qhave = qwalk.next(qseg);
+    int qg = 0, qi = 0, qs = 0, qstage = 0;   // its number, its index in qseg, qseg's number, its stage
+    uint32_t qphase = 0;
+    bool third = false;
+    auto done = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, sm100::mbar_test_wait(bar, parity)) != 0; };
+    auto try_qk = [&]() -> bool {        // false: not ready
+      if (!done(&k_full[qstage], qphase)) return false;
+      if (qi == 0) {
+        if (!done(q_full, (uint32_t)(qs & 1))) return false;
+        third = rest[qs % kSegs] != 0;
+      }
+      const bool last = qi + 1 == qseg.tiles();
+      sm100::tc_fence_after();
+      if (sm100::elect_one()) {
+        const uint32_t d = tmem + (qg & 1) * 128;
+        const uint64_t kd = kd0 + (uint64_t)(qstage * (S::kTile >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, kk ? 1u : 0u);
+        if (third) {
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + (uint64_t)((S::kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_rest, 1u);
+        }
+        sm100::tc_commit(&s_full[qg & 1]);
+        sm100::tc_commit(&k_empty[qstage]);
+        if (last) sm100::tc_commit(q_empty);
+      }
+      __syncwarp();
+      ++qg;
+      if (++qstage == kStages) {
+        qstage = 0;
+        qphase ^= 1u;
+      }
+      if (last) {
+        qhave = qwalk.next(qseg);
+        qi = 0;
+        ++qs;
+      } else {
+        ++qi;
+      }
+      return true;
+    };
+    int g = 0, vstage = 0;
+    uint32_t vphase = 0;
+    for (; have && ok; have = walk.next(seg)) {
+      const int tiles = seg.tiles();
+      for (int i = 0; i < tiles && ok; ++i, ++g) {
+        const uint64_t start = sm100::globaltimer();
+        uint32_t spins = 0;
+        for (;;) {
+          if (qhave && qg <= g + 1 && try_qk()) continue;    // (P V of tile qg - 2 has been issued)
+          const int buf = g & 1;
+          if (qg > g && done(&p_full[buf], (uint32_t)((g >> 1) & 1)) && done(&v_ready[vstage], vphase)) {
+            sm100::tc_fence_after();
+            if (sm100::elect_one()) {
+              const uint64_t vd = vd0 + (uint64_t)(vstage * (S::kTile >> 4));
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 32; ++kk)
+                mma_f8_ts(tmem + kColO + buf * 128, tmem + buf * 128 + kk * 8, vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv,
+                          (i > 1 || kk > 0) ? 1u : 0u);   // the first two tiles begin the two O
+              sm100::tc_commit(&pv_done[buf]);
+              sm100::tc_commit(&v_empty[vstage]);
+            }
+            __syncwarp();
+            if (++vstage == kStages) {
+              vstage = 0;
+              vphase ^= 1u;
+            }
+            break;
+          }
+          if ((++spins & 255u) == 0 && __any_sync(0xffffffffu, *abort || sm100::globaltimer() - start > sm100::kWaitTimeoutNs)) {
+            ok = false;
+            break;
+          }
+        }
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
+      // MMAs in flight end before the shared memory and TMEM go (else the softmax warps have waited for every P V)
+      if (g > 0) sm100::mbar_wait_timeout(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), sm100::kWaitTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- TMA
+    const uint64_t pol = sm100::l2_policy_evict_first();
+    if (lane == 0) {
+      sm100::tma_prefetch_desc(&tm_k);
+      sm100::tma_prefetch_desc(&tm_v);
+    }
+    int g = 0;
+    Seg seg;
+    while (ok && walk.next(seg)) {
+      const PageSpan span = page_span(seg.ctx, p.R, p.window, p.sinks);
+      for (int i = seg.i0; i < seg.i1 && ok; i += kWarp) {
+        int blk = -1, page = -1;
+        float sk = 1.0f, lsv = 0.0f, isv = 1.0f;
+        if (i + lane < seg.i1) {
+          page = span.page(i + lane);
+          blk = p.block_table[(int64_t)seg.b * p.max_blocks + page];
+          if (blk < 0 || blk >= p.num_blocks) {
+            raise_error(p.err, MTP_ERR_BLOCK_ID);
+            page = -1;
+          } else {
+            sk = p.k_scale[(int64_t)blk * p.Hkv + kvh];
+            const float sv = p.v_scale[(int64_t)blk * p.Hkv + kvh];
+            if (!scale_ok(sk) || !scale_ok(sv)) {
+              raise_error(p.err, MTP_ERR_SCALE);
+              page = -1;
+              sk = 1.0f;
+            } else {
+              lsv = log2f(sv);
+              isv = 1.0f / sv;
+              if (!page_whole(p, page, seg.ctx)) page = -2 - page;
+            }
+          }
+        }
+        const int n = min(kWarp, seg.i1 - i);
+        for (int x = 0; x < n; x += 2, ++g) {
+          TileInfo in;
+          int id[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {        // (lane 31 of an odd rest has page -1)
+            id[y] = __shfl_sync(0xffffffffu, blk, x + y);
+            in.page[y] = __shfl_sync(0xffffffffu, page, x + y);
+            in.sk[y] = __shfl_sync(0xffffffffu, sk, x + y);
+            in.lsv[y] = __shfl_sync(0xffffffffu, lsv, x + y);
+            in.isv[y] = __shfl_sync(0xffffffffu, isv, x + y);
+          }
+          int go = 1;
+          if (lane == 0) {
+            const int s = g % kStages;
+            const uint32_t parity = (uint32_t)((g / kStages) & 1) ^ 1u;
+            const uint32_t bytes = ((in.page[0] != -1) + (in.page[1] != -1)) * (uint32_t)(S::kTile / 2);
+            go = sm100::mbar_wait(&k_empty[s], parity, abort);
+            if (go) {
+              info[g % kInfo] = in;
+              sm100::mbar_arrive(&info_full[g % kInfo]);
+              if (bytes) sm100::mbar_arrive_expect_tx(&k_full[s], bytes);
+              else sm100::mbar_arrive(&k_full[s]);
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (in.page[y] != -1)
+                  sm100::tma_load_4d(smem + S::kK + s * S::kTile + y * (S::kTile / 2), &tm_k, &k_full[s], 0, kvh, 0, id[y], pol);
+              go = sm100::mbar_wait(&v_empty[s], parity, abort);
+            }
+            if (go) {
+              if (bytes) sm100::mbar_arrive_expect_tx(&v_full[s], bytes);
+              else sm100::mbar_arrive(&v_full[s]);
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (in.page[y] != -1)
+                  sm100::tma_load_4d(smem + S::kV + s * S::kTile + y * (S::kTile / 2), &tm_v, &v_full[s], 0, kvh, 0, id[y], pol);
+            } else {
+              *abort = 1;
+              raise_error(p.err, MTP_ERR_TIMEOUT);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+          if (!ok) break;
+        }
+      }
+    }
+    // Every copy issued lands before the CTA may exit: the last fill of each
+    // stage (after a timeout the K copy of tile g may be on its way too).
+    if (lane == 0) {
+      const int nk = ok ? g : g + 1;
+      for (int s = 0; s < kStages; ++s) {
+        const int fills = g > s ? (g - 1 - s) / kStages + 1 : 0;
+        const int kfills = nk > s ? (nk - 1 - s) / kStages + 1 : 0;
+        if (ok) {
+          if (fills) {
+            sm100::mbar_wait_timeout(&k_full[s], (uint32_t)((fills - 1) & 1), sm100::kWaitTimeoutNs);
+            sm100::mbar_wait_timeout(&v_full[s], (uint32_t)((fills - 1) & 1), sm100::kWaitTimeoutNs);
+          }
+        } else {
+          if (fills) sm100::mbar_wait_timeout(&v_full[s], (uint32_t)((fills - 1) & 1), 1000000);
+          if (kfills) sm100::mbar_wait_timeout(&k_full[s], (uint32_t)((kfills - 1) & 1), 1000000);
+        }
+      }
+    }
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    // -------------------------------------------------- softmax and output
+    const int w = warp & 3, wg = (warp >> 2) - 1, st = threadIdx.x - 128;
+    const int rb = w % NRB, kg = w / NRB, half = lane >> 4, r16 = lane & 15;
+    const int page_half = (kg * 2 + half) * NK / kBlock;   // which page of a tile the lane's keys are in
+    const int in_page = (kg * 2 + half) * NK % kBlock;
+    const int row = row_tile * 64 + rb * 16 + r16;
+    const int j = min(row, p.rows - 1) / p.group;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + wg * 128, lanes_lo = lanes + (16u << 16);
+    auto soft_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    int g = 0;
+    Seg seg;
+    for (int sn = 0; walk.next(seg); ++sn) {
+      const int tiles = seg.tiles(), pos = seg.ctx + j;
+      const int low = p.window == 0 ? 0 : pos - p.window + 1;
+      ok = ok && __all_sync(0xffffffffu, sm100::mbar_wait(&fac_full[sn % kSegs], (uint32_t)((sn / kSegs) & 1), abort) ? 1 : 0);
+      const float row_fac = fac[(sn % kSegs) * 64 + rb * 16 + r16];
+      float ref = -INFINITY, top_ref = -INFINITY;          // of the probabilities; the largest it was
+      float lref = -INFINITY, sum = 0.0f;                  // maximum of the scores (lazy), sum relative to it
+      int low_tiles = 0;                                   // in a row, with a small largest probability
+      bool begun = false;                                  // O holds something
+      const int g_end = g + tiles;
+      for (g += (g ^ wg) & 1; g < g_end; g += 2) {         // this group's tiles
+        ok = ok && __all_sync(0xffffffffu, (sm100::mbar_wait(&info_full[g % kInfo], (uint32_t)((g / kInfo) & 1), abort) &&
+                                            sm100::mbar_wait(&s_full[wg], (uint32_t)((g >> 1) & 1), abort))
+                                               ? 1
+                                               : 0);
+        if (!ok) break;                                    // the segment's end still meets the others
+        sm100::tc_fence_after();
+        float x[NK];
+        {
+          constexpr int N = NK < 32 ? NK : 32;
+#pragma unroll
+          for (int k0 = 0; k0 < NK; k0 += N) {
+            float y[N];
+            ld_halves<N, NK>(lanes + kg * 2 * NK + k0, x + k0);
+            ld_halves<N, NK>(lanes_lo + kg * 2 * NK + k0, y);
+            sm100::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < N; ++k) x[k0 + k] += y[k];
+          }
+        }
+        const float sk = info[g % kInfo].sk[page_half], lsv = info[g % kInfo].lsv[page_half];
+        const float isv = info[g % kInfo].isv[page_half];
+        const int mark = info[g % kInfo].page[page_half];
+        if (__any_sync(0xffffffffu, mark < 0)) {
+          const int slot = (mark < 0 ? -2 - mark : mark) * kBlock + in_page, top = mark == -1 ? INT_MIN : pos;
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+            if (!(slot + k <= top && (slot + k >= low || slot + k < p.sinks))) x[k] = -INFINITY;
+        }
+        // (a factor of 0 would turn a hidden -inf into NaN; scores that small are 0 all the same)
+        const float f = fmaxf(row_fac * sk, 1e-36f);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < NK; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
+        const float score = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+        float most = score + lsv, highest = score;
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));   // with the row's other half
+        highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, 16));
+        if (highest > lref + 20.0f) {
+          sum *= lref == -INFINITY ? 0.0f : ex2(lref - highest);
+          lref = highest;
+        }
+        // (a row with nothing visible in the tile stays as it is)
+        const float to = fmaxf(most - kNominalP, top_ref - kDown);
+        const bool low = most < ref + kLeastP && most != -INFINITY;
+        low_tiles = low ? low_tiles + 1 : 0;
+        const bool move = most > ref + kMostP || (low_tiles >= kLowTiles && to < ref - 1.0f);
+        if (__any_sync(0xffffffffu, move)) {
+          const float c = !move ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - to);
+          if (move) ref = to;
+          top_ref = fmaxf(top_ref, ref);
+          if (begun) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {               // this thread's half of the row's dims, 16 at a time
+              float o[16], o2[16];
+              ld_halves<16, D / 2>(lanes + kColO + q * 16, o);
+              ld_halves<16, D / 2>(lanes_lo + kColO + q * 16, o2);
+              sm100::tmem_ld_wait();
+              uint32_t r[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * c);
+              st_halves<16, D / 2>(lanes + kColO + q * 16, r);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o2[k] * c);
+              st_halves<16, D / 2>(lanes_lo + kColO + q * 16, r);
+            }
+          }
+        }
+        const float shift = lsv - (ref == -INFINITY ? 0.0f : ref);
+        float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t hi[NK / 4], lo[NK / 4];
+#pragma unroll
+        for (int k = 0; k < NK; k += 4) {
+          const float a = ex2(fmaf(x[k], f, shift)), b = ex2(fmaf(x[k + 1], f, shift));
+          const float c = ex2(fmaf(x[k + 2], f, shift)), d = ex2(fmaf(x[k + 3], f, shift));
+          add[0] += a, add[1] += b, add[2] += c, add[3] += d;
+          split4(a, b, c, d, hi[k / 4], lo[k / 4]);
+        }
+        // 2^(score - lref) in sum: without the scale of V
+        if (lref != -INFINITY) sum += ((add[0] + add[1]) + (add[2] + add[3])) * ex2(-shift - lref);
+        else sum += (add[0] + add[1]) + (add[2] + add[3]);   // nothing visible yet: 0, or NaN from K
+        if constexpr (KG > 1) {                            // columns of the other warps' keys
+          const uint32_t z[NK / 4] = {};
+#pragma unroll
+          for (int y = 0; y < KG; ++y) {
+            if (y == kg) continue;
+            st_halves<NK / 4, NK / 4>(lanes + y * (NK / 2), z);
+            st_halves<NK / 4, NK / 4>(lanes_lo + y * (NK / 2), z);
+          }
+        }
+        st_halves<NK / 4, NK / 4>(lanes + kg * (NK / 2), hi);
+        st_halves<NK / 4, NK / 4>(lanes_lo + kg * (NK / 2), lo);
+        begun = true;
+        tmem_st_wait();
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&p_full[wg]);
+      }
+      // ---- the request's part is done: join the lanes of each row
+      g = g_end;
+      const int last_g = g - 1 - ((g - 1 - wg) & 1);       // this group's last tile so far
+      ok = ok && (!begun || __all_sync(0xffffffffu, sm100::mbar_wait(&pv_done[wg], (uint32_t)((last_g >> 1) & 1), abort) ? 1 : 0));
+      sm100::tc_fence_after();
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (half == 0) red[(wg * 4 + w) * 16 + r16] = make_float2(lref, sum);
+      soft_sync();
+      float M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int y = 0; y < 2 * KG; ++y) M = fmaxf(M, red[((y / KG) * 4 + rb + NRB * (y % KG)) * 16 + r16].x);
+#pragma unroll
+      for (int y = 0; y < 2 * KG; ++y) {
+        const float2 v = red[((y / KG) * 4 + rb + NRB * (y % KG)) * 16 + r16];
+        L += v.y * (v.x == -INFINITY ? 1.0f : ex2(v.x - M));   // (nothing seen: 0, or NaN from K)
+      }
+      const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
+      const float own = (ref == -INFINITY ? 0.0f : ex2(ref - M)) * (whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f);
+      const float poison = sum != sum ? sum : 0.0f;            // NaN in K: every dim of the row
+      const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
+      const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
+      // Slot 0 of a CTA is for a request it did not begin, slot 1 for one it began.
+      const size_t rec = (size_t)NRB * 16 * (D + 2);
+      auto slot_of = [&](int gg, int which) {
+        return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * p.row_tiles + row_tile) * rec;
+      };
+      float* part = whole ? nullptr : slot_of(g_cta, seg.i0 > 0 ? 0 : 1);
+      if (!whole && wg == 0 && kg == 0 && half == 0) reinterpret_cast<float2*>(part + (size_t)NRB * 16 * D)[rb * 16 + r16] = make_float2(M, L);
+      auto out_row = [&](int local) {
+        const int rr = first_row + local;
+        return static_cast<__nv_bfloat16*>(p.out) + (out0 + (int64_t)(rr / p.group) * p.Hq + rr % p.group) * D;
+      };
+      __nv_bfloat16* put_out[(NRB + 1) / 2];                   // the rows whose dims this thread writes
+#pragma unroll
+      for (int u = 0; u < (NRB + 1) / 2; ++u) put_out[u] = out_row(min(u * 32 + (st >> 3), n_rows - 1));
+      auto put = [&](int u, int dim, const float4& v) {        // four dims of a row
+        const int local = u * 32 + (st >> 3);
+        if (local >= n_rows) return;
+        if (whole) {
+          __nv_bfloat16* to = put_out[u] + dim;
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        } else {
+          *reinterpret_cast<float4*>(part + (size_t)local * D + dim) = v;
+        }
+      };
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {                       // 16 dims of each half of the row
+        float y[16], y2[16];
+        if (ok) {
+          ld_halves<16, D / 2>(lanes + kColO + c * 16, y);
+          ld_halves<16, D / 2>(lanes_lo + kColO + c * 16, y2);
+          sm100::tmem_ld_wait();
+        }
+        const int dim0 = half * (D / 2) + c * 16;
+        const uint32_t bits = nanmap[((sn % kNanSegs) * 16 + j) * 4 + (dim0 >> 5)] >> (dim0 & 31);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          // (nothing seen: the lane's O may be anything, so it takes no part)
+          y[k] = own == 0.0f || !ok ? 0.0f : fmaf(y2[k], 1.0f / kLoScale, y[k]) * own;
+          if ((bits >> k) & 1) y[k] = NAN;
+          y[k] += poison;
+        }
+        float* to = xbuf + (size_t)((wg * 4 + w) * 16 + r16) * 36 + half * 16;
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+        soft_sync();
+#pragma unroll
+        for (int u = 0; u < (NRB + 1) / 2; ++u) {
+          const int local = u * 32 + (st >> 3), d4 = (st & 7) * 4;
+          if (local < NRB * 16) {
+            const float* from = xbuf + (size_t)((local >> 4) * 16 + (local & 15)) * 36 + d4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int y2 = 0; y2 < 2 * KG; ++y2) {
+              const float4 o4 = *reinterpret_cast<const float4*>(from + ((y2 / KG) * 4 + NRB * (y2 % KG)) * 16 * 36);
+              v.x += o4.x, v.y += o4.y, v.z += o4.z, v.w += o4.w;
+            }
+            put(u, (d4 >> 4) * (D / 2) + c * 16 + (d4 & 15), v);
+          }
+        }
+        soft_sync();
+      }
+      sm100::tc_fence_before();
+      if (!whole) {
+        __threadfence();
+        soft_sync();
+        const int g0 = (int)(((seg.p0 + 1) * G - 1) / total), g1 = (int)(((seg.p0 + seg.n) * G - 1) / total);
+        if (st == 0) {
+          const int before = atomicAdd(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile, 1);
+          *last_flag = before == g1 - g0;
+        }
+        soft_sync();
+        if (*last_flag) {
+          // Last of the CTAs that share the request: join their parts, in order.
+          __threadfence();
+          for (int u = st; u < n_rows * (D / 4); u += 256) {
+            const int local = u / (D / 4), dim = u % (D / 4) * 4;
+            float m = -INFINITY, l = 0.0f;
+            for (int gg = g0; gg <= g1; ++gg)
+              m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(slot_of(gg, gg == g0) + (size_t)NRB * 16 * D) + local).x);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int gg = g0; gg <= g1; ++gg) {
+              const float* from = slot_of(gg, gg == g0);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (size_t)NRB * 16 * D) + local);
+              const float4 o4 = __ldcg(reinterpret_cast<const float4*>(from + (size_t)local * D + dim));
+              const float c = ml.x == -INFINITY ? 1.0f : ex2(ml.x - m);   // (nothing seen: zeros, or NaN)
+              l += ml.y * c;
+              v.x += o4.x * c, v.y += o4.y * c, v.z += o4.z * c, v.w += o4.w * c;
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            __nv_bfloat16* to = out_row(local) + dim;
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+          }
+        }
+      }
+      soft_sync();                                             // red, the flag and the bitmap have been read
+      if (st < 64) nanmap[(sn % kNanSegs) * 64 + st] = 0;
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      raise_error(p.err, MTP_ERR_TIMEOUT);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // --------------------------------------------------- Q, then masked V
+    // Q of a request: eight threads a row, D/8 dims each, read while the last
+    // one's tiles are still worked on, and written once its last S is done.
+    constexpr int kDims = D / 8, kVec = kDims / 8;         // 16-byte vectors of bf16
+    const int cw = warp - 12;            // 32 of a tile's keys
+    const int t128 = threadIdx.x - 384, r16 = t128 >> 3, part = t128 & 7;
+    int s = 0, g = 0;
+    uint32_t phase = 0;
+    Seg seg;
+    for (int sn = 0; ok && walk.next(seg); ++sn) {
+      uint4 w[NRB][kVec];
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb) {
+        const int row = min(row_tile * 64 + rb * 16 + r16, p.rows - 1);   // padding repeats the last row
+        const int64_t at = ((int64_t)(seg.b * (int64_t)p.R + row / p.group) * p.Hq + kvh * p.group + row % p.group) * D;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at + part * kDims);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) w[rb][v] = __ldg(src + v);
+      }
+      if (threadIdx.x == 384) rest[sn % kSegs] = 0;
+      ok = __all_sync(0xffffffffu, sm100::mbar_wait(q_empty, (uint32_t)((sn & 1) ^ 1), abort) ? 1 : 0);
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      bool need = false;
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb) {
+        float top = 0.0f, sum = 0.0f, left = 0.0f;
+        float q[kDims];
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          const uint32_t word[4] = {w[rb][v].x, w[rb][v].y, w[rb][v].z, w[rb][v].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            q[v * 8 + e] = __uint_as_float((e & 1) ? word[e >> 1] & 0xffff0000u : word[e >> 1] << 16);
+            const float a = fabsf(q[v * 8 + e]);
+            top = fmaxf(top, a <= FLT_MAX ? a : 0.0f);
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = top > 0.0f ? max(-100, (int)(__float_as_uint(top) >> 23) - 127 - 7) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        uint32_t hi[kDims / 4], lo[kDims / 4], re[kDims / 4];
+#pragma unroll
+        for (int x = 0; x < kDims / 4; ++x) {
+          float a[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = fabsf(q[x * 4 + e]) <= FLT_MAX ? q[x * 4 + e] * down : __uint_as_float(0x7fffffffu);
+            sum += fabsf(a[e]);
+          }
+          hi[x] = f_to_e4m3x4(a[0], a[1], a[2], a[3]);
+          const float4 h = e4m3x4_to_f(hi[x]);
+          a[0] -= h.x, a[1] -= h.y, a[2] -= h.z, a[3] -= h.w;
+          lo[x] = f_to_e4m3x4(a[0], a[1], a[2], a[3]);
+          const float4 l = e4m3x4_to_f(lo[x]);
+          a[0] -= l.x, a[1] -= l.y, a[2] -= l.z, a[3] -= l.w;
+          left += fabsf(a[0]) + fabsf(a[1]) + fabsf(a[2]) + fabsf(a[3]);
+          const uint32_t r0 = __nv_cvt_float2_to_fp8x2(make_float2(a[0], a[1]), __NV_SATFINITE, __NV_E5M2);
+          const uint32_t r1 = __nv_cvt_float2_to_fp8x2(make_float2(a[2], a[3]), __NV_SATFINITE, __NV_E5M2);
+          re[x] = r0 | (r1 << 16);
+        }
+#pragma unroll
+        for (int y = 0; y < KG; ++y) {                     // the row's lanes: of warps rb, rb + NRB, ..
+          const int l128 = 32 * (rb + NRB * y) + r16;
+          auto put = [&](uint8_t* to, const uint32_t* v) {  // 16 or 8 bytes
+            if constexpr (kDims == 16) *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+            else *reinterpret_cast<uint2*>(to) = make_uint2(v[0], v[1]);
+          };
+          const int chunk = part * kDims / 16, in = part * kDims % 16;
+          if (ok) {
+            put(smem + S::kQ + S::at(l128, chunk) + in, hi);
+            put(smem + S::kQ + S::at(l128 + 16, chunk) + in, lo);
+            put(smem + S::kQ + S::kTile + S::at(l128, chunk) + in, re);
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          left += __shfl_xor_sync(0xffffffffu, left, o);
+        }
+        need |= left > sum * 0x1p-19f;
+        if (part == 0) fac[(sn % kSegs) * 64 + rb * 16 + r16] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + ex) << 23);
+      }
+      if (need) rest[sn % kSegs] = 1;
+      fence_async_smem();
+      sm100::mbar_arrive(&fac_full[sn % kSegs]);
+      sm100::mbar_arrive(q_full);
+
+      const int tiles = seg.tiles();
+      for (int i = 0; i < tiles; ++i, ++g) {
+        ok = ok && __all_sync(0xffffffffu, (sm100::mbar_wait(&info_full[g % kInfo], (uint32_t)((g / kInfo) & 1), abort) &&
+                                            sm100::mbar_wait(&v_full[s], phase, abort))
+                                               ? 1
+                                               : 0);
+        if (!ok) break;
+        const int mark = info[g % kInfo].page[cw >> 1];
+        if (mark < 0) {                  // some of its slots are hidden, or nothing was loaded
+          uint8_t* v = smem + S::kV + s * S::kTile;
+          for (int x = lane; x < 32 * (D / 16); x += kWarp) {
+            const int key = cw * 32 + x / (D / 16), c = x % (D / 16);
+            uint4* at = reinterpret_cast<uint4*>(v + S::at(key, c));
+            uint4 b = *at;
+            const int slot = (-2 - mark) * kBlock + (key & 63), bit = c * 16 & 31;
+            uint32_t* row_bits = nanmap + (sn % kNanSegs) * 64 + (c >> 1);
+            if (mark == -1) {
+              b = make_uint4(0, 0, 0, 0);
+            } else {
+              b.x = hide_nan(p, b.x, slot, seg.ctx, row_bits, bit);
+              b.y = hide_nan(p, b.y, slot, seg.ctx, row_bits, bit + 4);
+              b.z = hide_nan(p, b.z, slot, seg.ctx, row_bits, bit + 8);
+              b.w = hide_nan(p, b.w, slot, seg.ctx, row_bits, bit + 12);
+            }
+            *at = b;
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&v_ready[s]);
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      raise_error(p.err, MTP_ERR_TIMEOUT);
+    }
+  }
+
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  if (warp == 0) sm100::tmem_dealloc(tmem, 512);
+}
+
+template <int D, int NRB>
+cudaError_t launch(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
+  auto encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)kBlock, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)a.Hkv * D, (cuuint64_t)kBlock * a.Hkv * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, 1, (cuuint32_t)kBlock, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i) {
+    if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i == 0 ? a.k_cache : a.v_cache, dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  auto kern = kv8_tc_kernel<D, NRB>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(pl.ctas_per_head * a.Hkv * pl.row_tiles), kThreads, Smem<D>::kBytes, s>>>(maps[0], maps[1], p);
+  return cudaGetLastError();
+}
+
+// Blocks of 16 rows of a CTA: 1, 2 or 4; a KV head of more than 64 rows takes
+// several CTAs of 64.
+int row_blocks(const mtp_window_attn_args& a) {
+  const int rows = a.Hq / a.Hkv * (a.D + 1);
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+
+}  // namespace
+
+WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count) {
+  WindowPlan pl{};
+  const int nrb = row_blocks(a);
+  pl.row_tiles = (a.Hq / a.Hkv * (a.D + 1) + 63) / 64;
+  pl.row_warps = 1;                                        // arrival counters per (request, KV head, row tile)
+  pl.ctas_per_head = (int)std::max<long long>(1, sm_count / ((long long)a.Hkv * pl.row_tiles));
+  const size_t heads = (size_t)a.Hkv * pl.row_tiles;
+  pl.ws_prefix = 0;
+  pl.ws_arrived = ((size_t)(a.B + 1) * sizeof(int64_t) + 255) / 256 * 256;
+  pl.ws_partial_o = pl.ws_arrived + ((size_t)a.B * heads * sizeof(int32_t) + 255) / 256 * 256;
+  pl.ws_bytes = pl.ws_partial_o + (size_t)pl.ctas_per_head * 2 * heads * nrb * 16 * (a.d + 2) * sizeof(float);
+  pl.ws_bytes = (pl.ws_bytes + 255) / 256 * 256;
+  return pl;
+}
+
+cudaError_t launch_kv8_tc(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
+  const int nrb = row_blocks(a);
+  if (a.d == 128) return nrb == 1 ? launch<128, 1>(a, pl, p, s) : nrb == 2 ? launch<128, 2>(a, pl, p, s) : launch<128, 4>(a, pl, p, s);
+  return nrb == 1 ? launch<64, 1>(a, pl, p, s) : nrb == 2 ? launch<64, 2>(a, pl, p, s) : launch<64, 4>(a, pl, p, s);
+}
+
+}  // namespace mtp

@@ -131,6 +131,10 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
     if (p.k_scale != nullptr) {
       sk = p.k_scale[(int64_t)blk * p.Hkv + kvh];
       sv = p.v_scale[(int64_t)blk * p.Hkv + kvh];
+      if (!scale_ok(sk) || !scale_ok(sv)) {
+        if (threadIdx.x == 0) raise_error(p.err, MTP_ERR_SCALE);
+        continue;
+      }
     }
     __syncthreads();                           // the last page has been read
     for (int x = threadIdx.x; x < kBlock * (D / 4); x += kSimtWarps * kWarp) {
@@ -308,7 +312,7 @@ int check_window(const mtp_window_attn_args* a, bool kv8) {
 bool uses_mma(const mtp_window_attn_args& a) { return a.dtype == MTP_BF16; }
 
 WindowPlan plan_window(const mtp_window_attn_args& a, bool kv8, int sm_count) {
-  if (uses_mma(a)) return plan_window_mma(a, kv8, sm_count);
+  if (uses_mma(a)) return kv8 ? plan_kv8_tc(a, sm_count) : plan_window_mma(a, kv8, sm_count);
   WindowPlan p{};
   const int rows = a.Hq / a.Hkv * (a.D + 1);
   const long long ctas = (long long)a.B * a.Hkv * ((rows + kSimtRows - 1) / kSimtRows);
@@ -429,7 +433,7 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
   int launches = 0;
   if (mma) {
     launches = 1;
-    e = launch_window_mma(*a, kv8, pl, p, s);
+    e = kv8 ? launch_kv8_tc(*a, pl, p, s) : launch_window_mma(*a, kv8, pl, p, s);
   } else {
     e = launch_simt<float>(p, a->d, kv8, s, &launches);
   }

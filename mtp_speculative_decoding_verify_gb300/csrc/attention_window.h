@@ -43,6 +43,8 @@ struct WindowSchedule {
 WindowPlan plan_window_mma(const mtp_window_attn_args& a, bool kv8, int sm_count);
 cudaError_t launch_window_mma(const mtp_window_attn_args& a, bool kv8, const WindowPlan& pl, const WindowParams& p,
                               cudaStream_t s);
+WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count);
+cudaError_t launch_kv8_tc(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, const WindowSchedule& sch, unsigned* err,
                               cudaStream_t s);
 

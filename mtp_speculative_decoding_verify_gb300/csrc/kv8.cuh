@@ -32,6 +32,10 @@ __device__ __forceinline__ uint32_t f_to_e4m3x4(float a, float b, float c, float
   return lo | (hi << 16);
 }
 
+// Scales that the append makes lie in [2^-100, 2^121): what is outside was not
+// written by it, and a block with such a scale takes no part.
+__device__ __forceinline__ bool scale_ok(float s) { return s >= 0x1p-100f && s < 0x1p121f; }
+
 // Scale of a block's head after values of largest finite magnitude `a` are
 // written to it: the old scale (2^-100 when the block's first slot is among
 // the written ones) doubled until a <= 448 scale. Doubling keeps what the

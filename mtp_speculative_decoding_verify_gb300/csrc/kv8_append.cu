@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   const int lo = max(ctx, i * kBlock), cnt = min(ctx + n, (i + 1) * kBlock) - lo, off = lo - i * kBlock;
   float* scale = (is_v ? p.v_scale : p.k_scale) + (int64_t)blk * p.Hkv + h;
   const float old = *scale;
-  if (off > 0 && !(old > 0.0f && old <= FLT_MAX)) {
+  if (off > 0 && !scale_ok(old)) {
     if (tid == 0) raise_error(p.err, MTP_ERR_SCALE);
     return;
   }
