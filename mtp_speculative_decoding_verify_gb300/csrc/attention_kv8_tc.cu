@@ -21,8 +21,7 @@
 // query rows as hi, lanes 32 w + 16 .. the same rows as lo: one MMA gives
 // both terms, added after they are read. With fewer than 64 rows several
 // warps hold the same block (row block w % NRB, key group w / NRB) and each
-// takes its own keys of the tile (two pages, 128 keys): P is zero outside a
-// warp's own keys (those columns are written once, at the start), so every
+// takes its own keys of the tile: P is zero outside a warp's own keys, so every
 // row of every warp is an online softmax of its own, and warps exchange
 // nothing until the request ends. The 16x32bx2 form of the TMEM loads and
 // stores gives the threads t and t + 16 of a warp two column ranges of one
@@ -33,21 +32,21 @@
 // scale of V rides along, and the sum, which is kept relative to a maximum of
 // scores alone, divides it out again. e4m3 holds 2^-9 (lo: 2^-13) to 2^8, so
 // ref follows the tiles up and down: when a tile's largest probability would
-// pass 2^8, or was below 2^-2 for three tiles, O is rescaled in TMEM to put
-// it at 2. (Down, so that a few large scores do not cost the rest of the
+// pass 2^8, or was below 2^-4 for three of the row's tiles, O is rescaled in TMEM. (Down, so that a few large scores do not cost the rest of the
 // context its bits; O in fp32 has room for the 60 octaves that are allowed.)
 //
-// Two groups of four softmax warps take alternate tiles, each with an S
-// buffer and an O of its own, joined with the rest when the request ends.
-// P lies in the columns of the S it came from: P V of tile g and S of tile
-// g + 2 are issued back to back, in the order in which they use the buffer.
+// Two groups of four softmax warps take alternate tiles, each with an S buffer
+// and an O of its own (joined with the rest when the request ends), so that
+// one computes while the other waits for its products. P lies in the columns
+// of the S it came from.
 //
 // Hidden slots: only tiles with a slot that not every row sees are masked.
 // There V's bytes that are NaN become 0 in shared memory (0 x NaN), and a
 // bitmap of (verify token, dim) puts NaN back into the rows that do see them.
 //
-// Warps: 0 MMA issue, 1 TMA (block ids and scales of 32 pages at a time, one
-// a lane), 4-11 softmax and output, 12-15 masked V and the next request's Q.
+// Warps: 0 S = Q K^T, 1 TMA (block ids and scales of 32 pages at a time, one a
+// lane), 2 and 3 P V (with polling for all three products in one warp, its
+// checks were the slowest part of a tile), 4-11 softmax and output, 12-15 masked V and the next request's Q.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <limits.h>
@@ -71,8 +70,11 @@ constexpr int kKeys = 128;
 constexpr int kInfo = 8;               // tiles whose scales and pages are held: the TMA warp is at most 6 stages and 2 S buffers ahead
 constexpr int kSegs = 4;               // requests whose row factors are held; the Q warps are at most 3 ahead
 constexpr int kNanSegs = 8;            // requests whose NaN bitmaps are held; their writers are at most 6 stages ahead
-// log2 of a tile's largest probability: the bounds that ref keeps, and where a rescale puts it
-constexpr float kMostP = 8.0f, kLeastP = -2.0f, kNominalP = 1.0f;
+constexpr int kSegRing = 16;           // requests announced; the TMA warp is at most 6 stages, 2 S and 1 ahead
+// log2 of a tile's largest probability: the bounds that ref keeps, where the first tile puts it, and where a rescale
+// up and one down do. Twelve octaves apart, and the landings leave room for what comes: tiles whose maxima alternate
+// over up to nine octaves (blocks of different scales) settle after a move or two.
+constexpr float kMostP = 8.0f, kLeastP = -4.0f, kFirstP = 1.0f, kUpP = 5.0f, kDownP = -1.0f;
 constexpr int kLowTiles = 3;
 constexpr float kDown = 60.0f;         // ref is never further below the largest there was
 constexpr float kLoScale = 16.0f;      // P's second term is held times this
@@ -87,10 +89,11 @@ struct Smem {
   static constexpr int kX = kQ + 2 * kTile;               // join of a row's partial results: [8 warps][16][36] floats
   static constexpr int kRed = kX + 128 * 36 * 4;          // [8 warps][16] (maximum, sum)
   static constexpr int kInfoOff = kRed + 128 * 8;         // [kInfo] TileInfo
-  static constexpr int kFac = kInfoOff + kInfo * 32;      // [kSegs][64] factors of the rows' scores
+  static constexpr int kRing = kInfoOff + kInfo * 32;     // [kSegRing] Seg
+  static constexpr int kFac = kRing + kSegRing * 32;      // [kSegs][64] factors of the rows' scores
   static constexpr int kNan = kFac + kSegs * 64 * 4;      // [kNanSegs][16][4] words
   static constexpr int kBar = kNan + kNanSegs * 16 * 4 * 4;
-  static constexpr int kBars = 5 * kStages + 2 + 2 + 2 + 2 + kInfo + kSegs;
+  static constexpr int kBars = 5 * kStages + 2 + 2 + 2 + 2 + kInfo + kSegs + kSegRing;
   static constexpr int kMisc = kBar + kBars * 8;          // rest flags [kSegs][2], join flag, abort, TMEM base
   static constexpr int kBytes = kMisc + kSegs * 8 + 16 + 1024;
   // byte offset of 16-byte chunk c of row r of a K-major operand tile, as TMA swizzles it
@@ -101,10 +104,13 @@ struct Smem {
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "227 KB of shared memory");
 
-struct TileInfo {            // of its two pages
-  float sk[2];               // scale of K
-  float lsv[2], isv[2];      // log2 and reciprocal of the scale of V
-  int page[2];               // index in the request, -1: nothing loaded; -2 - index: some row does not see all of it
+struct PageInfo {
+  float sk, lsv;             // scale of K, log2 of the scale of V
+  int mark;                  // the page's index in the request; -2 - index: some row does not see all of it; -1: not loaded
+  int pad;
+};
+struct TileInfo {
+  PageInfo page[2];
 };
 
 // ------------------------------------------------------------- instructions
@@ -145,6 +151,20 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
       : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
+// Named barrier over `count` threads; true if all of them passed true. What
+// decides whether a group of warps that meet at barriers goes on.
+template <int kId, int kCount>
+__device__ __forceinline__ bool barrier_all(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbar.red.and.pred po, %2, %3, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kId), "n"(kCount)
+      : "memory");
+  return r != 0;
+}
+
 // D[tmem] (+)= A[smem] x B[smem]^T of 8-bit operands, K = 32.
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -177,8 +197,12 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 template <int N, int HALF>
 __device__ __forceinline__ void ld_halves(uint32_t addr, float* v) {
   uint32_t r[32];
-  static_assert(N == 16 || N == 32, "columns");
-  if constexpr (N == 16) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], %9;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr), "n"(HALF));
+  } else if constexpr (N == 16) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], %17;"
@@ -202,8 +226,11 @@ __device__ __forceinline__ void ld_halves(uint32_t addr, float* v) {
 
 template <int N, int HALF>
 __device__ __forceinline__ void st_halves(uint32_t addr, const uint32_t* r) {
-  static_assert(N == 4 || N == 8 || N == 16, "columns");
-  if constexpr (N == 4) {
+  static_assert(N == 2 || N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 2) {
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x2.b32 [%0], %1, {%2, %3};" ::"r"(addr), "n"(HALF), "r"(r[0]), "r"(r[1])
+                 : "memory");
+  } else if constexpr (N == 4) {
     asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %1, {%2, %3, %4, %5};" ::"r"(addr), "n"(HALF), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
@@ -248,14 +275,15 @@ __device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_
   return lo;
 }
 
-// The part of a request that this CTA does: pages i0 .. i1-1 of its n.
+// The part of a request that this CTA does: pages i0 .. i1-1 of its n, the
+// first of which is page p0 of the line; n = 0 ends the work.
 struct Seg {
-  int b, i0, i1, n, ctx;
+  int b, i0, i1, n, ctx, pad;
   int64_t p0;
   __device__ __forceinline__ int tiles() const { return (i1 - i0 + 1) / 2; }
 };
 
-// Walks the segments of pages [pos, end) in order; every role has one.
+// Walks the segments of pages [pos, end) in order.
 struct Walk {
   const WindowParams& p;
   int64_t pos, end;
@@ -304,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<D>;
   constexpr int kStages = S::kStages;
   constexpr int KG = 4 / NRB;            // key groups: warps that share a row block
-  constexpr int NK = 16 * NRB;           // keys of a tile that a lane takes
+  constexpr int NK = 16 * NRB;           // keys of a tile that a thread takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* xbuf = reinterpret_cast<float*>(smem + S::kX);
@@ -324,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pv_done = p_full + 2;        // [2] O holds tile g
   uint64_t* info_full = pv_done + 2;     // [kInfo]
   uint64_t* fac_full = info_full + kInfo;   // [kSegs]
+  uint64_t* seg_full = fac_full + kSegs;    // [kSegRing]
+  Seg* ring = reinterpret_cast<Seg*>(smem + S::kRing);
   volatile int* rest = reinterpret_cast<volatile int*>(smem + S::kMisc);   // [kSegs] the third term of Q is needed
   volatile int* last_flag = rest + kSegs * 2;
   volatile int* abort = last_flag + 1;
@@ -352,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&p_full[i], 4);
       sm100::mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < kSegRing; ++i) sm100::mbar_init(&seg_full[i], 1);
     for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&info_full[i], 1);
     for (int i = 0; i < kSegs; ++i) sm100::mbar_init(&fac_full[i], 128);
     *abort = 0;
@@ -371,125 +402,138 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = sm100::smem_u32(smem);
 
-  const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
   // Registers: 128 a thread at launch; the softmax warps take what the others
   // leave (104 + 2 x 152 + 104 = 4 x 128).
-  Walk walk{p, t_begin, t_end, find_request(p.prefix, p.B, t_begin, lane)};
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {   // the whole warp
+    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort) ? 1 : 0) != 0;
+  };
+  // Segment sn, as the TMA warp announced it.
+  auto take = [&](int sn, Seg& seg) -> bool {
+    if (!wait(&seg_full[sn % kSegRing], (uint32_t)((sn / kSegRing) & 1))) return false;
+    seg = ring[sn % kSegRing];
+    return true;
+  };
   bool ok = true;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == 0) {
-    // ----------------------------------------------------------------- MMA
-    // The whole warp walks the tiles, so that the descriptors stay uniform,
-    // and one elected lane issues. It polls: S of tile g + 1 as soon as its
-    // keys are there (it runs during the softmax of tile g), P V of tile g as
-    // soon as its probabilities and values are.
     constexpr uint32_t kShape = (1u << 4) | ((uint32_t)(128 >> 4) << 24);   // fp32 D, M = 128
+    if (warp == 0) {
+    // ------------------------------------------------------------------- S
+    // S of each tile, as soon as its keys are there and P V of tile g - 2 is
+    // done with the buffer. (The whole warp walks the tiles, so that the
+    // descriptors stay uniform; one elected lane issues.)
     constexpr uint32_t idesc_qk = kShape | ((uint32_t)(kKeys >> 3) << 17);              // e4m3 x e4m3
     constexpr uint32_t idesc_rest = idesc_qk | (1u << 7);                               // e5m2 x e4m3
-    constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // V MN-major
     const uint64_t qd = desc_kmajor<D>(sbase + S::kQ), kd0 = desc_kmajor<D>(sbase + S::kK);
-    const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV);
-    Seg seg, qseg;
-    Walk qwalk = walk;                   // the tile whose S is issued next
-    bool have = walk.next(seg), qhave = qwalk.next(qseg);
-    int qg = 0, qi = 0, qs = 0, qstage = 0;   // its number, its index in qseg, qseg's number, its stage
-    uint32_t qphase = 0;
-    bool third = false;
-    auto done = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, sm100::mbar_test_wait(bar, parity)) != 0; };
-    auto try_qk = [&]() -> bool {        // false: not ready
-      if (!done(&k_full[qstage], qphase)) return false;
-      if (qi == 0) {
-        if (!done(q_full, (uint32_t)(qs & 1))) return false;
-        third = rest[qs % kSegs] != 0;
-      }
-      const bool last = qi + 1 == qseg.tiles();
-      sm100::tc_fence_after();
-      if (sm100::elect_one()) {
-        const uint32_t d = tmem + (qg & 1) * 128;
-        const uint64_t kd = kd0 + (uint64_t)(qstage * (S::kTile >> 4));
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, kk ? 1u : 0u);
-        if (third) {
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + (uint64_t)((S::kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_rest, 1u);
-        }
-        sm100::tc_commit(&s_full[qg & 1]);
-        sm100::tc_commit(&k_empty[qstage]);
-        if (last) sm100::tc_commit(q_empty);
-      }
-      __syncwarp();
-      ++qg;
-      if (++qstage == kStages) {
-        qstage = 0;
-        qphase ^= 1u;
-      }
-      if (last) {
-        qhave = qwalk.next(qseg);
-        qi = 0;
-        ++qs;
-      } else {
-        ++qi;
-      }
-      return true;
-    };
-    int g = 0, vstage = 0;
-    uint32_t vphase = 0;
-    for (; have && ok; have = walk.next(seg)) {
+    int g = 0, stage = 0;
+    uint32_t phase = 0;
+    Seg seg;
+    for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
       const int tiles = seg.tiles();
-      for (int i = 0; i < tiles && ok; ++i, ++g) {
-        const uint64_t start = sm100::globaltimer();
-        uint32_t spins = 0;
-        for (;;) {
-          if (qhave && qg <= g + 1 && try_qk()) continue;    // (P V of tile qg - 2 has been issued)
-          const int buf = g & 1;
-          if (qg > g && done(&p_full[buf], (uint32_t)((g >> 1) & 1)) && done(&v_ready[vstage], vphase)) {
-            sm100::tc_fence_after();
-            if (sm100::elect_one()) {
-              const uint64_t vd = vd0 + (uint64_t)(vstage * (S::kTile >> 4));
+      ok = wait(q_full, (uint32_t)(sn & 1));
+      if (!ok) break;
+      const bool third = rest[sn % kSegs] != 0;
+      for (int i = 0; i < tiles; ++i, ++g) {
+        const int buf = g & 1;
+        ok = wait(&k_full[stage], phase) && (g < 2 || wait(&pv_done[buf], (uint32_t)(((g - 2) >> 1) & 1)));
+        if (!ok) break;
+        sm100::tc_fence_after();
+        if (sm100::elect_one()) {
+          const uint32_t d = tmem + buf * 128;
+          const uint64_t kd = kd0 + (uint64_t)(stage * (S::kTile >> 4));
 #pragma unroll
-              for (int kk = 0; kk < kKeys / 32; ++kk)
-                mma_f8_ts(tmem + kColO + buf * 128, tmem + buf * 128 + kk * 8, vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv,
-                          (i > 1 || kk > 0) ? 1u : 0u);   // the first two tiles begin the two O
-              sm100::tc_commit(&pv_done[buf]);
-              sm100::tc_commit(&v_empty[vstage]);
-            }
-            __syncwarp();
-            if (++vstage == kStages) {
-              vstage = 0;
-              vphase ^= 1u;
-            }
-            break;
+          for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, kk ? 1u : 0u);
+          if (third) {
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + (uint64_t)((S::kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_rest, 1u);
           }
-          if ((++spins & 255u) == 0 && __any_sync(0xffffffffu, *abort || sm100::globaltimer() - start > sm100::kWaitTimeoutNs)) {
-            ok = false;
-            break;
-          }
+          sm100::tc_commit(&s_full[buf]);
+          sm100::tc_commit(&k_empty[stage]);
+          if (i + 1 == tiles) sm100::tc_commit(q_empty);
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
     if (!ok) {
       *abort = 1;
       if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
-      // MMAs in flight end before the shared memory and TMEM go (else the softmax warps have waited for every P V)
-      if (g > 0) sm100::mbar_wait_timeout(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), sm100::kWaitTimeoutNs);
+      // MMAs in flight end before the shared memory and TMEM go (else the softmax warps have waited for every one)
+      if (g > 0) sm100::mbar_wait_timeout(&s_full[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), sm100::kWaitTimeoutNs);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp >= 2) {
+    // ----------------------------------------------------------------- P V
+    // Warp 2 + wg: the tiles of softmax group wg, into its O.
+    constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // V MN-major
+    const int wg = warp - 2;
+    const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV);
+    int g = 0, stage = 0, last_g = -1;
+    uint32_t phase = 0;
+    Seg seg;
+    for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
+      const int tiles = seg.tiles();
+      for (int i = 0; i < tiles; ++i, ++g) {
+        if ((g & 1) != wg) {
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          continue;
+        }
+        last_g = g;
+        ok = wait(&v_ready[stage], phase) && wait(&p_full[wg], (uint32_t)((g >> 1) & 1));
+        if (!ok) break;
+        sm100::tc_fence_after();
+        if (sm100::elect_one()) {
+          const uint64_t vd = vd0 + (uint64_t)(stage * (S::kTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            mma_f8_ts(tmem + kColO + wg * 128, tmem + wg * 128 + kk * 8, vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv,
+                      (i > 1 || kk > 0) ? 1u : 0u);        // the first two tiles begin the two O
+          sm100::tc_commit(&pv_done[wg]);
+          sm100::tc_commit(&v_empty[stage]);
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
+      // (the last product may have been issued or not; a short wait either way)
+      if (last_g >= 0) sm100::mbar_wait_timeout(&pv_done[wg], (uint32_t)((last_g >> 1) & 1), 1000000);
+    }
+    __syncwarp();
+  } else {
     // ----------------------------------------------------------------- TMA
     const uint64_t pol = sm100::l2_policy_evict_first();
     if (lane == 0) {
       sm100::tma_prefetch_desc(&tm_k);
       sm100::tma_prefetch_desc(&tm_v);
     }
+    const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
+    Walk walk{p, t_begin, t_end, find_request(p.prefix, p.B, t_begin, lane)};
     int g = 0;
     Seg seg;
-    while (ok && walk.next(seg)) {
+    for (int sn = 0; ok; ++sn) {
+      if (!walk.next(seg)) seg.n = 0;
+      if (lane == 0) {
+        ring[sn % kSegRing] = seg;
+        sm100::mbar_arrive(&seg_full[sn % kSegRing]);
+      }
+      if (seg.n == 0) break;
       const PageSpan span = page_span(seg.ctx, p.R, p.window, p.sinks);
       for (int i = seg.i0; i < seg.i1 && ok; i += kWarp) {
         int blk = -1, page = -1;
-        float sk = 1.0f, lsv = 0.0f, isv = 1.0f;
+        float sk = 1.0f, lsv = 0.0f;
         if (i + lane < seg.i1) {
           page = span.page(i + lane);
           blk = p.block_table[(int64_t)seg.b * p.max_blocks + page];
@@ -505,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               sk = 1.0f;
             } else {
               lsv = log2f(sv);
-              isv = 1.0f / sv;
               if (!page_whole(p, page, seg.ctx)) page = -2 - page;
             }
           }
@@ -517,16 +560,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {        // (lane 31 of an odd rest has page -1)
             id[y] = __shfl_sync(0xffffffffu, blk, x + y);
-            in.page[y] = __shfl_sync(0xffffffffu, page, x + y);
-            in.sk[y] = __shfl_sync(0xffffffffu, sk, x + y);
-            in.lsv[y] = __shfl_sync(0xffffffffu, lsv, x + y);
-            in.isv[y] = __shfl_sync(0xffffffffu, isv, x + y);
+            in.page[y].mark = __shfl_sync(0xffffffffu, page, x + y);
+            in.page[y].sk = __shfl_sync(0xffffffffu, sk, x + y);
+            in.page[y].lsv = __shfl_sync(0xffffffffu, lsv, x + y);
           }
           int go = 1;
           if (lane == 0) {
             const int s = g % kStages;
             const uint32_t parity = (uint32_t)((g / kStages) & 1) ^ 1u;
-            const uint32_t bytes = ((in.page[0] != -1) + (in.page[1] != -1)) * (uint32_t)(S::kTile / 2);
+            const uint32_t bytes = ((in.page[0].mark != -1) + (in.page[1].mark != -1)) * (uint32_t)(S::kTile / 2);
             go = sm100::mbar_wait(&k_empty[s], parity, abort);
             if (go) {
               info[g % kInfo] = in;
@@ -535,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               else sm100::mbar_arrive(&k_full[s]);
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                if (in.page[y] != -1)
+                if (in.page[y].mark != -1)
                   sm100::tma_load_4d(smem + S::kK + s * S::kTile + y * (S::kTile / 2), &tm_k, &k_full[s], 0, kvh, 0, id[y], pol);
               go = sm100::mbar_wait(&v_empty[s], parity, abort);
             }
@@ -544,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               else sm100::mbar_arrive(&v_full[s]);
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                if (in.page[y] != -1)
+                if (in.page[y].mark != -1)
                   sm100::tma_load_4d(smem + S::kV + s * S::kTile + y * (S::kTile / 2), &tm_v, &v_full[s], 0, kvh, 0, id[y], pol);
             } else {
               *abort = 1;
@@ -580,15 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------- softmax and output
     const int w = warp & 3, wg = (warp >> 2) - 1, st = threadIdx.x - 128;
     const int rb = w % NRB, kg = w / NRB, half = lane >> 4, r16 = lane & 15;
-    const int page_half = (kg * 2 + half) * NK / kBlock;   // which page of a tile the lane's keys are in
-    const int in_page = (kg * 2 + half) * NK % kBlock;
+    const int page_half = (kg * 2 + half) * NK / kBlock, in_page = (kg * 2 + half) * NK % kBlock;   // the thread's keys
     const int row = row_tile * 64 + rb * 16 + r16;
     const int j = min(row, p.rows - 1) / p.group;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + wg * 128, lanes_lo = lanes + (16u << 16);
+    const uint32_t quarter = tmem + ((uint32_t)(32 * w) << 16);
+    const uint32_t o_hi = quarter + kColO + wg * 128, o_lo = o_hi + (16u << 16);
+    const uint32_t s_hi = quarter + wg * 128, s_lo = s_hi + (16u << 16);
     auto soft_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     int g = 0;
     Seg seg;
-    for (int sn = 0; walk.next(seg); ++sn) {
+    for (int sn = 0; (ok = barrier_all<1, 256>(ok && take(sn, seg))) && seg.n != 0; ++sn) {
       const int tiles = seg.tiles(), pos = seg.ctx + j;
       const int low = p.window == 0 ? 0 : pos - p.window + 1;
       ok = ok && __all_sync(0xffffffffu, sm100::mbar_wait(&fac_full[sn % kSegs], (uint32_t)((sn / kSegs) & 1), abort) ? 1 : 0);
@@ -599,41 +642,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool begun = false;                                  // O holds something
       const int g_end = g + tiles;
       for (g += (g ^ wg) & 1; g < g_end; g += 2) {         // this group's tiles
-        ok = ok && __all_sync(0xffffffffu, (sm100::mbar_wait(&info_full[g % kInfo], (uint32_t)((g / kInfo) & 1), abort) &&
-                                            sm100::mbar_wait(&s_full[wg], (uint32_t)((g >> 1) & 1), abort))
-                                               ? 1
-                                               : 0);
+        ok = ok && wait(&info_full[g % kInfo], (uint32_t)((g / kInfo) & 1)) && wait(&s_full[wg], (uint32_t)((g >> 1) & 1));
         if (!ok) break;                                    // the segment's end still meets the others
         sm100::tc_fence_after();
+        const PageInfo in = info[g % kInfo].page[page_half];
         float x[NK];
         {
           constexpr int N = NK < 32 ? NK : 32;
 #pragma unroll
           for (int k0 = 0; k0 < NK; k0 += N) {
             float y[N];
-            ld_halves<N, NK>(lanes + kg * 2 * NK + k0, x + k0);
-            ld_halves<N, NK>(lanes_lo + kg * 2 * NK + k0, y);
+            ld_halves<N, NK>(s_hi + kg * 2 * NK + k0, x + k0);
+            ld_halves<N, NK>(s_lo + kg * 2 * NK + k0, y);
             sm100::tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < N; ++k) x[k0 + k] += y[k];
           }
         }
-        const float sk = info[g % kInfo].sk[page_half], lsv = info[g % kInfo].lsv[page_half];
-        const float isv = info[g % kInfo].isv[page_half];
-        const int mark = info[g % kInfo].page[page_half];
-        if (__any_sync(0xffffffffu, mark < 0)) {
+        const int mark = in.mark;
+        if (mark < 0) {
           const int slot = (mark < 0 ? -2 - mark : mark) * kBlock + in_page, top = mark == -1 ? INT_MIN : pos;
 #pragma unroll
           for (int k = 0; k < NK; ++k)
             if (!(slot + k <= top && (slot + k >= low || slot + k < p.sinks))) x[k] = -INFINITY;
         }
         // (a factor of 0 would turn a hidden -inf into NaN; scores that small are 0 all the same)
-        const float f = fmaxf(row_fac * sk, 1e-36f);
+        const float f = fmaxf(row_fac * in.sk, 1e-36f);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int k = 0; k < NK; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
         const float score = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-        float most = score + lsv, highest = score;
+        float most = score + in.lsv, highest = score;
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));   // with the row's other half
         highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, 16));
         if (highest > lref + 20.0f) {
@@ -641,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lref = highest;
         }
         // (a row with nothing visible in the tile stays as it is)
-        const float to = fmaxf(most - kNominalP, top_ref - kDown);
+        const float to = fmaxf(most - (ref == -INFINITY ? kFirstP : most > ref ? kUpP : kDownP), top_ref - kDown);
         const bool low = most < ref + kLeastP && most != -INFINITY;
         low_tiles = low ? low_tiles + 1 : 0;
         const bool move = most > ref + kMostP || (low_tiles >= kLowTiles && to < ref - 1.0f);
@@ -649,24 +688,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float c = !move ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - to);
           if (move) ref = to;
           top_ref = fmaxf(top_ref, ref);
-          if (begun) {
-#pragma unroll 1
+          if (begun) {                                     // (S of tile g came after P V of tile g - 2)
+#pragma unroll 2
             for (int q = 0; q < D / 32; ++q) {               // this thread's half of the row's dims, 16 at a time
               float o[16], o2[16];
-              ld_halves<16, D / 2>(lanes + kColO + q * 16, o);
-              ld_halves<16, D / 2>(lanes_lo + kColO + q * 16, o2);
+              ld_halves<16, D / 2>(o_hi + q * 16, o);
+              ld_halves<16, D / 2>(o_lo + q * 16, o2);
               sm100::tmem_ld_wait();
               uint32_t r[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * c);
-              st_halves<16, D / 2>(lanes + kColO + q * 16, r);
+              st_halves<16, D / 2>(o_hi + q * 16, r);
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o2[k] * c);
-              st_halves<16, D / 2>(lanes_lo + kColO + q * 16, r);
+              st_halves<16, D / 2>(o_lo + q * 16, r);
             }
           }
         }
-        const float shift = lsv - (ref == -INFINITY ? 0.0f : ref);
+        const float shift = in.lsv - (ref == -INFINITY ? 0.0f : ref);
         float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t hi[NK / 4], lo[NK / 4];
 #pragma unroll
@@ -682,24 +721,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (KG > 1) {                            // columns of the other warps' keys
           const uint32_t z[NK / 4] = {};
 #pragma unroll
-          for (int y = 0; y < KG; ++y) {
-            if (y == kg) continue;
-            st_halves<NK / 4, NK / 4>(lanes + y * (NK / 2), z);
-            st_halves<NK / 4, NK / 4>(lanes_lo + y * (NK / 2), z);
+          for (int y = 1; y < KG; ++y) {
+            const int other = (kg + y) % KG * (NK / 2);
+            st_halves<NK / 4, NK / 4>(s_hi + other, z);
+            st_halves<NK / 4, NK / 4>(s_lo + other, z);
           }
         }
-        st_halves<NK / 4, NK / 4>(lanes + kg * (NK / 2), hi);
-        st_halves<NK / 4, NK / 4>(lanes_lo + kg * (NK / 2), lo);
-        begun = true;
+        st_halves<NK / 4, NK / 4>(s_hi + kg * (NK / 2), hi);
+        st_halves<NK / 4, NK / 4>(s_lo + kg * (NK / 2), lo);
         tmem_st_wait();
         sm100::tc_fence_before();
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&p_full[wg]);
+        begun = true;
       }
       // ---- the request's part is done: join the lanes of each row
       g = g_end;
       const int last_g = g - 1 - ((g - 1 - wg) & 1);       // this group's last tile so far
-      ok = ok && (!begun || __all_sync(0xffffffffu, sm100::mbar_wait(&pv_done[wg], (uint32_t)((last_g >> 1) & 1), abort) ? 1 : 0));
+      ok = ok && (!begun || wait(&pv_done[wg], (uint32_t)((last_g >> 1) & 1)));
       sm100::tc_fence_after();
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       if (half == 0) red[(wg * 4 + w) * 16 + r16] = make_float2(lref, sum);
@@ -745,8 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D / 32; ++c) {                       // 16 dims of each half of the row
         float y[16], y2[16];
         if (ok) {
-          ld_halves<16, D / 2>(lanes + kColO + c * 16, y);
-          ld_halves<16, D / 2>(lanes_lo + kColO + c * 16, y2);
+          ld_halves<16, D / 2>(o_hi + c * 16, y);
+          ld_halves<16, D / 2>(o_lo + c * 16, y2);
           sm100::tmem_ld_wait();
         }
         const int dim0 = half * (D / 2) + c * 16;
@@ -830,7 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0, g = 0;
     uint32_t phase = 0;
     Seg seg;
-    for (int sn = 0; ok && walk.next(seg); ++sn) {
+    for (int sn = 0;; ++sn) {
+      if (threadIdx.x == 384) rest[sn % kSegs] = 0;
+      ok = barrier_all<2, 128>(ok && take(sn, seg));
+      if (!ok || seg.n == 0) break;
       uint4 w[NRB][kVec];
 #pragma unroll
       for (int rb = 0; rb < NRB; ++rb) {
@@ -840,9 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int v = 0; v < kVec; ++v) w[rb][v] = __ldg(src + v);
       }
-      if (threadIdx.x == 384) rest[sn % kSegs] = 0;
       ok = __all_sync(0xffffffffu, sm100::mbar_wait(q_empty, (uint32_t)((sn & 1) ^ 1), abort) ? 1 : 0);
-      asm volatile("bar.sync 2, 128;" ::: "memory");
       bool need = false;
 #pragma unroll
       for (int rb = 0; rb < NRB; ++rb) {
@@ -916,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                ? 1
                                                : 0);
         if (!ok) break;
-        const int mark = info[g % kInfo].page[cw >> 1];
+        const int mark = info[g % kInfo].page[cw >> 1].mark;
         if (mark < 0) {                  // some of its slots are hidden, or nothing was loaded
           uint8_t* v = smem + S::kV + s * S::kTile;
           for (int x = lane; x < 32 * (D / 16); x += kWarp) {

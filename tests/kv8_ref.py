@@ -75,7 +75,7 @@ def visible(t, p, window, sinks):
 def attention(q, k_rows, v_rows, ctx, sm_scale, window, sinks):
     """One request: q [R, Hq, d], k_rows / v_rows(t) -> [len(t), Hkv, d]; float64 [R, Hq, d]. Also, for error bounds,
     sum_t p_t |v_t| of every output, the largest sum |q k| sm_scale of every row, and sum_t m_t |v_t| of every output
-    with m_t the largest p within 127 visible slots of t."""
+    with m_t the largest p within 767 visible slots of t."""
     R, Hq, d = q.shape
     t = np.arange(ctx + R)
     t = t[visible(t, ctx, window, sinks) | (t > ctx)]
@@ -90,7 +90,7 @@ def attention(q, k_rows, v_rows, ctx, sm_scale, window, sinks):
             w = np.exp(x - x.max())
             w /= w.sum()
             out[j, h], absolute[j, h] = w @ vh, w @ np.abs(vh)
-            wide = np.lib.stride_tricks.sliding_window_view(np.pad(w, 127), 255).max(axis=1)
+            wide = np.lib.stride_tricks.sliding_window_view(np.pad(w, 767), 1535).max(axis=1)
             near[j, h] = wide @ np.abs(vh)
             score[j, h] = (np.abs(kh) @ np.abs(qh)).max() * sm_scale
     return out, absolute, score, near

@@ -155,10 +155,10 @@ def bound(t, kv8, d, n, ref, absolute, score, near):
       fp32 rows 0; bf16 cache 2^-8 (bf16);
       8-bit cache 2^-8 + 2^-11: p = hi + lo / 16 with e4m3 hi and lo, each off by at most 2^-4 of what it rounds (2^-4
       2^-4), after a rounding to f16 (2^-11). Below e4m3's normal numbers lo is off by half a step of 2^-9, over 16:
-      2^-14, where the largest p of a tile's keys of the row is kept at 2^-2 or more: 2^-12 of that largest one, which
-      is within 127 visible slots of the key."""
+      2^-14, where the largest p of a row's keys in a tile of 128 is 2^-4 or more at least in each fifth tile: 2^-10 of
+      the largest one within 767 visible slots of the key."""
     p_eps = 0.0 if t == "f32" else 2.0 ** -8 + 2.0 ** -11 if kv8 else 2.0 ** -8
-    floor = 2.0 ** -12 * near if kv8 and t == "bf16" else 0.0
+    floor = 2.0 ** -10 * near if kv8 and t == "bf16" else 0.0
     # |ref| <= absolute, so every relative change of p counts at most twice
     return EPS[t] * np.abs(ref) * 1.01 + (p_eps + 2 * (d + 8) * 2.0 ** -23 * np.maximum(score, 1.0) + 2 * n * 2.0 ** -23) * absolute + floor
 
