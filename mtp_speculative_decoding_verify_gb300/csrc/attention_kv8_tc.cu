@@ -44,9 +44,9 @@
 // There V's bytes that are NaN become 0 in shared memory (0 x NaN), and a
 // bitmap of (verify token, dim) puts NaN back into the rows that do see them.
 //
-// Warps: 0 S = Q K^T, 1 TMA (block ids and scales of 32 pages at a time, one a
-// lane), 2 and 3 P V (with polling for all three products in one warp, its
-// checks were the slowest part of a tile), 4-11 softmax and output, 12-15 masked V and the next request's Q.
+// Warps: 0 and 1 MMA issue, 2 TMA (block ids and scales of 32 pages at a time,
+// one a lane), 4-11 softmax and output, 12-15 masked V and the next request's
+// Q. (One polling warp for all products was the slowest part of a tile.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <limits.h>
@@ -83,9 +83,12 @@ constexpr uint32_t kColO = 256;        // S (and P) buffers at columns 0 and 128
 template <int D>
 struct Smem {
   static constexpr int kTile = kKeys * D;                 // bytes of K or V of a tile
-  static constexpr int kStages = D == 128 ? 5 : 6;
-  static constexpr int kK = 0, kV = kK + kStages * kTile;
-  static constexpr int kQ = kV + kStages * kTile;         // hi and lo, rest
+  // Even: a stage then serves tiles of one softmax group only, whose MMA warp meets its phases one after the other (a
+  // wait's parity tells only two apart).
+  // V is held longer (to P V, two tiles behind S).
+  static constexpr int kKStages = D == 128 ? 4 : 6, kVStages = 6;
+  static constexpr int kK = 0, kV = kK + kKStages * kTile;
+  static constexpr int kQ = kV + kVStages * kTile;         // hi and lo, rest
   static constexpr int kX = kQ + 2 * kTile;               // join of a row's partial results: [8 warps][16][36] floats
   static constexpr int kRed = kX + 128 * 36 * 4;          // [8 warps][16] (maximum, sum)
   static constexpr int kInfoOff = kRed + 128 * 8;         // [kInfo] TileInfo
@@ -93,7 +96,7 @@ struct Smem {
   static constexpr int kFac = kRing + kSegRing * 32;      // [kSegs][64] factors of the rows' scores
   static constexpr int kNan = kFac + kSegs * 64 * 4;      // [kNanSegs][16][4] words
   static constexpr int kBar = kNan + kNanSegs * 16 * 4 * 4;
-  static constexpr int kBars = 5 * kStages + 2 + 2 + 2 + 2 + kInfo + kSegs + kSegRing;
+  static constexpr int kBars = 2 * kKStages + 3 * kVStages + 2 + 2 + 2 + 2 + kInfo + kSegs + kSegRing;
   static constexpr int kMisc = kBar + kBars * 8;          // rest flags [kSegs][2], join flag, abort, TMEM base
   static constexpr int kBytes = kMisc + kSegs * 8 + 16 + 1024;
   // byte offset of 16-byte chunk c of row r of a K-major operand tile, as TMA swizzles it
@@ -123,6 +126,19 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// (a, b) += (c, d) and (a, b) = (a, b) f + g as one instruction each.
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n  .reg .b64 p, q;\n  mov.b64 p, {%0, %1};\n  mov.b64 q, {%2, %3};\n  add.rn.f32x2 p, p, q;\n  mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void fma2(float& a, float& b, float f, float g) {
+  asm("{\n  .reg .b64 p, q, r;\n  mov.b64 p, {%0, %1};\n  mov.b64 q, {%2, %2};\n  mov.b64 r, {%3, %3};\n"
+      "  fma.rn.f32x2 p, p, q, r;\n  mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(f), "f"(g));
 }
 
 // Four probabilities (at most 2^8) as e4m3 terms: hi, and lo = 16 (p - hi).
@@ -330,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const WindowParams p) {
   using S = Smem<D>;
-  constexpr int kStages = S::kStages;
+  constexpr int kKStages = S::kKStages, kVStages = S::kVStages;
   constexpr int KG = 4 / NRB;            // key groups: warps that share a row block
   constexpr int NK = 16 * NRB;           // keys of a tile that a thread takes
   extern __shared__ uint8_t smem_raw[];
@@ -341,11 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* fac = reinterpret_cast<float*>(smem + S::kFac);
   uint32_t* nanmap = reinterpret_cast<uint32_t*>(smem + S::kNan);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kBar);
-  uint64_t* k_empty = k_full + kStages;
-  uint64_t* v_full = k_empty + kStages;
-  uint64_t* v_ready = v_full + kStages;  // masked bytes have been dealt with
-  uint64_t* v_empty = v_ready + kStages;
-  uint64_t* q_full = v_empty + kStages;  // Q of the next request is in place
+  uint64_t* k_empty = k_full + kKStages;
+  uint64_t* v_full = k_empty + kKStages;
+  uint64_t* v_ready = v_full + kVStages;  // masked bytes have been dealt with
+  uint64_t* v_empty = v_ready + kVStages;
+  uint64_t* q_full = v_empty + kVStages;  // Q of the next request is in place
   uint64_t* q_empty = q_full + 1;        // the last S of a request is done
   uint64_t* s_full = q_full + 2;         // [2] S of tile g is there, and so O of tile g - 2
   uint64_t* p_full = s_full + 2;         // [2] P of tile g has replaced S
@@ -368,15 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (g_cta >= G) return;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kKStages; ++s) {
       sm100::mbar_init(&k_full[s], 1);
       sm100::mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
       sm100::mbar_init(&v_full[s], 1);
       sm100::mbar_init(&v_ready[s], 4);
       sm100::mbar_init(&v_empty[s], 1);
     }
     sm100::mbar_init(q_full, 128);
-    sm100::mbar_init(q_empty, 1);
+    sm100::mbar_init(q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&s_full[i], 1);
       sm100::mbar_init(&p_full[i], 4);
@@ -418,101 +436,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     constexpr uint32_t kShape = (1u << 4) | ((uint32_t)(128 >> 4) << 24);   // fp32 D, M = 128
-    if (warp == 0) {
-    // ------------------------------------------------------------------- S
-    // S of each tile, as soon as its keys are there and P V of tile g - 2 is
-    // done with the buffer. (The whole warp walks the tiles, so that the
-    // descriptors stay uniform; one elected lane issues.)
+    if (warp < 2) {
+    // ---------------------------------------------------------------- MMA
+    // Warp wg issues the products of softmax group wg's tiles: P V of one,
+    // then, once that has read P, S of the next into the same buffer. (The whole warp walks the tiles, so that the descriptors stay
+    // uniform; one elected lane issues.)
     constexpr uint32_t idesc_qk = kShape | ((uint32_t)(kKeys >> 3) << 17);              // e4m3 x e4m3
     constexpr uint32_t idesc_rest = idesc_qk | (1u << 7);                               // e5m2 x e4m3
+    constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // V MN-major
+    const int wg = warp;
     const uint64_t qd = desc_kmajor<D>(sbase + S::kQ), kd0 = desc_kmajor<D>(sbase + S::kK);
-    int g = 0, stage = 0;
-    uint32_t phase = 0;
+    const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV);
+    int pv_g = -1;                       // the tile whose P V is next (its S has been issued), -1: none
+    bool pv_first = false;               // it begins O
+    auto do_pv = [&]() -> bool {
+      const int pv_stage = pv_g % kVStages;
+      if (!wait(&v_ready[pv_stage], (uint32_t)((pv_g / kVStages) & 1)) || !wait(&p_full[wg], (uint32_t)((pv_g >> 1) & 1))) return false;
+      sm100::tc_fence_after();
+      if (sm100::elect_one()) {
+        const uint64_t vd = vd0 + (uint64_t)(pv_stage * (S::kTile >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 32; ++kk)
+          mma_f8_ts(tmem + kColO + wg * 128, tmem + wg * 128 + kk * 8, vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv,
+                    (!pv_first || kk > 0) ? 1u : 0u);
+        sm100::tc_commit(&pv_done[wg]);
+        sm100::tc_commit(&v_empty[pv_stage]);
+      }
+      __syncwarp();
+      return true;
+    };
+    int g = 0;
     Seg seg;
     for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
       const int tiles = seg.tiles();
-      ok = wait(q_full, (uint32_t)(sn & 1));
-      if (!ok) break;
-      const bool third = rest[sn % kSegs] != 0;
-      for (int i = 0; i < tiles; ++i, ++g) {
-        const int buf = g & 1;
-        ok = wait(&k_full[stage], phase) && (g < 2 || wait(&pv_done[buf], (uint32_t)(((g - 2) >> 1) & 1)));
-        if (!ok) break;
-        sm100::tc_fence_after();
-        if (sm100::elect_one()) {
-          const uint32_t d = tmem + buf * 128;
-          const uint64_t kd = kd0 + (uint64_t)(stage * (S::kTile >> 4));
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, kk ? 1u : 0u);
-          if (third) {
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + (uint64_t)((S::kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_rest, 1u);
+      const int mine = (tiles + ((g ^ wg ^ 1) & 1)) / 2;   // this group's tiles of the segment
+      if (mine == 0) {                   // (every Q is waited for: a parity tells only two phases apart)
+        if (pv_g >= 0) ok = do_pv();
+        pv_g = -1;
+        if (!ok || !(ok = wait(q_full, (uint32_t)(sn & 1)))) break;
+        if (lane == 0) sm100::mbar_arrive(q_empty);
+      }
+      bool third = false;
+      for (int i = 0, m = 0; i < tiles; ++i, ++g) {
+        if ((g & 1) == wg) {
+          const int stage = g % kKStages;
+          if (pv_g >= 0 && !(ok = do_pv())) break;
+          if (m == 0) {
+            ok = wait(q_full, (uint32_t)(sn & 1));
+            third = rest[sn % kSegs] != 0;
           }
-          sm100::tc_commit(&s_full[buf]);
-          sm100::tc_commit(&k_empty[stage]);
-          if (i + 1 == tiles) sm100::tc_commit(q_empty);
-        }
-        __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+          ok = ok && wait(&k_full[stage], (uint32_t)((g / kKStages) & 1)) && (g < 2 || wait(&pv_done[wg], (uint32_t)(((g - 2) >> 1) & 1)));
+          if (!ok) break;
+          sm100::tc_fence_after();
+          if (sm100::elect_one()) {
+            const uint32_t d = tmem + wg * 128;
+            const uint64_t kd = kd0 + (uint64_t)(stage * (S::kTile >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, kk ? 1u : 0u);
+            if (third) {
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + (uint64_t)((S::kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_rest, 1u);
+            }
+            sm100::tc_commit(&s_full[wg]);
+            sm100::tc_commit(&k_empty[stage]);
+            if (m + 1 == mine) sm100::tc_commit(q_empty);
+          }
+          __syncwarp();
+          pv_g = g;
+          pv_first = m == 0;
+          ++m;
         }
       }
     }
+    if (ok && pv_g >= 0) ok = do_pv();
     if (!ok) {
       *abort = 1;
       if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
       // MMAs in flight end before the shared memory and TMEM go (else the softmax warps have waited for every one)
-      if (g > 0) sm100::mbar_wait_timeout(&s_full[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), sm100::kWaitTimeoutNs);
-    }
-    __syncwarp();
-  } else if (warp >= 2) {
-    // ----------------------------------------------------------------- P V
-    // Warp 2 + wg: the tiles of softmax group wg, into its O.
-    constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // V MN-major
-    const int wg = warp - 2;
-    const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV);
-    int g = 0, stage = 0, last_g = -1;
-    uint32_t phase = 0;
-    Seg seg;
-    for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
-      const int tiles = seg.tiles();
-      for (int i = 0; i < tiles; ++i, ++g) {
-        if ((g & 1) != wg) {
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          continue;
-        }
-        last_g = g;
-        ok = wait(&v_ready[stage], phase) && wait(&p_full[wg], (uint32_t)((g >> 1) & 1));
-        if (!ok) break;
-        sm100::tc_fence_after();
-        if (sm100::elect_one()) {
-          const uint64_t vd = vd0 + (uint64_t)(stage * (S::kTile >> 4));
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk)
-            mma_f8_ts(tmem + kColO + wg * 128, tmem + wg * 128 + kk * 8, vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv,
-                      (i > 1 || kk > 0) ? 1u : 0u);        // the first two tiles begin the two O
-          sm100::tc_commit(&pv_done[wg]);
-          sm100::tc_commit(&v_empty[stage]);
-        }
-        __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      if (pv_g >= 0) {
+        sm100::mbar_wait_timeout(&s_full[wg], (uint32_t)((pv_g >> 1) & 1), 1000000);
+        sm100::mbar_wait_timeout(&pv_done[wg], (uint32_t)((pv_g >> 1) & 1), 1000000);
       }
     }
-    if (!ok) {
-      *abort = 1;
-      if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
-      // (the last product may have been issued or not; a short wait either way)
-      if (last_g >= 0) sm100::mbar_wait_timeout(&pv_done[wg], (uint32_t)((last_g >> 1) & 1), 1000000);
-    }
     __syncwarp();
-  } else {
+  } else if (warp == 2) {
     // ----------------------------------------------------------------- TMA
     const uint64_t pol = sm100::l2_policy_evict_first();
     if (lane == 0) {
@@ -566,10 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           int go = 1;
           if (lane == 0) {
-            const int s = g % kStages;
-            const uint32_t parity = (uint32_t)((g / kStages) & 1) ^ 1u;
+            const int s = g % kKStages, vs = g % kVStages;
             const uint32_t bytes = ((in.page[0].mark != -1) + (in.page[1].mark != -1)) * (uint32_t)(S::kTile / 2);
-            go = sm100::mbar_wait(&k_empty[s], parity, abort);
+            go = sm100::mbar_wait(&k_empty[s], (uint32_t)((g / kKStages) & 1) ^ 1u, abort);
             if (go) {
               info[g % kInfo] = in;
               sm100::mbar_arrive(&info_full[g % kInfo]);
@@ -579,15 +585,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int y = 0; y < 2; ++y)
                 if (in.page[y].mark != -1)
                   sm100::tma_load_4d(smem + S::kK + s * S::kTile + y * (S::kTile / 2), &tm_k, &k_full[s], 0, kvh, 0, id[y], pol);
-              go = sm100::mbar_wait(&v_empty[s], parity, abort);
+              go = sm100::mbar_wait(&v_empty[vs], (uint32_t)((g / kVStages) & 1) ^ 1u, abort);
             }
             if (go) {
-              if (bytes) sm100::mbar_arrive_expect_tx(&v_full[s], bytes);
-              else sm100::mbar_arrive(&v_full[s]);
+              if (bytes) sm100::mbar_arrive_expect_tx(&v_full[vs], bytes);
+              else sm100::mbar_arrive(&v_full[vs]);
 #pragma unroll
               for (int y = 0; y < 2; ++y)
                 if (in.page[y].mark != -1)
-                  sm100::tma_load_4d(smem + S::kV + s * S::kTile + y * (S::kTile / 2), &tm_v, &v_full[s], 0, kvh, 0, id[y], pol);
+                  sm100::tma_load_4d(smem + S::kV + vs * S::kTile + y * (S::kTile / 2), &tm_v, &v_full[vs], 0, kvh, 0, id[y], pol);
             } else {
               *abort = 1;
               raise_error(p.err, MTP_ERR_TIMEOUT);
@@ -599,22 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // Every copy issued lands before the CTA may exit: the last fill of each
-    // stage (after a timeout the K copy of tile g may be on its way too).
+    // stage (after a timeout the K copy of tile g may be on its way too; each
+    // wait is bounded).
     if (lane == 0) {
       const int nk = ok ? g : g + 1;
-      for (int s = 0; s < kStages; ++s) {
-        const int fills = g > s ? (g - 1 - s) / kStages + 1 : 0;
-        const int kfills = nk > s ? (nk - 1 - s) / kStages + 1 : 0;
-        if (ok) {
-          if (fills) {
-            sm100::mbar_wait_timeout(&k_full[s], (uint32_t)((fills - 1) & 1), sm100::kWaitTimeoutNs);
-            sm100::mbar_wait_timeout(&v_full[s], (uint32_t)((fills - 1) & 1), sm100::kWaitTimeoutNs);
-          }
-        } else {
-          if (fills) sm100::mbar_wait_timeout(&v_full[s], (uint32_t)((fills - 1) & 1), 1000000);
-          if (kfills) sm100::mbar_wait_timeout(&k_full[s], (uint32_t)((kfills - 1) & 1), 1000000);
-        }
-      }
+      for (int x = max(0, nk - kKStages); x < nk; ++x)
+        sm100::mbar_wait_timeout(&k_full[x % kKStages], (uint32_t)((x / kKStages) & 1), ok ? sm100::kWaitTimeoutNs : 1000000);
+      for (int x = max(0, g - kVStages); x < g; ++x)
+        sm100::mbar_wait_timeout(&v_full[x % kVStages], (uint32_t)((x / kVStages) & 1), ok ? sm100::kWaitTimeoutNs : 1000000);
     }
     }
   } else if (warp < 12) {
@@ -656,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ld_halves<N, NK>(s_lo + kg * 2 * NK + k0, y);
             sm100::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < N; ++k) x[k0 + k] += y[k];
+            for (int k = 0; k < N; k += 2) add2(x[k0 + k], x[k0 + k + 1], y[k], y[k + 1]);
           }
         }
         const int mark = in.mark;
@@ -710,10 +708,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t hi[NK / 4], lo[NK / 4];
 #pragma unroll
         for (int k = 0; k < NK; k += 4) {
-          const float a = ex2(fmaf(x[k], f, shift)), b = ex2(fmaf(x[k + 1], f, shift));
-          const float c = ex2(fmaf(x[k + 2], f, shift)), d = ex2(fmaf(x[k + 3], f, shift));
-          add[0] += a, add[1] += b, add[2] += c, add[3] += d;
-          split4(a, b, c, d, hi[k / 4], lo[k / 4]);
+          fma2(x[k], x[k + 1], f, shift);
+          fma2(x[k + 2], x[k + 3], f, shift);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[k + e] = ex2(x[k + e]);
+          add2(add[0], add[1], x[k], x[k + 1]);
+          add2(add[2], add[3], x[k + 2], x[k + 3]);
+          split4(x[k], x[k + 1], x[k + 2], x[k + 3], hi[k / 4], lo[k / 4]);
         }
         // 2^(score - lref) in sum: without the scale of V
         if (lref != -INFINITY) sum += ((add[0] + add[1]) + (add[2] + add[3])) * ex2(-shift - lref);
@@ -979,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&v_ready[s]);
-        if (++s == kStages) {
+        if (++s == kVStages) {
           s = 0;
           phase ^= 1u;
         }
