@@ -5,7 +5,6 @@ contiguity, their raw pointers go into the C argument structs, and every step
 of the verify path runs in the library's CUDA kernels. There is no CPU
 fallback: if the library is missing, loading it raises.
 """
-import contextlib
 import ctypes
 import os
 
@@ -408,28 +407,52 @@ def kv_rollback(block_table, seq_lens, num_accepted, free_list, free_count, *, D
     _check(lib().kv_rollback(ctypes.byref(a), _stream_handle(stream)))
 
 
-def _same_device(first, *tensors):
-    """The CUDA device that all the tensors are on."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError("the tensors must be CUDA tensors")
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError("tensors on %s and %s in one call" % (dev, t.device))
-    return dev
+def _refuse(t, name, index, dtype, shape):
+    """Say what is wrong with one tensor argument of a call."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != index:
+        raise ValueError("%s is on cuda:%d, the call's first tensor on cuda:%d" % (name, t.get_device(), index))
+    _dev(t, name, dtype, shape)
 
 
-def _launch(dev, stream, call):
-    """call(stream handle) with the tensors' device current, on `stream` or that device's current one.
-    The workspace that a call allocates meanwhile belongs to that stream, so that no other call shares it."""
-    with contextlib.ExitStack() as stack:
-        if torch.cuda.current_device() != dev.index:
-            stack.enter_context(torch.cuda.device(dev))
-        if stream is not None:
-            stack.enter_context(torch.cuda.stream(stream))
+def _check_all(index, args):
+    """Each (tensor, name, dtype, shape): on that device, of that type and shape, contiguous. (These checks are a large
+    part of a small call's time on the host, so the tests that pass are made in place.)"""
+    for t, name, dtype, shape in args:
+        if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _refuse(t, name, index, dtype, shape)
+
+
+def _cuda_index(t, name):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return index
+
+
+def _on(index, stream, call):
+    """_check(call(stream handle)) with device `index` current, on `stream` or that device's current one. A workspace
+    that `call` allocates belongs to that stream, so that no other call shares it."""
+    if stream is None and torch.cuda.current_device() == index:
+        _check(call(_raw_stream(index)))
+        return
+    with torch.cuda.device(index):
+        if stream is None:
+            _check(call(_raw_stream(index)))
         else:
-            stream = torch.cuda.current_stream(dev)
-        _check(call(stream.cuda_stream))
+            with torch.cuda.stream(stream):
+                _check(call(stream.cuda_stream))
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own quick form of the same, where this build of it has one
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+_INT_MAX = 2 ** 31 - 1
 
 
 def mtp_kv8_append(k_new, v_new, starts, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, *, stream=None):
@@ -442,64 +465,52 @@ def mtp_kv8_append(k_new, v_new, starts, k_cache, v_cache, k_scale, v_scale, blo
     T, Hkv, d = k_new.shape
     B, max_blocks = block_table.shape
     dt, nb = k_new.dtype, k_cache.shape[0]
-    dev = _same_device(k_new, v_new, starts, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens)
-    _dev(k_new, "k_new")
-    _dev(v_new, "v_new", dt, (T, Hkv, d))
-    _dev(starts, "starts", torch.int32, (B + 1,))
-    _kv8_cache(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(ctx_lens, "ctx_lens", torch.int32, (B,))
+    index = _cuda_index(k_new, "k_new")
+    new, cache, scale, i32, f8 = (T, Hkv, d), (nb, BLOCK_SIZE, Hkv, d), (nb, Hkv), torch.int32, torch.float8_e4m3fn
+    _check_all(index, ((k_new, "k_new", dt, new), (v_new, "v_new", dt, new), (starts, "starts", i32, (B + 1,)),
+                       (k_cache, "k_cache", f8, cache), (v_cache, "v_cache", f8, cache),
+                       (k_scale, "k_scale", torch.float32, scale), (v_scale, "v_scale", torch.float32, scale),
+                       (block_table, "block_table", i32, (B, max_blocks)), (ctx_lens, "ctx_lens", i32, (B,))))
     a = Kv8AppendArgs(k_new.data_ptr(), v_new.data_ptr(), starts.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                       k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(), T, B, Hkv,
                       d, BLOCK_SIZE, max_blocks, nb, _dtype_code(k_new))
-    _launch(dev, stream, lambda s: lib().mtp_kv8_append(ctypes.byref(a), s))
+    _on(index, stream, lambda s: lib().mtp_kv8_append(ctypes.byref(a), s))
 
 
-def _kv8_cache(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d):
-    _dev(k_cache, "k_cache", torch.float8_e4m3fn, (nb, BLOCK_SIZE, Hkv, d))
-    _dev(v_cache, "v_cache", torch.float8_e4m3fn, (nb, BLOCK_SIZE, Hkv, d))
-    _dev(k_scale, "k_scale", torch.float32, (nb, Hkv))
-    _dev(v_scale, "v_scale", torch.float32, (nb, Hkv))
-
-
-def _window_attention(name, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, window,
-                      sinks, sm_scale, workspace, stream):
+def _window_attention(size, attend, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out,
+                      window, sinks, sm_scale, workspace, stream):
     B, R, Hq, d = q.shape
     nb, _, Hkv, _ = k_cache.shape
-    dt = q.dtype
-    dev = _same_device(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, out)
-    if k_scale is None:
-        _dev(k_cache, "k_cache", dt, (nb, BLOCK_SIZE, Hkv, d))
-        _dev(v_cache, "v_cache", dt, (nb, BLOCK_SIZE, Hkv, d))
-    else:
-        _same_device(q, k_scale, v_scale)
-        _kv8_cache(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d)
-    _dev(q, "q")
-    _dev(k_new, "k_new", dt, (B, R, Hkv, d))
-    _dev(v_new, "v_new", dt, (B, R, Hkv, d))
-    _dev(out, "out", dt, (B, R, Hq, d))
-    _dev(block_table, "block_table", torch.int32)
-    _dev(ctx_lens, "ctx_lens", torch.int32, (B,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must have shape (%d, max_blocks), got %s" % (B, tuple(block_table.shape)))
+    max_blocks = block_table.shape[-1]
+    dt, i32 = q.dtype, torch.int32
+    index = _cuda_index(q, "q")
+    new, cache = (B, R, Hkv, d), (nb, BLOCK_SIZE, Hkv, d)
+    ct = dt
+    if k_scale is not None:
+        ct, scale = torch.float8_e4m3fn, (nb, Hkv)
+        _check_all(index, ((k_scale, "k_scale", torch.float32, scale), (v_scale, "v_scale", torch.float32, scale)))
+    _check_all(index, ((q, "q", dt, (B, R, Hq, d)), (k_new, "k_new", dt, new), (v_new, "v_new", dt, new),
+                       (k_cache, "k_cache", ct, cache), (v_cache, "v_cache", ct, cache),
+                       (block_table, "block_table", i32, (B, max_blocks)), (ctx_lens, "ctx_lens", i32, (B,)),
+                       (out, "out", dt, (B, R, Hq, d))))
     a = WindowAttnArgs(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                        None if k_scale is None else k_scale.data_ptr(), None if v_scale is None else v_scale.data_ptr(),
                        block_table.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), B, R - 1, Hq, Hkv, d, BLOCK_SIZE,
-                       block_table.shape[1], nb, min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1),
+                       max_blocks, nb, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
                        d ** -0.5 if sm_scale is None else float(sm_scale), _dtype_code(q))
-    L, ref = lib(), ctypes.byref(a)
+    ref = ctypes.byref(a)
 
     def call(s):
         ws = workspace
         if ws is None:
-            n = getattr(L, "mtp_attention_%s_workspace_size" % name)(ref)
+            n = size(ref)
             if n == 0:
                 _check(MTP_INVALID_ARG)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
         a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        return getattr(L, "mtp_verify_attention_" + name)(ref, s)
+        return attend(ref, s)
 
-    _launch(dev, stream, call)
+    _on(index, stream, call)
 
 
 def mtp_verify_attention_kv8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, *,
@@ -511,8 +522,9 @@ def mtp_verify_attention_kv8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale
     block_table [B, max_blocks] int32, ctx_lens [B] int32. window > 0: a row sees the last `window` positions and the
     first `sinks` tokens; window = 0: all. Chains of drafts only.
     """
-    _window_attention("kv8", q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, window,
-                      sinks, sm_scale, workspace, stream)
+    L = lib()
+    _window_attention(L.mtp_attention_kv8_workspace_size, L.mtp_verify_attention_kv8, q, k_new, v_new, k_cache, v_cache,
+                      k_scale, v_scale, block_table, ctx_lens, out, window, sinks, sm_scale, workspace, stream)
 
 
 def mtp_verify_attention_window(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, out, *, window, sinks=0,
@@ -520,31 +532,30 @@ def mtp_verify_attention_window(q, k_new, v_new, k_cache, v_cache, block_table, 
     """mtp_verify_attention for chains in which a row sees the last `window` >= 1 positions, its own among them, and
     the first `sinks` tokens (GQA/MHA caches [blocks, 64, Hkv, d] of q's type, d 64 or 128). Blocks that no row sees
     are not read; their table entries may be -1."""
-    _window_attention("window", q, k_new, v_new, k_cache, v_cache, None, None, block_table, ctx_lens, out, window,
-                      sinks, sm_scale, workspace, stream)
+    L = lib()
+    _window_attention(L.mtp_attention_window_workspace_size, L.mtp_verify_attention_window, q, k_new, v_new, k_cache,
+                      v_cache, None, None, block_table, ctx_lens, out, window, sinks, sm_scale, workspace, stream)
 
 
 def kv_window_release(block_table, seq_lens, free_list, free_count, *, window, sinks=0, workspace=None, stream=None):
     """Return the blocks that no row at a position >= seq_lens sees behind `window` and `sinks` to the free list."""
     B, max_blocks = block_table.shape
-    dev = _same_device(block_table, seq_lens, free_list, free_count)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32, (B,))
-    _dev(free_list, "free_list", torch.int32)
-    _dev(free_count, "free_count", torch.int32, (1,))
+    index, i32 = _cuda_index(block_table, "block_table"), torch.int32
+    n_free = free_list.numel()
+    _check_all(index, ((block_table, "block_table", i32, (B, max_blocks)), (seq_lens, "seq_lens", i32, (B,)),
+                       (free_list, "free_list", i32, (n_free,)), (free_count, "free_count", i32, (1,))))
     L = lib()
     a = WindowReleaseArgs(block_table.data_ptr(), seq_lens.data_ptr(), free_list.data_ptr(), free_count.data_ptr(), B,
-                          BLOCK_SIZE, max_blocks, free_list.numel(), min(int(window), 2 ** 31 - 1),
-                          min(int(sinks), 2 ** 31 - 1))
+                          BLOCK_SIZE, max_blocks, n_free, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX))
 
     def call(s):
         ws = workspace
         if ws is None:
-            ws = torch.empty(L.mtp_window_release_workspace_size(B), dtype=torch.uint8, device=dev)
+            ws = torch.empty(L.mtp_window_release_workspace_size(B), dtype=torch.uint8, device=block_table.device)
         a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
         return L.kv_window_release(ctypes.byref(a), s)
 
-    _launch(dev, stream, call)
+    _on(index, stream, call)
 
 
 def sync_status(stream=None):
