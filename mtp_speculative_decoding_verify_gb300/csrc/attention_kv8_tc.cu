@@ -35,17 +35,21 @@
 // pass 2^8, or was below 2^-4 for three of the row's tiles, O is rescaled in TMEM. (Down, so that a few large scores do not cost the rest of the
 // context its bits; O in fp32 has room for the 60 octaves that are allowed.)
 //
-// Two groups of four softmax warps take alternate tiles, each with an S buffer
-// and an O of its own (joined with the rest when the request ends), so that
-// one computes while the other waits for its products. P lies in the columns
-// of the S it came from.
+// Two groups of four softmax warps share the work, each with an O of its own
+// (joined with the rest when the request ends); P lies in the columns of the S
+// it came from. Up to 32 rows they take alternate tiles, each with its own S
+// buffer, so that one computes while the other waits for its products. With
+// more rows the softmax is the longer part: there each takes a page of every
+// tile, and both S buffers serve the two of them, so that the next S is there
+// before this softmax ends (64 requests x 48 rows, 4096 tokens: 184 us with
+// alternate tiles, 170 us with pages; 16 rows, 1k-32k: 350 us and 372 us).
 //
 // Hidden slots: only tiles with a slot that not every row sees are masked.
 // There V's bytes that are NaN become 0 in shared memory (0 x NaN), and a
 // bitmap of (verify token, dim) puts NaN back into the rows that do see them.
 //
-// Warps: 0 and 1 MMA issue, 2 TMA (block ids and scales of 32 pages at a time,
-// one a lane), 4-11 softmax and output, 12-15 masked V and the next request's
+// Warps: 0 and 1 P V, 2 TMA (block ids and scales of 32 pages at a time, one a
+// lane), 3 S, 4-11 softmax and output, 12-15 masked V and the next request's
 // Q. (One polling warp for all products was the slowest part of a tile.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -83,8 +87,8 @@ constexpr uint32_t kColO = 256;        // S (and P) buffers at columns 0 and 128
 template <int D>
 struct Smem {
   static constexpr int kTile = kKeys * D;                 // bytes of K or V of a tile
-  // Even: a stage then serves tiles of one softmax group only, whose MMA warp meets its phases one after the other (a
-  // wait's parity tells only two apart).
+  // Even: a stage of V then serves tiles of one softmax group only, whose P V warp meets its phases one after the other
+  // (a wait's parity tells only two apart).
   // V is held longer (to P V, two tiles behind S).
   static constexpr int kKStages = D == 128 ? 4 : 6, kVStages = 6;
   static constexpr int kK = 0, kV = kK + kKStages * kTile;
@@ -96,7 +100,7 @@ struct Smem {
   static constexpr int kFac = kRing + kSegRing * 32;      // [kSegs][64] factors of the rows' scores
   static constexpr int kNan = kFac + kSegs * 64 * 4;      // [kNanSegs][16][4] words
   static constexpr int kBar = kNan + kNanSegs * 16 * 4 * 4;
-  static constexpr int kBars = 2 * kKStages + 3 * kVStages + 2 + 2 + 2 + 2 + kInfo + kSegs + kSegRing;
+  static constexpr int kBars = 2 * kKStages + 3 * kVStages + 2 + 2 + 4 + 4 + kInfo + kSegs + kSegRing;
   static constexpr int kMisc = kBar + kBars * 8;          // rest flags [kSegs][2], join flag, abort, TMEM base
   static constexpr int kBytes = kMisc + kSegs * 8 + 16 + 1024;
   // byte offset of 16-byte chunk c of row r of a K-major operand tile, as TMA swizzles it
@@ -296,6 +300,7 @@ __device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_
 struct Seg {
   int b, i0, i1, n, ctx, pad;
   int64_t p0;
+  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == n; }
   __device__ __forceinline__ int tiles() const { return (i1 - i0 + 1) / 2; }
 };
 
@@ -340,6 +345,60 @@ __device__ __forceinline__ uint32_t hide_nan(const WindowParams& p, uint32_t w, 
   return w;
 }
 
+// Where CTA gg of a KV head leaves its part of a request: slot 0 for one it
+// did not begin, slot 1 for one it began. [rows][D] values, then (maximum,
+// sum) of each row.
+template <int D, int NRB>
+__device__ __forceinline__ float* part_slot(const WindowParams& p, int gg, int which, int kvh, int row_tile) {
+  return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * p.row_tiles + row_tile) * ((size_t)NRB * 16 * (D + 2));
+}
+
+// The CTAs that share a request: of pages p0 and p0 + n - 1 of the line.
+__device__ __forceinline__ void sharers(const Seg& seg, int G, int64_t total, int* g0, int* g1) {
+  *g0 = (int)(((seg.p0 + 1) * G - 1) / total);
+  *g1 = (int)(((seg.p0 + seg.n) * G - 1) / total);
+}
+
+// Count this CTA's part as left; true for the last of them. One thread, after
+// all that wrote the part have met it at a barrier.
+__device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int G, int64_t total) {
+  int g0, g1;
+  sharers(seg, G, total, &g0, &g1);
+  __threadfence();
+  const int before = atomicAdd(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile, 1);
+  __threadfence();
+  return before == g1 - g0;
+}
+
+// Join the parts of a request, in the order of the CTAs. Thread t of n.
+template <int D, int NRB>
+__device__ void join_parts(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int G, int64_t total, int t, int n) {
+  int g0, g1;
+  sharers(seg, G, total, &g0, &g1);
+  const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
+  const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
+  for (int u = t; u < n_rows * (D / 4); u += n) {
+    const int local = u / (D / 4), dim = u % (D / 4) * 4;
+    float m = -INFINITY, l = 0.0f;
+    for (int gg = g0; gg <= g1; ++gg)
+      m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(part_slot<D, NRB>(p, gg, gg == g0, kvh, row_tile) + NRB * 16 * D) + local).x);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int gg = g0; gg <= g1; ++gg) {
+      const float* from = part_slot<D, NRB>(p, gg, gg == g0, kvh, row_tile);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + NRB * 16 * D) + local);
+      const float4 o4 = __ldcg(reinterpret_cast<const float4*>(from + (size_t)local * D + dim));
+      const float c = ml.x == -INFINITY ? 1.0f : ex2(ml.x - m);   // (nothing seen: zeros, or NaN)
+      l += ml.y * c;
+      v.x += o4.x * c, v.y += o4.y * c, v.z += o4.z * c, v.w += o4.w * c;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int row = first_row + local;
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (out0 + (int64_t)(row / p.group) * p.Hq + row % p.group) * D + dim;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  }
+}
+
 // NRB: blocks of 16 query rows (1, 2, 4).
 template <int D, int NRB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -348,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<D>;
   constexpr int kKStages = S::kKStages, kVStages = S::kVStages;
   constexpr int KG = 4 / NRB;            // key groups: warps that share a row block
-  constexpr int NK = 16 * NRB;           // keys of a tile that a thread takes
+  constexpr bool kPages = NRB == 4;      // the groups take pages instead of tiles
+  constexpr int NK = kPages ? 8 * NRB : 16 * NRB;   // keys of a tile that a thread takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* xbuf = reinterpret_cast<float*>(smem + S::kX);
@@ -363,10 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_empty = v_ready + kVStages;
   uint64_t* q_full = v_empty + kVStages;  // Q of the next request is in place
   uint64_t* q_empty = q_full + 1;        // the last S of a request is done
-  uint64_t* s_full = q_full + 2;         // [2] S of tile g is there, and so O of tile g - 2
-  uint64_t* p_full = s_full + 2;         // [2] P of tile g has replaced S
-  uint64_t* pv_done = p_full + 2;        // [2] O holds tile g
-  uint64_t* info_full = pv_done + 2;     // [kInfo]
+  // Of tile g, in buffer g % 2 (pages: of each group, at 2 group + g % 2):
+  uint64_t* s_full = q_full + 2;         // S is there, and so O of tile g - 2
+  uint64_t* p_full = s_full + 2;         // P has replaced S
+  uint64_t* pv_done = p_full + 4;        // O holds the tile
+  uint64_t* info_full = pv_done + 4;     // [kInfo]
   uint64_t* fac_full = info_full + kInfo;   // [kSegs]
   uint64_t* seg_full = fac_full + kSegs;    // [kSegRing]
   Seg* ring = reinterpret_cast<Seg*>(smem + S::kRing);
@@ -378,10 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int heads = p.Hkv * p.row_tiles;
   const int kvh = blockIdx.x % heads / p.row_tiles, row_tile = blockIdx.x % heads % p.row_tiles;
-  const int64_t total = __ldg(p.prefix + p.B);
-  const int G = (int)min((int64_t)(gridDim.x / heads), total);
   const int g_cta = blockIdx.x / heads;
-  if (g_cta >= G) return;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKStages; ++s) {
@@ -391,12 +449,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kVStages; ++s) {
       sm100::mbar_init(&v_full[s], 1);
       sm100::mbar_init(&v_ready[s], 4);
-      sm100::mbar_init(&v_empty[s], 1);
+      sm100::mbar_init(&v_empty[s], kPages ? 2 : 1);
     }
     sm100::mbar_init(q_full, 128);
-    sm100::mbar_init(q_empty, 2);
-    for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&s_full[i], 1);
+    sm100::mbar_init(q_empty, 1);
+    for (int i = 0; i < 4; ++i) {
+      if (i < 2) {
+        sm100::mbar_init(&s_full[i], 1);
+      }
       sm100::mbar_init(&p_full[i], 4);
       sm100::mbar_init(&pv_done[i], 1);
     }
@@ -406,14 +466,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     sm100::fence_barrier_init();
   }
-  if (warp == 0) {
-    sm100::tmem_alloc(tmem_slot, 512);
-    sm100::tmem_relinquish();
+  if (threadIdx.x == 32) {
+    sm100::tma_prefetch_desc(&tm_k);
+    sm100::tma_prefetch_desc(&tm_v);
   }
   for (int i = threadIdx.x; i < kNanSegs * 16 * 4; i += kThreads) nanmap[i] = 0;
   for (int i = threadIdx.x; i < S::kTile / 16; i += kThreads)   // the rest term has no second one
     *reinterpret_cast<uint4*>(smem + S::kQ + S::kTile + i * 16) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
+  // Everything up to here may run while the append still does; what follows
+  // reads what it writes.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t total = __ldg(p.prefix + p.B);
+  const int G = window_ctas(total, gridDim.x / heads);
+  if (g_cta >= G) return;
+  if (warp == 0) {
+    sm100::tmem_alloc(tmem_slot, 512);
+    sm100::tmem_relinquish();
+  }
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
@@ -436,60 +506,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     constexpr uint32_t kShape = (1u << 4) | ((uint32_t)(128 >> 4) << 24);   // fp32 D, M = 128
+    // (In the warps that issue MMAs the whole warp walks the tiles, so that
+    // the descriptors stay uniform; one elected lane issues.)
     if (warp < 2) {
-    // ---------------------------------------------------------------- MMA
-    // Warp wg issues the products of softmax group wg's tiles: P V of one,
-    // then, once that has read P, S of the next into the same buffer. (The whole warp walks the tiles, so that the descriptors stay
-    // uniform; one elected lane issues.)
-    constexpr uint32_t idesc_qk = kShape | ((uint32_t)(kKeys >> 3) << 17);              // e4m3 x e4m3
-    constexpr uint32_t idesc_rest = idesc_qk | (1u << 7);                               // e5m2 x e4m3
-    constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // V MN-major
-    const int wg = warp;
-    const uint64_t qd = desc_kmajor<D>(sbase + S::kQ), kd0 = desc_kmajor<D>(sbase + S::kK);
-    const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV);
-    int pv_g = -1;                       // the tile whose P V is next (its S has been issued), -1: none
-    bool pv_first = false;               // it begins O
-    auto do_pv = [&]() -> bool {
-      const int pv_stage = pv_g % kVStages;
-      if (!wait(&v_ready[pv_stage], (uint32_t)((pv_g / kVStages) & 1)) || !wait(&p_full[wg], (uint32_t)((pv_g >> 1) & 1))) return false;
-      sm100::tc_fence_after();
-      if (sm100::elect_one()) {
-        const uint64_t vd = vd0 + (uint64_t)(pv_stage * (S::kTile >> 4));
+      // --------------------------------------------------------------- P V
+      // Of softmax group `warp`: its tiles, or its page of each.
+      constexpr uint32_t idesc_pv = kShape | ((uint32_t)(D >> 3) << 17) | (1u << 16);   // V MN-major
+      constexpr int kCount = kPages ? kBlock : kKeys;      // keys of a product
+      const int wg = warp;
+      const uint64_t vd0 = desc_mnmajor<D>(sbase + S::kV + (kPages ? wg * (S::kTile / 2) : 0));
+      int g = 0, last_g = -1;
+      Seg seg;
+      for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
+        const int tiles = seg.tiles();
+        for (int i = 0; i < tiles; ++i, ++g) {
+          const int buf = g & 1, stage = g % kVStages, bar = kPages ? wg * 2 + buf : wg;
+          if (!kPages && buf != wg) continue;
+          ok = wait(&p_full[bar], (uint32_t)((g >> 1) & 1)) && wait(&v_ready[stage], (uint32_t)((g / kVStages) & 1));
+          if (!ok) break;
+          last_g = g;
+          sm100::tc_fence_after();
+          if (sm100::elect_one()) {
+            const uint64_t vd = vd0 + (uint64_t)(stage * (S::kTile >> 4));
+            const uint32_t first = i < (kPages ? 1 : 2) ? 1u : 0u;   // it begins the group's O
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 32; ++kk)
-          mma_f8_ts(tmem + kColO + wg * 128, tmem + wg * 128 + kk * 8, vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv,
-                    (!pv_first || kk > 0) ? 1u : 0u);
-        sm100::tc_commit(&pv_done[wg]);
-        sm100::tc_commit(&v_empty[pv_stage]);
+            for (int kk = 0; kk < kCount / 32; ++kk)
+              mma_f8_ts(tmem + kColO + wg * 128, tmem + buf * 128 + (kPages ? wg * 64 : 0) + kk * 8,
+                        vd + (uint64_t)(kk * (32 * D >> 4)), idesc_pv, kk > 0 ? 1u : 1u - first);
+            sm100::tc_commit(&pv_done[bar]);
+            sm100::tc_commit(&v_empty[stage]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {
+        *abort = 1;
+        if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
+        // MMAs in flight end before the shared memory and TMEM go (else the softmax warps have waited for every one)
+        if (last_g >= 0)
+          sm100::mbar_wait_timeout(&pv_done[kPages ? wg * 2 + (last_g & 1) : wg], (uint32_t)((last_g >> 1) & 1), sm100::kWaitTimeoutNs);
       }
       __syncwarp();
-      return true;
-    };
-    int g = 0;
-    Seg seg;
-    for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
-      const int tiles = seg.tiles();
-      const int mine = (tiles + ((g ^ wg ^ 1) & 1)) / 2;   // this group's tiles of the segment
-      if (mine == 0) {                   // (every Q is waited for: a parity tells only two phases apart)
-        if (pv_g >= 0) ok = do_pv();
-        pv_g = -1;
-        if (!ok || !(ok = wait(q_full, (uint32_t)(sn & 1)))) break;
-        if (lane == 0) sm100::mbar_arrive(q_empty);
-      }
-      bool third = false;
-      for (int i = 0, m = 0; i < tiles; ++i, ++g) {
-        if ((g & 1) == wg) {
-          const int stage = g % kKStages;
-          if (pv_g >= 0 && !(ok = do_pv())) break;
-          if (m == 0) {
-            ok = wait(q_full, (uint32_t)(sn & 1));
-            third = rest[sn % kSegs] != 0;
-          }
-          ok = ok && wait(&k_full[stage], (uint32_t)((g / kKStages) & 1)) && (g < 2 || wait(&pv_done[wg], (uint32_t)(((g - 2) >> 1) & 1)));
+    } else if (warp == 3) {
+      // ----------------------------------------------------------------- S
+      // Of each tile, as soon as its keys are there and P V of tile g - 2 (of
+      // both groups' pages) has read P from the buffer.
+      constexpr uint32_t idesc_qk = kShape | ((uint32_t)(kKeys >> 3) << 17);            // e4m3 x e4m3
+      constexpr uint32_t idesc_rest = idesc_qk | (1u << 7);                             // e5m2 x e4m3
+      const uint64_t qd = desc_kmajor<D>(sbase + S::kQ), kd0 = desc_kmajor<D>(sbase + S::kK);
+      int g = 0;
+      Seg seg;
+      for (int sn = 0; (ok = ok && take(sn, seg)) && seg.n != 0; ++sn) {
+        const int tiles = seg.tiles();
+        if (!(ok = wait(q_full, (uint32_t)(sn & 1)))) break;
+        const bool third = rest[sn % kSegs] != 0;
+        for (int i = 0; i < tiles; ++i, ++g) {
+          const int buf = g & 1, stage = g % kKStages;
+          const uint32_t two_back = (uint32_t)(((g - 2) >> 1) & 1);
+          ok = wait(&k_full[stage], (uint32_t)((g / kKStages) & 1)) &&
+               (g < 2 || (wait(&pv_done[buf], two_back) && (!kPages || wait(&pv_done[2 + buf], two_back))));
           if (!ok) break;
           sm100::tc_fence_after();
           if (sm100::elect_one()) {
-            const uint32_t d = tmem + wg * 128;
+            const uint32_t d = tmem + buf * 128;
             const uint64_t kd = kd0 + (uint64_t)(stage * (S::kTile >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, kk ? 1u : 0u);
@@ -497,35 +576,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, qd + (uint64_t)((S::kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_rest, 1u);
             }
-            sm100::tc_commit(&s_full[wg]);
+            sm100::tc_commit(&s_full[buf]);
             sm100::tc_commit(&k_empty[stage]);
-            if (m + 1 == mine) sm100::tc_commit(q_empty);
+            if (i + 1 == tiles) sm100::tc_commit(q_empty);
           }
           __syncwarp();
-          pv_g = g;
-          pv_first = m == 0;
-          ++m;
         }
       }
-    }
-    if (ok && pv_g >= 0) ok = do_pv();
-    if (!ok) {
-      *abort = 1;
-      if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
-      // MMAs in flight end before the shared memory and TMEM go (else the softmax warps have waited for every one)
-      if (pv_g >= 0) {
-        sm100::mbar_wait_timeout(&s_full[wg], (uint32_t)((pv_g >> 1) & 1), 1000000);
-        sm100::mbar_wait_timeout(&pv_done[wg], (uint32_t)((pv_g >> 1) & 1), 1000000);
+      if (!ok) {
+        *abort = 1;
+        if (lane == 0) raise_error(p.err, MTP_ERR_TIMEOUT);
+        if (g > 0) sm100::mbar_wait_timeout(&s_full[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), sm100::kWaitTimeoutNs);
       }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
+      __syncwarp();
+    } else {
     // ----------------------------------------------------------------- TMA
     const uint64_t pol = sm100::l2_policy_evict_first();
-    if (lane == 0) {
-      sm100::tma_prefetch_desc(&tm_k);
-      sm100::tma_prefetch_desc(&tm_v);
-    }
     const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
     Walk walk{p, t_begin, t_end, find_request(p.prefix, p.B, t_begin, lane)};
     int g = 0;
@@ -620,12 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------- softmax and output
     const int w = warp & 3, wg = (warp >> 2) - 1, st = threadIdx.x - 128;
     const int rb = w % NRB, kg = w / NRB, half = lane >> 4, r16 = lane & 15;
-    const int page_half = (kg * 2 + half) * NK / kBlock, in_page = (kg * 2 + half) * NK % kBlock;   // the thread's keys
+    const int page_half = kPages ? wg : (kg * 2 + half) * NK / kBlock, in_page = (kg * 2 + half) * NK % kBlock;   // its keys
     const int row = row_tile * 64 + rb * 16 + r16;
     const int j = min(row, p.rows - 1) / p.group;
     const uint32_t quarter = tmem + ((uint32_t)(32 * w) << 16);
     const uint32_t o_hi = quarter + kColO + wg * 128, o_lo = o_hi + (16u << 16);
-    const uint32_t s_hi = quarter + wg * 128, s_lo = s_hi + (16u << 16);
     auto soft_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     int g = 0;
     Seg seg;
@@ -639,8 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int low_tiles = 0;                                   // in a row, with a small largest probability
       bool begun = false;                                  // O holds something
       const int g_end = g + tiles;
-      for (g += (g ^ wg) & 1; g < g_end; g += 2) {         // this group's tiles
-        ok = ok && wait(&info_full[g % kInfo], (uint32_t)((g / kInfo) & 1)) && wait(&s_full[wg], (uint32_t)((g >> 1) & 1));
+      for (g += kPages ? 0 : (g ^ wg) & 1; g < g_end; g += kPages ? 1 : 2) {   // this group's tiles
+        const int buf = g & 1;                             // (its own buffer where it takes tiles)
+        const uint32_t s_hi = quarter + buf * 128 + (kPages ? wg * 64 : 0), s_lo = s_hi + (16u << 16);
+        ok = ok && wait(&info_full[g % kInfo], (uint32_t)((g / kInfo) & 1)) && wait(&s_full[buf], (uint32_t)((g >> 1) & 1));
         if (!ok) break;                                    // the segment's end still meets the others
         sm100::tc_fence_after();
         const PageInfo in = info[g % kInfo].page[page_half];
@@ -686,7 +753,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float c = !move ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - to);
           if (move) ref = to;
           top_ref = fmaxf(top_ref, ref);
-          if (begun) {                                     // (S of tile g came after P V of tile g - 2)
+          if (begun) {
+            if (kPages) {                                  // (else S of tile g came after the group's last P V)
+              ok = wait(&pv_done[wg * 2 + (buf ^ 1)], (uint32_t)(((g - 1) >> 1) & 1));
+              if (!ok) break;
+              sm100::tc_fence_after();
+            }
 #pragma unroll 2
             for (int q = 0; q < D / 32; ++q) {               // this thread's half of the row's dims, 16 at a time
               float o[16], o2[16];
@@ -733,13 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         sm100::tc_fence_before();
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&p_full[wg]);
+        if (lane == 0) sm100::mbar_arrive(&p_full[kPages ? wg * 2 + buf : wg]);
         begun = true;
       }
       // ---- the request's part is done: join the lanes of each row
       g = g_end;
-      const int last_g = g - 1 - ((g - 1 - wg) & 1);       // this group's last tile so far
-      ok = ok && (!begun || wait(&pv_done[wg], (uint32_t)((last_g >> 1) & 1)));
+      const int last_g = kPages ? g - 1 : g - 1 - ((g - 1 - wg) & 1);   // this group's last tile so far
+      ok = ok && (!begun || wait(&pv_done[kPages ? wg * 2 + (last_g & 1) : wg], (uint32_t)((last_g >> 1) & 1)));
       sm100::tc_fence_after();
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       if (half == 0) red[(wg * 4 + w) * 16 + r16] = make_float2(lref, sum);
@@ -752,38 +824,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 v = red[((y / KG) * 4 + rb + NRB * (y % KG)) * 16 + r16];
         L += v.y * (v.x == -INFINITY ? 1.0f : ex2(v.x - M));   // (nothing seen: 0, or NaN from K)
       }
-      const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
+      const bool whole = seg.whole();
       const float own = (ref == -INFINITY ? 0.0f : ex2(ref - M)) * (whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f);
       const float poison = sum != sum ? sum : 0.0f;            // NaN in K: every dim of the row
       const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
       const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
-      // Slot 0 of a CTA is for a request it did not begin, slot 1 for one it began.
-      const size_t rec = (size_t)NRB * 16 * (D + 2);
-      auto slot_of = [&](int gg, int which) {
-        return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * p.row_tiles + row_tile) * rec;
-      };
-      float* part = whole ? nullptr : slot_of(g_cta, seg.i0 > 0 ? 0 : 1);
+      float* part = whole ? nullptr : part_slot<D, NRB>(p, g_cta, seg.i0 > 0 ? 0 : 1, kvh, row_tile);
       if (!whole && wg == 0 && kg == 0 && half == 0) reinterpret_cast<float2*>(part + (size_t)NRB * 16 * D)[rb * 16 + r16] = make_float2(M, L);
       auto out_row = [&](int local) {
         const int rr = first_row + local;
         return static_cast<__nv_bfloat16*>(p.out) + (out0 + (int64_t)(rr / p.group) * p.Hq + rr % p.group) * D;
       };
-      __nv_bfloat16* put_out[(NRB + 1) / 2];                   // the rows whose dims this thread writes
-#pragma unroll
-      for (int u = 0; u < (NRB + 1) / 2; ++u) put_out[u] = out_row(min(u * 32 + (st >> 3), n_rows - 1));
-      auto put = [&](int u, int dim, const float4& v) {        // four dims of a row
-        const int local = u * 32 + (st >> 3);
-        if (local >= n_rows) return;
-        if (whole) {
-          __nv_bfloat16* to = put_out[u] + dim;
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-        } else {
-          *reinterpret_cast<float4*>(part + (size_t)local * D + dim) = v;
-        }
-      };
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {                       // 16 dims of each half of the row
-        float y[16], y2[16];
+      // 16 of the thread's output dims, from dim0 on, with its weight
+      auto get = [&](int c, float (&y)[16]) {
+        float y2[16];
         if (ok) {
           ld_halves<16, D / 2>(o_hi + c * 16, y);
           ld_halves<16, D / 2>(o_lo + c * 16, y2);
@@ -798,59 +852,71 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((bits >> k) & 1) y[k] = NAN;
           y[k] += poison;
         }
-        float* to = xbuf + (size_t)((wg * 4 + w) * 16 + r16) * 36 + half * 16;
+      };
+      // four dims of a row whose output starts at `to`
+      auto put = [&](int local, __nv_bfloat16* to, int dim, const float4& v) {
+        if (local >= n_rows) return;
+        if (whole) *reinterpret_cast<uint2*>(to + dim) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        else *reinterpret_cast<float4*>(part + (size_t)local * D + dim) = v;
+      };
+      if constexpr (KG == 1) {
+        // A row is in two warps, one of each group: they swap halves of its
+        // dims, 16 a thread and step, each thread for its counterpart's.
+        const int local = rb * 16 + r16;
+        __nv_bfloat16* to = out_row(min(local, n_rows - 1));
+        float4* mine = reinterpret_cast<float4*>(xbuf) + (st & 127) + wg * 512;
+        const float4* theirs = reinterpret_cast<const float4*>(xbuf) + (st & 127) + (wg ^ 1) * 512;
+#pragma unroll 1
+        for (int u = 0; u < D / 32; ++u) {
+          const bool give = (u & 1) == 0;
+          const int c = (give ? wg ^ 1 : wg) * (D / 64) + (u >> 1);
+          float y[16];
+          get(c, y);
+          if (!give || u > 0) soft_sync();
+          if (give) {
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-        soft_sync();
+            for (int k = 0; k < 4; ++k) mine[k * 128] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          } else {
 #pragma unroll
-        for (int u = 0; u < (NRB + 1) / 2; ++u) {
-          const int local = u * 32 + (st >> 3), d4 = (st & 7) * 4;
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = theirs[k * 128];
+              put(local, to, half * (D / 2) + c * 16 + 4 * k,
+                  make_float4(y[4 * k] + v.x, y[4 * k + 1] + v.y, y[4 * k + 2] + v.z, y[4 * k + 3] + v.w));
+            }
+          }
+        }
+      } else {
+        // A row is in 2 KG warps: all of them leave 32 of its dims, and 256
+        // threads add four dims each.
+        __nv_bfloat16* put_out = out_row(min(st >> 3, n_rows - 1));
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float y[16];
+          get(c, y);
+          float* to = xbuf + (size_t)((wg * 4 + w) * 16 + r16) * 36 + half * 16;
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+          soft_sync();
+          const int local = st >> 3, d4 = (st & 7) * 4;
           if (local < NRB * 16) {
-            const float* from = xbuf + (size_t)((local >> 4) * 16 + (local & 15)) * 36 + d4;
+            const float* from = xbuf + (size_t)local * 36 + d4;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int y2 = 0; y2 < 2 * KG; ++y2) {
               const float4 o4 = *reinterpret_cast<const float4*>(from + ((y2 / KG) * 4 + NRB * (y2 % KG)) * 16 * 36);
               v.x += o4.x, v.y += o4.y, v.z += o4.z, v.w += o4.w;
             }
-            put(u, (d4 >> 4) * (D / 2) + c * 16 + (d4 & 15), v);
+            put(local, put_out, (d4 >> 4) * (D / 2) + c * 16 + (d4 & 15), v);
           }
+          soft_sync();
         }
-        soft_sync();
       }
       sm100::tc_fence_before();
       if (!whole) {
-        __threadfence();
         soft_sync();
-        const int g0 = (int)(((seg.p0 + 1) * G - 1) / total), g1 = (int)(((seg.p0 + seg.n) * G - 1) / total);
-        if (st == 0) {
-          const int before = atomicAdd(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile, 1);
-          *last_flag = before == g1 - g0;
-        }
+        if (st == 0) *last_flag = arrive_part(p, seg, kvh, row_tile, G, total);
         soft_sync();
-        if (*last_flag) {
-          // Last of the CTAs that share the request: join their parts, in order.
-          __threadfence();
-          for (int u = st; u < n_rows * (D / 4); u += 256) {
-            const int local = u / (D / 4), dim = u % (D / 4) * 4;
-            float m = -INFINITY, l = 0.0f;
-            for (int gg = g0; gg <= g1; ++gg)
-              m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(slot_of(gg, gg == g0) + (size_t)NRB * 16 * D) + local).x);
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int gg = g0; gg <= g1; ++gg) {
-              const float* from = slot_of(gg, gg == g0);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (size_t)NRB * 16 * D) + local);
-              const float4 o4 = __ldcg(reinterpret_cast<const float4*>(from + (size_t)local * D + dim));
-              const float c = ml.x == -INFINITY ? 1.0f : ex2(ml.x - m);   // (nothing seen: zeros, or NaN)
-              l += ml.y * c;
-              v.x += o4.x * c, v.y += o4.y * c, v.z += o4.z * c, v.w += o4.w * c;
-            }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            __nv_bfloat16* to = out_row(local) + dim;
-            *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-          }
-        }
+        if (*last_flag) join_parts<D, NRB>(p, seg, kvh, row_tile, G, total, st, 256);
       }
       soft_sync();                                             // red, the flag and the bitmap have been read
       if (st < 64) nanmap[(sn % kNanSegs) * 64 + st] = 0;
@@ -1016,8 +1082,8 @@ cudaError_t launch(const mtp_window_attn_args& a, const WindowPlan& pl, const Wi
   auto kern = kv8_tc_kernel<D, NRB>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(pl.ctas_per_head * a.Hkv * pl.row_tiles), kThreads, Smem<D>::kBytes, s>>>(maps[0], maps[1], p);
-  return cudaGetLastError();
+  return launch_behind_append(kern, (unsigned)(pl.ctas_per_head * a.Hkv * pl.row_tiles), kThreads, Smem<D>::kBytes, s, maps[0],
+                              maps[1], p);
 }
 
 // Blocks of 16 rows of a CTA: 1, 2 or 4; a KV head of more than 64 rows takes

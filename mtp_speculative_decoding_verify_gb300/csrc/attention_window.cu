@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(128) window_append_kernel(const uint4* __restr
                                                             const int32_t* __restrict__ ctx_lens, int R, int vecs,
                                                             int max_blocks, int num_blocks, unsigned* err,
                                                             const WindowSchedule schedule) {
+  asm volatile("griddepcontrol.launch_dependents;");   // (the attention behind it may set up)
   if (schedule.prefix != nullptr && blockIdx.x == gridDim.x - 1) {
     window_schedule<128>(schedule);
     return;
@@ -281,7 +282,7 @@ int check_window(const mtp_window_attn_args* a, bool kv8) {
   if (a->block_size != MTP_BLOCK_SIZE) return fail(name, "block_size must be 64");
   if (a->max_blocks <= 0 || a->max_blocks > (1 << 24) || a->num_blocks <= 0)
     return fail(name, "max_blocks outside [1, 2^24], or num_blocks <= 0");
-  if (a->Hq <= 0 || a->Hkv <= 0 || a->Hq % a->Hkv) return fail(name, "Hq % Hkv != 0");
+  if (a->Hq <= 0 || a->Hkv <= 0 || a->Hkv > (1 << 16) || a->Hq % a->Hkv) return fail(name, "Hkv outside [1, 2^16], or Hq % Hkv != 0");
   if (a->dtype != MTP_F32 && a->dtype != MTP_BF16) return fail(name, "dtype");
   if (!(a->sm_scale > 0.0f && a->sm_scale <= 1e30f)) return fail(name, "sm_scale must be > 0 and finite");
   if (a->window < (kv8 ? 0 : 1)) return fail(name, kv8 ? "window must be >= 0" : "window must be >= 1");
@@ -312,7 +313,7 @@ int check_window(const mtp_window_attn_args* a, bool kv8) {
 bool uses_mma(const mtp_window_attn_args& a) { return a.dtype == MTP_BF16; }
 
 WindowPlan plan_window(const mtp_window_attn_args& a, bool kv8, int sm_count) {
-  if (uses_mma(a)) return kv8 ? plan_kv8_tc(a, sm_count) : plan_window_mma(a, kv8, sm_count);
+  if (uses_mma(a)) return kv8 ? plan_kv8_tc(a, sm_count) : plan_window_mma(a, sm_count);
   WindowPlan p{};
   const int rows = a.Hq / a.Hkv * (a.D + 1);
   const long long ctas = (long long)a.B * a.Hkv * ((rows + kSimtRows - 1) / kSimtRows);
@@ -433,7 +434,7 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
   int launches = 0;
   if (mma) {
     launches = 1;
-    e = kv8 ? launch_kv8_tc(*a, pl, p, s) : launch_window_mma(*a, kv8, pl, p, s);
+    e = kv8 ? launch_kv8_tc(*a, pl, p, s) : launch_window_mma(*a, pl, p, s);
   } else {
     e = launch_simt<float>(p, a->d, kv8, s, &launches);
   }

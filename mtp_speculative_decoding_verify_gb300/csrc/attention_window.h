@@ -40,12 +40,29 @@ struct WindowSchedule {
   int B, R, max_blocks, window, sinks;
 };
 
-WindowPlan plan_window_mma(const mtp_window_attn_args& a, bool kv8, int sm_count);
-cudaError_t launch_window_mma(const mtp_window_attn_args& a, bool kv8, const WindowPlan& pl, const WindowParams& p,
-                              cudaStream_t s);
+WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count);
+cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
 WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_kv8_tc(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, const WindowSchedule& sch, unsigned* err,
                               cudaStream_t s);
+
+// Launch a kernel that waits (griddepcontrol.wait) for the append before it:
+// its CTAs may be set up while the append's still run.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind_append(void (*kern)(Params...), unsigned grid, unsigned threads, int smem, cudaStream_t s,
+                                 Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
+}
 
 }  // namespace mtp

@@ -1,4 +1,4 @@
-// Windowed and 8-bit verify attention of bf16 rows on the tensor cores.
+// Windowed verify attention of bf16 rows over the bf16 cache.
 //
 // out = softmax(scale Q K^T) V over the slots each row sees, one pass over
 // the cache with a running maximum and sum, fp32 accumulation (mma.sync
@@ -19,16 +19,6 @@
 // A warp takes 16 query rows (row warp) and every key_parts-th tile; the
 // parts join in shared memory at the end of a request. Registers hold Q, the
 // scores and the output.
-//
-// The 8-bit cache: e4m3 bytes become f16 in registers, which is exact, and
-// meet Q in f16. A row of Q is scaled by a power of two so that its largest
-// value is near 2^14; bf16's 8 bits then fit f16 exactly except for values
-// 2^-28 below the row's largest. For Q K^T a lane's four consecutive bytes
-// serve as k = 2t, 2t+1, 2t+8, 2t+9 of the product, with Q's fragments loaded
-// in the same order; for P V a transposing load yields pairs of dims, whose
-// even and odd dims become two column tiles. Probabilities are rounded to f16
-// times 2^15 (of f16's range all but the top bit), sums are not rounded. A
-// tile's P V is summed apart and joins the output times the block's scale.
 //
 // Slots that not every row sees occur in the last pages, at the window's edge
 // and behind the sinks. Only those tiles take the masked path: hidden scores
@@ -56,18 +46,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxWarps = 8;              // producer + consumers, two per SM sub-partition: up to 255 registers a thread
 constexpr int kMaxStages = 16;
 constexpr int kMaxSmem = 232448;          // 227 KB
-constexpr int kPShift = 15;               // f16 probabilities are kept times 2^15
 
-template <int D, bool KV8>
+template <int D>
 struct Tile {
-  static constexpr int kRowBytes = D * (KV8 ? 1 : 2);
+  static constexpr int kRowBytes = D * 2;
   static constexpr int kBoxes = kRowBytes > 128 ? kRowBytes / 128 : 1;
   static constexpr int kBytes = kBlock * kRowBytes;      // K or V of a page's head
   static constexpr int kStage = 2 * kBytes;
   // byte offset of the 16-byte chunk c of a key's row
   __device__ __forceinline__ static uint32_t at(int key, int c) {
-    if constexpr (kRowBytes == 64) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);                 // 64-byte swizzle
-    return (c >> 3) * (kBlock * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);                     // 128-byte
+    return (c >> 3) * (kBlock * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);   // boxes of 64 dims, 128-byte swizzle
   }
 };
 
@@ -77,42 +65,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Four e4m3 bytes to two f16x2: bytes 0, 1 and bytes 2, 3.
-__device__ __forceinline__ void cvt_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n"
-      "  .reg .b16 a, b;\n"
-      "  mov.b32 {a, b}, %2;\n"
-      "  cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      "  cvt.rn.f16x2.e4m3x2 %1, b;\n"
-      "}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Take what is not finite out of a pair; true if there was any.
-template <bool KV8>
 __device__ __forceinline__ bool take_out(uint32_t& w) {
-  uint32_t keep;
-  if constexpr (KV8) {
-    const __half2 h = *reinterpret_cast<const __half2*>(&w), z = __hsub2(h, h);
-    keep = __heq2_mask(z, z);
-  } else {
-    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w), z = __hsub2(h, h);
-    keep = __heq2_mask(z, z);
-  }
+  const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w), z = __hsub2(h, h);
+  const uint32_t keep = __heq2_mask(z, z);
   w &= keep;
   return keep != 0xffffffffu;
 }
@@ -130,30 +86,25 @@ __device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_
   return lo;
 }
 
-template <int D, bool KV8>
+template <int D>
 __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     window_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const WindowParams p) {
-  using T = Tile<D, KV8>;
+  using T = Tile<D>;
   constexpr int kVals = D / 2 + 4;        // fp32 values of a lane's partial result: output, two maxima, two sums
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* xchg = reinterpret_cast<float*>(smem + p.stages * T::kStage);     // [row warp][key_parts / 2][kVals][32]
   uint64_t* full = reinterpret_cast<uint64_t*>(xchg + p.row_warps * (p.key_parts / 2) * kVals * kWarp);
   uint64_t* empty = full + kMaxStages;
-  float2* stage_scale = reinterpret_cast<float2*>(empty + kMaxStages);     // K and V scale of its block
-  int* stage_valid = reinterpret_cast<int*>(stage_scale + kMaxStages);     // 0: the table named no block
+  int* stage_valid = reinterpret_cast<int*>(empty + kMaxStages);           // 0: the table named no block
   int* last_flag = stage_valid + kMaxStages;                               // [row warp]
   volatile int* abort = last_flag + kMaxWarps;
 
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int heads = p.Hkv * p.row_tiles;
   const int kvh = blockIdx.x % heads / p.row_tiles, row_tile = blockIdx.x % heads % p.row_tiles;
-  const int64_t total = __ldg(p.prefix + p.B);
-  const int G = (int)min((int64_t)(gridDim.x / heads), total);             // every CTA g < G has a page
   const int g_cta = blockIdx.x / heads;
-  if (g_cta >= G) return;
-  const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -162,8 +113,17 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     }
     *abort = 0;
     sm100::fence_barrier_init();
+    sm100::tma_prefetch_desc(&tm_k);
+    sm100::tma_prefetch_desc(&tm_v);
   }
   __syncthreads();
+  // Everything up to here may run while the append still does; what follows
+  // reads what it writes.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t total = __ldg(p.prefix + p.B);
+  const int G = window_ctas(total, gridDim.x / heads);                      // every CTA g < G has a page
+  if (g_cta >= G) return;
+  const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
 
   int b = find_request(p.prefix, p.B, t_begin, lane);
   int stage = 0;             // of tile n (counted over the CTA's life): n % stages
@@ -171,16 +131,12 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // The warp reads the block ids and scales of 32 pages at a time, one a
-    // lane, so that their latency is paid once for 32 tiles.
+    // The warp reads the block ids of 32 pages at a time, one a lane, so that
+    // their latency is paid once for 32 tiles.
     const uint64_t pol = sm100::l2_policy_evict_first();
     int last_parity[kMaxStages];
 #pragma unroll
     for (int s = 0; s < kMaxStages; ++s) last_parity[s] = -1;
-    if (lane == 0) {
-      sm100::tma_prefetch_desc(&tm_k);
-      sm100::tma_prefetch_desc(&tm_v);
-    }
     bool ok = true;
     for (int64_t pos = t_begin; pos < t_end && ok;) {
       while (__ldg(p.prefix + b + 1) <= pos) ++b;
@@ -189,33 +145,28 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
       const PageSpan span = page_span(p.ctx_lens[b], p.R, p.window, p.sinks);
       for (int i = (int)(pos - p0); i < i1 && ok; i += kWarp) {
         int blk = -1;
-        float2 sc = make_float2(1.0f, 1.0f);
         if (i + lane < i1) {
           blk = p.block_table[(int64_t)b * p.max_blocks + span.page(i + lane)];
           if (blk < 0 || blk >= p.num_blocks) {
             raise_error(p.err, MTP_ERR_BLOCK_ID);
             blk = -1;
-          } else if (KV8) {
-            sc = make_float2(p.k_scale[(int64_t)blk * p.Hkv + kvh], p.v_scale[(int64_t)blk * p.Hkv + kvh]);
           }
         }
         const int n = min(kWarp, i1 - i);
         for (int x = 0; x < n; ++x) {
           const int id = __shfl_sync(0xffffffffu, blk, x);
-          const float sk = __shfl_sync(0xffffffffu, sc.x, x), sv = __shfl_sync(0xffffffffu, sc.y, x);
           int go = 1;
           if (lane == 0) {
             go = sm100::mbar_wait(&empty[stage], phase ^ 1u, abort);
             if (go) {
-              stage_scale[stage] = make_float2(sk, sv);
               stage_valid[stage] = id >= 0;
               if (id >= 0) {
                 uint8_t* ks = smem + stage * T::kStage;
                 sm100::mbar_arrive_expect_tx(&full[stage], T::kStage);
 #pragma unroll
                 for (int c = 0; c < T::kBoxes; ++c) {
-                  sm100::tma_load_4d(ks + c * kBlock * 128, &tm_k, &full[stage], c * (KV8 ? D : 64), kvh, 0, id, pol);
-                  sm100::tma_load_4d(ks + T::kBytes + c * kBlock * 128, &tm_v, &full[stage], c * (KV8 ? D : 64), kvh, 0,
+                  sm100::tma_load_4d(ks + c * kBlock * 128, &tm_k, &full[stage], c * 64, kvh, 0, id, pol);
+                  sm100::tma_load_4d(ks + T::kBytes + c * kBlock * 128, &tm_v, &full[stage], c * 64, kvh, 0,
                                      id, pol);
                 }
                 last_parity[stage] = (int)phase;
@@ -260,7 +211,7 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
   uint32_t qa[D / 16][4];
   float o[D / 8][4];
   float m_lo, m_hi, l_lo, l_hi;           // running maxima (log2 units, scaled) and this lane's part of the sums
-  float f_lo = p.sm_scale * kLog2e, f_hi = f_lo;   // 8-bit: times the power of two taken out of the row of Q
+  const float f = p.sm_scale * kLog2e;
   int tile = 0;                           // n % key_parts == kp: this part's tiles
 
   auto clear = [&]() {
@@ -314,39 +265,19 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
   auto consume = [&](int page, int ctx, auto masked_c) {
     constexpr bool kMasked = decltype(masked_c)::value;
     const uint32_t kbase = sm100::smem_u32(smem + stage * T::kStage), vbase = kbase + T::kBytes;
-    const float2 sc = stage_scale[stage];
     float s[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-    if constexpr (KV8) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
+    for (int kk = 0; kk < D / 16; ++kk) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t w[4];
-          mma::ldsm_x4(kbase + T::at(n * 8 + (lane & 7), c * 4 + mi), w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t b0, b1;
-            cvt_e4m3x4(w[x], b0, b1);
-            mma_f16_16816(s[n], qa[c * 4 + x], b0, b1);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t b0, b1, b2, b3;
-          mma::ldsm_x4(kbase + T::at(np * 16 + (mi >> 1) * 8 + (lane & 7), kk * 2 + (mi & 1)), b0, b1, b2, b3);
-          mma::mma_bf16_16816(s[2 * np], qa[kk], b0, b1);
-          mma::mma_bf16_16816(s[2 * np + 1], qa[kk], b2, b3);
-        }
+      for (int np = 0; np < 4; ++np) {
+        uint32_t b0, b1, b2, b3;
+        mma::ldsm_x4(kbase + T::at(np * 16 + (mi >> 1) * 8 + (lane & 7), kk * 2 + (mi & 1)), b0, b1, b2, b3);
+        mma::mma_bf16_16816(s[2 * np], qa[kk], b0, b1);
+        mma::mma_bf16_16816(s[2 * np + 1], qa[kk], b2, b3);
       }
     }
-    // (a factor of 0 would turn a hidden -inf into NaN; scores that small are 0 all the same)
-    const float fl = KV8 ? fmaxf(f_lo * sc.x, 1e-36f) : f_lo, fh = KV8 ? fmaxf(f_hi * sc.x, 1e-36f) : f_hi;
     if constexpr (kMasked) {
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
@@ -367,88 +298,48 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 2));
     x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 1));
     x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 2));
-    const float n_lo = fmaxf(m_lo, x_lo * fl), n_hi = fmaxf(m_hi, x_hi * fh);
+    const float n_lo = fmaxf(m_lo, x_lo * f), n_hi = fmaxf(m_hi, x_hi * f);
     const float z_lo = n_lo == -INFINITY ? 0.0f : n_lo, z_hi = n_hi == -INFINITY ? 0.0f : n_hi;
     const float k_lo = ex2(m_lo - z_lo), k_hi = ex2(m_hi - z_hi);
     m_lo = n_lo;
     m_hi = n_hi;
-    constexpr float kUp = KV8 ? (float)kPShift : 0.0f;
     float t_lo = 0.0f, t_hi = 0.0f;
     uint32_t pa[4][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const float p0 = ex2(fmaf(s[n][0], fl, kUp - z_lo)), p1 = ex2(fmaf(s[n][1], fl, kUp - z_lo));
-      const float p2 = ex2(fmaf(s[n][2], fh, kUp - z_hi)), p3 = ex2(fmaf(s[n][3], fh, kUp - z_hi));
+      const float p0 = ex2(fmaf(s[n][0], f, -z_lo)), p1 = ex2(fmaf(s[n][1], f, -z_lo));
+      const float p2 = ex2(fmaf(s[n][2], f, -z_hi)), p3 = ex2(fmaf(s[n][3], f, -z_hi));
       t_lo += p0 + p1;
       t_hi += p2 + p3;
-      pa[n >> 1][(n & 1) * 2] = KV8 ? pack_f16(p0, p1) : mma::pack_bf16(p0, p1);
-      pa[n >> 1][(n & 1) * 2 + 1] = KV8 ? pack_f16(p2, p3) : mma::pack_bf16(p2, p3);
+      pa[n >> 1][(n & 1) * 2] = mma::pack_bf16(p0, p1);
+      pa[n >> 1][(n & 1) * 2 + 1] = mma::pack_bf16(p2, p3);
     }
     l_lo = l_lo * k_lo + t_lo;
     l_hi = l_hi * k_hi + t_hi;
     bool out_of = false;
-    if constexpr (KV8) {
-      const float v = sc.y;
+    if (__any_sync(0xffffffffu, k_lo != 1.0f || k_hi != 1.0f)) {
 #pragma unroll
-      for (int c2 = 0; c2 < D / 32; ++c2) {       // two 16-dim chunks at a time
-        float y[4][4];                             // chunk 0 even dims, odd dims, chunk 1 even, odd
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];                           // chunk 0 keys 0-7, 8-15, chunk 1 keys 0-7, 8-15
-          mma::ldsm_x4_trans(vbase + T::at(k * 16 + (mi & 1) * 8 + (lane & 7), c2 * 2 + (mi >> 1)), w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = __byte_perm(w[x], 0, 0x3120);   // pairs of keys: even dim, odd dim
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t e0, e1, d0, d1;
-            cvt_e4m3x4(w[2 * x], e0, d0);
-            cvt_e4m3x4(w[2 * x + 1], e1, d1);
-            if constexpr (kMasked) {
-              out_of |= take_out<true>(e0);
-              out_of |= take_out<true>(e1);
-              out_of |= take_out<true>(d0);
-              out_of |= take_out<true>(d1);
-            }
-            mma_f16_16816(y[2 * x], pa[k], e0, e1);
-            mma_f16_16816(y[2 * x + 1], pa[k], d0, d1);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float(&a)[4] = o[c2 * 4 + i];
-          a[0] = fmaf(a[0], k_lo, y[i][0] * v);
-          a[1] = fmaf(a[1], k_lo, y[i][1] * v);
-          a[2] = fmaf(a[2], k_hi, y[i][2] * v);
-          a[3] = fmaf(a[3], k_hi, y[i][3] * v);
-        }
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= k_lo;
+        o[i][1] *= k_lo;
+        o[i][2] *= k_hi;
+        o[i][3] *= k_hi;
       }
-    } else {
-      if (__any_sync(0xffffffffu, k_lo != 1.0f || k_hi != 1.0f)) {
+    }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= k_lo;
-          o[i][1] *= k_lo;
-          o[i][2] *= k_hi;
-          o[i][3] *= k_hi;
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int dp = 0; dp < D / 16; ++dp) {
+        uint32_t b0, b1, b2, b3;
+        mma::ldsm_x4_trans(vbase + T::at(k * 16 + (mi & 1) * 8 + (lane & 7), dp * 2 + (mi >> 1)), b0, b1, b2, b3);
+        if constexpr (kMasked) {
+          out_of |= take_out(b0);
+          out_of |= take_out(b1);
+          out_of |= take_out(b2);
+          out_of |= take_out(b3);
         }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int dp = 0; dp < D / 16; ++dp) {
-          uint32_t b0, b1, b2, b3;
-          mma::ldsm_x4_trans(vbase + T::at(k * 16 + (mi & 1) * 8 + (lane & 7), dp * 2 + (mi >> 1)), b0, b1, b2, b3);
-          if constexpr (kMasked) {
-            out_of |= take_out<false>(b0);
-            out_of |= take_out<false>(b1);
-            out_of |= take_out<false>(b2);
-            out_of |= take_out<false>(b3);
-          }
-          mma::mma_bf16_16816(o[2 * dp], pa[k], b0, b1);
-          mma::mma_bf16_16816(o[2 * dp + 1], pa[k], b2, b3);
-        }
+        mma::mma_bf16_16816(o[2 * dp], pa[k], b0, b1);
+        mma::mma_bf16_16816(o[2 * dp + 1], pa[k], b2, b3);
       }
     }
     if constexpr (kMasked) {
@@ -463,10 +354,8 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               // the dim of o[i][e] and o[i][e + 2]
-              const int dim = KV8 ? (i >> 1) * 16 + 4 * t + 2 * e + (i & 1) : i * 8 + 2 * t + e;
-              float v;
-              if constexpr (KV8) v = (vt[T::at(key, dim / 16) + dim % 16] & 127) == 127 ? NAN : 0.0f;
-              else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt + T::at(key, dim / 8) + dim % 8 * 2));
+              const int dim = i * 8 + 2 * t + e;
+              const float v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt + T::at(key, dim / 8) + dim % 8 * 2));
               if (!(fabsf(v) <= FLT_MAX)) {
                 if (see_lo) o[i][e] += v;
                 if (see_hi) o[i][e + 2] += v;
@@ -486,48 +375,14 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
     const int64_t row0 = (int64_t)b * p.R * p.Hq;
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q);
-    if constexpr (KV8) {
-      uint2 w[2][D / 16];
+    const uint32_t* lo = reinterpret_cast<const uint32_t*>(qp + (row0 + q_lo) * D);
+    const uint32_t* hi = reinterpret_cast<const uint32_t*>(qp + (row0 + q_hi) * D);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        w[0][kk] = __ldg(reinterpret_cast<const uint2*>(qp + (row0 + q_lo) * D + kk * 16 + 4 * t));
-        w[1][kk] = __ldg(reinterpret_cast<const uint2*>(qp + (row0 + q_hi) * D + kk * 16 + 4 * t));
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float top = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t v = e == 0 ? w[x][kk].x : w[x][kk].y;
-            const float a = fabsf(__uint_as_float(v << 16)), c = fabsf(__uint_as_float(v & 0xffff0000u));
-            top = fmaxf(top, fmaxf(a <= FLT_MAX ? a : 0.0f, c <= FLT_MAX ? c : 0.0f));
-          }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e with the row's largest value in [2^14, 2^15) after division; e >= -100 keeps the factors in range
-        const int e = top > 0.0f ? max(-100, (int)(__float_as_uint(top) >> 23) - 127 - 14) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        (x == 0 ? f_lo : f_hi) = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint2 v = w[x][kk];
-          qa[kk][x] = pack_f16(__uint_as_float(v.x << 16) * down, __uint_as_float(v.x & 0xffff0000u) * down);
-          qa[kk][x + 2] = pack_f16(__uint_as_float(v.y << 16) * down, __uint_as_float(v.y & 0xffff0000u) * down);
-        }
-      }
-    } else {
-      const uint32_t* lo = reinterpret_cast<const uint32_t*>(qp + (row0 + q_lo) * D);
-      const uint32_t* hi = reinterpret_cast<const uint32_t*>(qp + (row0 + q_hi) * D);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        qa[kk][0] = __ldg(lo + kk * 8 + t);
-        qa[kk][1] = __ldg(hi + kk * 8 + t);
-        qa[kk][2] = __ldg(lo + kk * 8 + 4 + t);
-        qa[kk][3] = __ldg(hi + kk * 8 + 4 + t);
-      }
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qa[kk][0] = __ldg(lo + kk * 8 + t);
+      qa[kk][1] = __ldg(hi + kk * 8 + t);
+      qa[kk][2] = __ldg(lo + kk * 8 + 4 + t);
+      qa[kk][3] = __ldg(hi + kk * 8 + 4 + t);
     }
     clear();
 
@@ -601,26 +456,12 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
       const float v_lo = l_lo == 0.0f ? 0.0f : 1.0f / l_lo, v_hi = l_hi == 0.0f ? 0.0f : 1.0f / l_hi;
       __nv_bfloat16* out_lo = static_cast<__nv_bfloat16*>(p.out) + (row0 + q_lo) * D;
       __nv_bfloat16* out_hi = static_cast<__nv_bfloat16*>(p.out) + (row0 + q_hi) * D;
-      if constexpr (KV8) {
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {       // four consecutive dims: even and odd tile interleaved
-          float(&e)[4] = o[2 * c];
-          float(&d)[4] = o[2 * c + 1];
-          if (r_lo < p.rows)
-            *reinterpret_cast<uint2*>(out_lo + c * 16 + 4 * t) =
-                make_uint2(mma::pack_bf16(e[0] * v_lo, d[0] * v_lo), mma::pack_bf16(e[1] * v_lo, d[1] * v_lo));
-          if (r_hi < p.rows)
-            *reinterpret_cast<uint2*>(out_hi + c * 16 + 4 * t) =
-                make_uint2(mma::pack_bf16(e[2] * v_hi, d[2] * v_hi), mma::pack_bf16(e[3] * v_hi, d[3] * v_hi));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          if (r_lo < p.rows)
-            *reinterpret_cast<uint32_t*>(out_lo + i * 8 + 2 * t) = mma::pack_bf16(o[i][0] * v_lo, o[i][1] * v_lo);
-          if (r_hi < p.rows)
-            *reinterpret_cast<uint32_t*>(out_hi + i * 8 + 2 * t) = mma::pack_bf16(o[i][2] * v_hi, o[i][3] * v_hi);
-        }
+      for (int i = 0; i < D / 8; ++i) {
+        if (r_lo < p.rows)
+          *reinterpret_cast<uint32_t*>(out_lo + i * 8 + 2 * t) = mma::pack_bf16(o[i][0] * v_lo, o[i][1] * v_lo);
+        if (r_hi < p.rows)
+          *reinterpret_cast<uint32_t*>(out_hi + i * 8 + 2 * t) = mma::pack_bf16(o[i][2] * v_hi, o[i][3] * v_hi);
       }
     }
   }
@@ -630,9 +471,9 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
 // A page of 64 keys keeps a warp busy for about as long as several pages take
 // to arrive, so a CTA (one per SM: 227 KB of stages) needs around 8 warps;
 // with few rows they come from key parts.
-template <int D, bool KV8>
+template <int D>
 void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
-  using T = Tile<D, KV8>;
+  using T = Tile<D>;
   const int blocks = (a.Hq / a.Hkv * (a.D + 1) + 15) / 16;     // of 16 rows
   pl->row_tiles = (blocks + kMaxWarps - 2) / (kMaxWarps - 1);
   pl->row_warps = (blocks + pl->row_tiles - 1) / pl->row_tiles;
@@ -641,7 +482,7 @@ void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
   // its phases one after the other, and two stages a part at least, so that
   // one fills while the other is read.
   for (pl->key_parts = (kMaxWarps - 1) / pl->row_warps;; --pl->key_parts) {
-    const int fixed = pl->row_warps * (pl->key_parts / 2) * (D / 2 + 4) * kWarp * 4 + kMaxStages * 28 + (kMaxWarps + 1) * 4 + 1024;
+    const int fixed = pl->row_warps * (pl->key_parts / 2) * (D / 2 + 4) * kWarp * 4 + kMaxStages * 20 + (kMaxWarps + 1) * 4 + 1024;
     pl->stages = std::min(kMaxStages, (kMaxSmem - fixed) / T::kStage) / pl->key_parts * pl->key_parts;
     pl->smem = pl->stages * T::kStage + fixed;
     if (pl->key_parts == 1 || pl->stages >= 2 * pl->key_parts) break;
@@ -650,36 +491,35 @@ void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
   pl->ctas_per_head = (int)std::max<long long>(1, sm_count / heads);
 }
 
-template <int D, bool KV8>
+template <int D>
 cudaError_t launch(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
   auto encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t elem = KV8 ? 1 : 2;
+  const cuuint64_t elem = 2;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)kBlock, (cuuint64_t)a.num_blocks};
   const cuuint64_t strides[3] = {D * elem, a.Hkv * D * elem, (cuuint64_t)kBlock * a.Hkv * D * elem};
-  const cuuint32_t box[4] = {KV8 ? (cuuint32_t)D : 64u, 1, (cuuint32_t)kBlock, 1};
+  const cuuint32_t box[4] = {64u, 1, (cuuint32_t)kBlock, 1};
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   CUtensorMap maps[2];
   for (int i = 0; i < 2; ++i) {
-    if (encode(&maps[i], KV8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+    if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                i == 0 ? a.k_cache : a.v_cache, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               Tile<D, KV8>::kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+  cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(pl.ctas_per_head * a.Hkv * pl.row_tiles);
-  window_mma_kernel<D, KV8><<<grid, (pl.row_warps * pl.key_parts + 1) * kWarp, pl.smem, s>>>(maps[0], maps[1], p);
-  return cudaGetLastError();
+  return launch_behind_append(window_mma_kernel<D>, grid, (pl.row_warps * pl.key_parts + 1) * kWarp, pl.smem, s, maps[0],
+                              maps[1], p);
 }
 
 }  // namespace
 
-WindowPlan plan_window_mma(const mtp_window_attn_args& a, bool kv8, int sm_count) {
+WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count) {
   WindowPlan pl{};
-  if (kv8) a.d == 128 ? layout<128, true>(a, sm_count, &pl) : layout<64, true>(a, sm_count, &pl);
-  else a.d == 128 ? layout<128, false>(a, sm_count, &pl) : layout<64, false>(a, sm_count, &pl);
+  a.d == 128 ? layout<128>(a, sm_count, &pl) : layout<64>(a, sm_count, &pl);
   const size_t rows = (size_t)a.Hkv * pl.row_tiles * pl.row_warps;     // row blocks of a request
   pl.ws_prefix = 0;
   pl.ws_arrived = ((size_t)(a.B + 1) * sizeof(int64_t) + 255) / 256 * 256;
@@ -689,10 +529,8 @@ WindowPlan plan_window_mma(const mtp_window_attn_args& a, bool kv8, int sm_count
   return pl;
 }
 
-cudaError_t launch_window_mma(const mtp_window_attn_args& a, bool kv8, const WindowPlan& pl, const WindowParams& p,
-                              cudaStream_t s) {
-  if (kv8) return a.d == 128 ? launch<128, true>(a, pl, p, s) : launch<64, true>(a, pl, p, s);
-  return a.d == 128 ? launch<128, false>(a, pl, p, s) : launch<64, false>(a, pl, p, s);
+cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
+  return a.d == 128 ? launch<128>(a, pl, p, s) : launch<64>(a, pl, p, s);
 }
 
 }  // namespace mtp

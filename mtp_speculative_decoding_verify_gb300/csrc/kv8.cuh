@@ -84,6 +84,13 @@ __host__ __device__ __forceinline__ PageSpan page_span(int ctx, int R, int windo
   return s;
 }
 
+// CTAs of a KV head that get work: all there are, as long as each has four
+// pages (a shared request costs a join, about as long as four pages take).
+__device__ __forceinline__ int window_ctas(int64_t total, int most) {
+  const int64_t want = (total + 3) / 4;
+  return (int)(want < most ? want : most);
+}
+
 // The work of one CTA of THREADS threads (a multiple of 32): see WindowSchedule.
 template <int THREADS>
 __device__ void window_schedule(const WindowSchedule& w) {
