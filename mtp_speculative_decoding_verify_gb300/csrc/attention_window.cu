@@ -179,14 +179,23 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
       l[x] = l[x] * c + warp_sum(p0 + p1);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[x][e] *= c;
+      const float* v = vs + lane * E;
+      if ((see[0] & see[1]) == 0xffffffffu) {
+#pragma unroll 8
+        for (int key = 0; key < kWarp; ++key) {
+          const float w0 = __shfl_sync(0xffffffffu, p0, key), w1 = __shfl_sync(0xffffffffu, p1, key);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        for (unsigned left = see[y]; left != 0; left &= left - 1) {
-          const int key = __ffs(left) - 1;
-          const float w = __shfl_sync(0xffffffffu, y == 0 ? p0 : p1, key);
-          const float* v = vs + (key + y * kWarp) * D + lane * E;
+          for (int e = 0; e < E; ++e) o[x][e] += w0 * v[key * D + e] + w1 * v[(key + kWarp) * D + e];
+        }
+      } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[x][e] += w * v[e];
+        for (int y = 0; y < 2; ++y) {
+          for (unsigned left = see[y]; left != 0; left &= left - 1) {
+            const int key = __ffs(left) - 1;
+            const float w = __shfl_sync(0xffffffffu, y == 0 ? p0 : p1, key);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[x][e] += w * v[(key + y * kWarp) * D + e];
+          }
         }
       }
     }
@@ -317,11 +326,12 @@ WindowPlan plan_window(const mtp_window_attn_args& a, bool kv8, int sm_count) {
   WindowPlan p{};
   const int rows = a.Hq / a.Hkv * (a.D + 1);
   const long long ctas = (long long)a.B * a.Hkv * ((rows + kSimtRows - 1) / kSimtRows);
-  // Two CTAs an SM where the batch alone has fewer, and at least two pages a split.
+  // Two CTAs an SM where the batch alone has fewer, and at least four pages a
+  // split (about what the merge's launch costs).
   const long long pages = a.window == 0 ? a.max_blocks
                                         : std::min<long long>(a.max_blocks, ((long long)a.window + a.sinks) / kBlock + 3);
   const long long want = std::max<long long>(1, (2ll * sm_count + ctas - 1) / std::max(ctas, 1ll));
-  p.n_splits = (int)std::max<long long>(1, std::min({want, (pages + 1) / 2, 64ll}));
+  p.n_splits = (int)std::max<long long>(1, std::min({want, pages / 4, 64ll}));
   p.ws_bytes = 256;
   if (p.n_splits > 1) {
     const size_t n = (size_t)a.B * (a.D + 1) * a.Hq * p.n_splits;

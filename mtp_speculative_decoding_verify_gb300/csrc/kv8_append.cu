@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   static_assert(TEAM % LANES == 0 && ROWS >= 1, "a token row is read by one team");
   __shared__ float s_max[kThreads / kWarp];
   const int tid = threadIdx.x % TEAM;
+  asm volatile("griddepcontrol.launch_dependents;");   // (an attention behind it may set up)
 
   if (p.schedule.prefix != nullptr && blockIdx.x == gridDim.x - 1) {
     window_schedule<kThreads>(p.schedule);
