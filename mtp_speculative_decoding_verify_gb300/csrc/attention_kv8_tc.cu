@@ -283,18 +283,6 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t addr) {
 }
 
 // --------------------------------------------------------------- work shares
-__device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_t pos, int lane) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + kWarp - 1) / kWarp;
-    const int b = lo + lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, lane == 0 || (b < hi && __ldg(prefix + b) <= pos));
-    lo += (31 - __clz(m)) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 // The part of a request that this CTA does: pages i0 .. i1-1 of its n, the
 // first of which is page p0 of the line; n = 0 ends the work.
 struct Seg {
@@ -353,17 +341,11 @@ __device__ __forceinline__ float* part_slot(const WindowParams& p, int gg, int w
   return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * p.row_tiles + row_tile) * ((size_t)NRB * 16 * (D + 2));
 }
 
-// The CTAs that share a request: of pages p0 and p0 + n - 1 of the line.
-__device__ __forceinline__ void sharers(const Seg& seg, int G, int64_t total, int* g0, int* g1) {
-  *g0 = (int)(((seg.p0 + 1) * G - 1) / total);
-  *g1 = (int)(((seg.p0 + seg.n) * G - 1) / total);
-}
-
 // Count this CTA's part as left; true for the last of them. One thread, after
 // all that wrote the part have met it at a barrier.
-__device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int G, int64_t total) {
-  int g0, g1;
-  sharers(seg, G, total, &g0, &g1);
+__device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& seg, int kvh, int row_tile) {
+  const int2 in = __ldg(p.sharers + seg.b);
+  const int g0 = in.x, g1 = in.y;
   __threadfence();
   const int before = atomicAdd(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile, 1);
   __threadfence();
@@ -372,9 +354,9 @@ __device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& se
 
 // Join the parts of a request, in the order of the CTAs. Thread t of n.
 template <int D, int NRB>
-__device__ void join_parts(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int G, int64_t total, int t, int n) {
-  int g0, g1;
-  sharers(seg, G, total, &g0, &g1);
+__device__ void join_parts(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int t, int n) {
+  const int2 in = __ldg(p.sharers + seg.b);
+  const int g0 = in.x, g1 = in.y;
   const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
   const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
   for (int u = t; u < n_rows * (D / 4); u += n) {
@@ -477,9 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Everything up to here may run while the append still does; what follows
   // reads what it writes.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t total = __ldg(p.prefix + p.B);
-  const int G = window_ctas(total, gridDim.x / heads);
-  if (g_cta >= G) return;
+  // (this CTA's share and the next one's begin are read at once; the last begin read is within the array)
+  const int n_shares = __ldg(&p.shares[0].pad);
+  const Share share = p.shares[g_cta];
+  const int64_t t_end = p.shares[g_cta + 1].begin;
+  if (g_cta >= n_shares) return;
   if (warp == 0) {
     sm100::tmem_alloc(tmem_slot, 512);
     sm100::tmem_relinquish();
@@ -592,8 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
     // ----------------------------------------------------------------- TMA
     const uint64_t pol = sm100::l2_policy_evict_first();
-    const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
-    Walk walk{p, t_begin, t_end, find_request(p.prefix, p.B, t_begin, lane)};
+    Walk walk{p, share.begin, t_end, share.b};
     int g = 0;
     Seg seg;
     for (int sn = 0; ok; ++sn) {
@@ -914,9 +897,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       if (!whole) {
         soft_sync();
-        if (st == 0) *last_flag = arrive_part(p, seg, kvh, row_tile, G, total);
+        if (st == 0) *last_flag = arrive_part(p, seg, kvh, row_tile);
         soft_sync();
-        if (*last_flag) join_parts<D, NRB>(p, seg, kvh, row_tile, G, total, st, 256);
+        if (*last_flag) join_parts<D, NRB>(p, seg, kvh, row_tile, st, 256);
       }
       soft_sync();                                             // red, the flag and the bitmap have been read
       if (st < 64) nanmap[(sn % kNanSegs) * 64 + st] = 0;
@@ -1102,9 +1085,7 @@ WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count) {
   pl.row_warps = 1;                                        // arrival counters per (request, KV head, row tile)
   pl.ctas_per_head = (int)std::max<long long>(1, sm_count / ((long long)a.Hkv * pl.row_tiles));
   const size_t heads = (size_t)a.Hkv * pl.row_tiles;
-  pl.ws_prefix = 0;
-  pl.ws_arrived = ((size_t)(a.B + 1) * sizeof(int64_t) + 255) / 256 * 256;
-  pl.ws_partial_o = pl.ws_arrived + ((size_t)a.B * heads * sizeof(int32_t) + 255) / 256 * 256;
+  pl.ws_partial_o = plan_schedule(&pl, a.B, a.Hkv);
   pl.ws_bytes = pl.ws_partial_o + (size_t)pl.ctas_per_head * 2 * heads * nrb * 16 * (a.d + 2) * sizeof(float);
   pl.ws_bytes = (pl.ws_bytes + 255) / 256 * 256;
   return pl;

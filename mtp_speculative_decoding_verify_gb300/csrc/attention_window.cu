@@ -427,7 +427,10 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
     p.key_parts = pl.key_parts;
     p.stages = pl.stages;
     sch.prefix = reinterpret_cast<int64_t*>(static_cast<char*>(a->workspace) + pl.ws_prefix);
+    sch.shares = reinterpret_cast<Share*>(static_cast<char*>(a->workspace) + pl.ws_shares);
+    sch.sharers = reinterpret_cast<int2*>(static_cast<char*>(a->workspace) + pl.ws_sharers);
     sch.arrived = reinterpret_cast<int32_t*>(static_cast<char*>(a->workspace) + pl.ws_arrived);
+    sch.ctas = pl.ctas_per_head;
     sch.n_arrived = (int64_t)p.B * p.Hkv * pl.row_tiles * pl.row_warps;
     sch.ctx_lens = p.ctx_lens;
     sch.B = p.B;
@@ -436,6 +439,8 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
     sch.window = p.window;
     sch.sinks = p.sinks;
     p.prefix = sch.prefix;
+    p.shares = sch.shares;
+    p.sharers = sch.sharers;
     p.arrived = sch.arrived;
   }
   cudaError_t e = append(*a, kv8, sch, err, s);

@@ -5,16 +5,13 @@
 // m16n8k16). Pages arrive by TMA in a ring of shared-memory stages that one
 // warp fills; a page of one KV head (64 keys) is a tile.
 //
-// What bounds it is the read of the cache, so the work is cut into equal
-// numbers of pages, whatever the lengths: the pages that the requests' rows
-// see, request after request, form one line per KV head (its prefix sums
-// come with the append launch), and CTA g of G takes pages [g T / G,
-// (g+1) T / G) of it. A CTA crosses from one request to the next without
-// draining its ring. A request that several CTAs share is joined by the last
-// of them to finish, in the order of the pages, so the result does not depend
-// on who that is. G x KV heads CTAs fill the device once; the KV heads of the
-// same pages run side by side, which keeps their interleaved rows together
-// in DRAM.
+// What bounds it is the read of the cache, so the work is cut into shares of
+// the same number of pages, whatever the lengths (Share). A CTA crosses from
+// one request to the next without draining its ring. A request that several
+// CTAs share is joined by the last of them to finish, in the order of the
+// pages, so the result does not depend on who that is. CTAs x KV heads fill
+// the device once; the KV heads of the same pages run side by side, which
+// keeps their interleaved rows together in DRAM.
 //
 // A warp takes 16 query rows (row warp) and every key_parts-th tile; the
 // parts join in shared memory at the end of a request. Registers hold Q, the
@@ -73,19 +70,6 @@ __device__ __forceinline__ bool take_out(uint32_t& w) {
   return keep != 0xffffffffu;
 }
 
-// The request that page `pos` of the line belongs to: prefix[b] <= pos < prefix[b+1].
-__device__ __forceinline__ int find_request(const int64_t* prefix, int B, int64_t pos, int lane) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + kWarp - 1) / kWarp;
-    const int b = lo + lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, lane == 0 || (b < hi && __ldg(prefix + b) <= pos));
-    lo += (31 - __clz(m)) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     window_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -120,12 +104,12 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
   // Everything up to here may run while the append still does; what follows
   // reads what it writes.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t total = __ldg(p.prefix + p.B);
-  const int G = window_ctas(total, gridDim.x / heads);                      // every CTA g < G has a page
-  if (g_cta >= G) return;
-  const int64_t t_begin = total * g_cta / G, t_end = total * (g_cta + 1) / G;
+  const int n_shares = __ldg(&p.shares[0].pad);
+  const Share share = p.shares[g_cta];
+  const int64_t t_begin = share.begin, t_end = p.shares[g_cta + 1].begin;
+  if (g_cta >= n_shares) return;
+  int b = share.b;
 
-  int b = find_request(p.prefix, p.B, t_begin, lane);
   int stage = 0;             // of tile n (counted over the CTA's life): n % stages
   uint32_t phase = 0;
 
@@ -418,7 +402,8 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
       // Shared with other CTAs: leave the partial result, and the last to
       // arrive at this (request, KV head, row block) joins them all. Slot 0
       // of a CTA is for a request it did not begin, slot 1 for one it began.
-      const int g0 = (int)(((p0 + 1) * G - 1) / total), g1 = (int)((p1 * G - 1) / total);   // CTAs of pages p0, p1 - 1
+      const int2 in = __ldg(p.sharers + b);
+      const int g0 = in.x, g1 = in.y;
       const size_t stride = (size_t)kVals * kWarp;
       auto slot_of = [&](int gg, int which) {
         return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * row_blocks + row_block) * stride + lane;
@@ -521,9 +506,7 @@ WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count) {
   WindowPlan pl{};
   a.d == 128 ? layout<128>(a, sm_count, &pl) : layout<64>(a, sm_count, &pl);
   const size_t rows = (size_t)a.Hkv * pl.row_tiles * pl.row_warps;     // row blocks of a request
-  pl.ws_prefix = 0;
-  pl.ws_arrived = ((size_t)(a.B + 1) * sizeof(int64_t) + 255) / 256 * 256;
-  pl.ws_partial_o = pl.ws_arrived + ((size_t)a.B * rows * sizeof(int32_t) + 255) / 256 * 256;
+  pl.ws_partial_o = plan_schedule(&pl, a.B, a.Hkv);
   pl.ws_bytes = pl.ws_partial_o + (size_t)pl.ctas_per_head * 2 * rows * (a.d / 2 + 4) * kWarp * sizeof(float);
   pl.ws_bytes = (pl.ws_bytes + 255) / 256 * 256;
   return pl;

@@ -84,11 +84,51 @@ __host__ __device__ __forceinline__ PageSpan page_span(int ctx, int R, int windo
   return s;
 }
 
-// CTAs of a KV head that get work: all there are, as long as each has four
-// pages (a shared request costs a join, about as long as four pages take).
-__device__ __forceinline__ int window_ctas(int64_t total, int most) {
-  const int64_t want = (total + 3) / 4;
-  return (int)(want < most ? want : most);
+// ----------------------------------------------------------- shares of work
+struct Cuts {
+  int64_t total;   // pages of the line
+  int G;           // shares: all CTAs that there are, as long as each has eight pages
+  int near;        // pages that a cut moves at most: less than half a share, so that none is empty, and no more
+                   // than a moved cut saves (none for shares over 64 pages)
+  __device__ __forceinline__ int64_t even(int64_t g) const { return total * g / G; }
+};
+
+__device__ __forceinline__ Cuts make_cuts(int64_t total, int ctas) {
+  Cuts c;
+  c.total = total;
+  const int64_t want = (total + 7) / 8;
+  c.G = (int)(want < ctas ? want : ctas);
+  const int64_t share = c.G == 0 ? 0 : total / c.G;
+  c.near = share == 0 || share > 64 ? 0 : (int)(share > 8 ? 4 : (share - 1) / 2);
+  return c;
+}
+
+// Where share g begins, and (an early bound of) its request.
+__device__ __forceinline__ Share share_begin(const Cuts& c, const int64_t* prefix, int B, int g) {
+  Share s{};
+  s.begin = c.total;
+  if (g == 0) s.begin = 0;
+  if (g == 0 || g >= c.G) return s;
+  const int64_t pos = c.even(g);
+  int lo = 0, hi = B;              // prefix[lo] <= pos < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (prefix[mid] <= pos) lo = mid;
+    else hi = mid;
+  }
+  const int64_t p0 = prefix[lo], p1 = prefix[lo + 1];
+  s.begin = pos - p0 <= c.near ? p0 : p1 - pos <= c.near ? p1 : pos;
+  s.b = lo;
+  return s;
+}
+
+// The first and last share that a request of pages p0 .. p1 - 1 of the line is in.
+__device__ __forceinline__ int2 request_shares(const Cuts& c, int64_t p0, int64_t p1) {
+  int a = (int)(((p0 + 1) * c.G - 1) / c.total), z = (int)((p1 * c.G - 1) / c.total);   // of even cuts
+  if (a + 1 < c.G && c.even(a + 1) < p1 && c.even(a + 1) - p0 <= c.near) ++a;            // the cut after p0 moved to p0
+  const int64_t cut = c.even(z);
+  if (z > 0 && cut >= p0 && cut - p0 > c.near && p1 - cut <= c.near) --z;                // the last one moved to p1
+  return make_int2(a, z);
 }
 
 // The work of one CTA of THREADS threads (a multiple of 32): see WindowSchedule.
@@ -120,6 +160,17 @@ __device__ void window_schedule(const WindowSchedule& w) {
     if (b < w.B) w.prefix[b + 1] = n;
   }
   if (threadIdx.x == 0) w.prefix[0] = 0;
+  __syncthreads();                         // (writes to global memory too, for this CTA)
+  const Cuts cuts = make_cuts(base, w.ctas);
+  for (int g = threadIdx.x; g <= cuts.G; g += THREADS) {
+    Share sh = share_begin(cuts, w.prefix, w.B, g);
+    sh.pad = cuts.G;
+    w.shares[g] = sh;
+  }
+  for (int b = threadIdx.x; b < w.B; b += THREADS) {
+    const int64_t p0 = w.prefix[b], p1 = w.prefix[b + 1];
+    if (p1 > p0) w.sharers[b] = request_shares(cuts, p0, p1);
+  }
   for (int64_t i = threadIdx.x; i < w.n_arrived; i += THREADS) w.arrived[i] = 0;
 }
 
