@@ -14,8 +14,8 @@
 //               where these rests pass 2^-19 of the row's sum.
 //   O += P V    p = hi + lo / 16: 8 bits, as bf16 would keep.
 // No operand is converted in shared memory, whose bandwidth is what two
-// products with f16 values of V would run out of (measured: 112 us where this
-// takes half).
+// products with f16 values of V run out of (32 requests x 48 rows, 4096
+// tokens: 112 us with V converted to f16, 68 us with the first form of this).
 //
 // M = 128 TMEM lanes. Lanes 32 w .. 32 w + 15, of warp w, hold a block of 16
 // query rows as hi, lanes 32 w + 16 .. the same rows as lo: one MMA gives
@@ -25,15 +25,17 @@
 // row of every warp is an online softmax of its own, and warps exchange
 // nothing until the request ends. The 16x32bx2 form of the TMEM loads and
 // stores gives the threads t and t + 16 of a warp two column ranges of one
-// lane: they share a row and halve its keys (16 NRB each) and output dims,
-// with a shuffle for the common maximum.
+// lane: they share a row and halve its keys and output dims, with a shuffle
+// for the common maximum.
 //
 // A row's probabilities are 2^(score + log2(v scale) - ref): the block's
 // scale of V rides along, and the sum, which is kept relative to a maximum of
 // scores alone, divides it out again. e4m3 holds 2^-9 (lo: 2^-13) to 2^8, so
 // ref follows the tiles up and down: when a tile's largest probability would
-// pass 2^8, or was below 2^-4 for three of the row's tiles, O is rescaled in TMEM. (Down, so that a few large scores do not cost the rest of the
-// context its bits; O in fp32 has room for the 60 octaves that are allowed.)
+// pass 2^8, or those of three of the row's tiles in turn were below 2^-4, O is
+// rescaled in TMEM. (Down, so that a few large scores do not cost the rest of
+// the context its bits; O in fp32 has room for the 60 octaves that are
+// allowed.)
 //
 // Two groups of four softmax warps share the work, each with an O of its own
 // (joined with the rest when the request ends); P lies in the columns of the S
@@ -101,8 +103,8 @@ struct Smem {
   static constexpr int kNan = kFac + kSegs * 64 * 4;      // [kNanSegs][16][4] words
   static constexpr int kBar = kNan + kNanSegs * 16 * 4 * 4;
   static constexpr int kBars = 2 * kKStages + 3 * kVStages + 2 + 2 + 4 + 4 + kInfo + kSegs + kSegRing;
-  static constexpr int kMisc = kBar + kBars * 8;          // rest flags [kSegs][2], join flag, abort, TMEM base
-  static constexpr int kBytes = kMisc + kSegs * 8 + 16 + 1024;
+  static constexpr int kMisc = kBar + kBars * 8;          // rest flags [kSegs], join flag, abort, TMEM base
+  static constexpr int kBytes = kMisc + kSegs * 4 + 16 + 1024;
   // byte offset of 16-byte chunk c of row r of a K-major operand tile, as TMA swizzles it
   __device__ __forceinline__ static uint32_t at(int r, int c) {
     if constexpr (D == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
@@ -286,28 +288,30 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t addr) {
 // The part of a request that this CTA does: pages i0 .. i1-1 of its n, the
 // first of which is page p0 of the line; n = 0 ends the work.
 struct Seg {
-  int b, i0, i1, n, ctx, pad;
-  int64_t p0;
+  int b, i0, i1, n, ctx;
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == n; }
   __device__ __forceinline__ int tiles() const { return (i1 - i0 + 1) / 2; }
 };
 
-// Walks the segments of pages [pos, end) in order.
+// Walks the segments of pages [pos, end) in order, from a place in request b
+// (pages p0 .. p1 - 1, context ctx) on.
 struct Walk {
   const WindowParams& p;
-  int64_t pos, end;
-  int b;
+  int pos, end, p0, p1, b, ctx;
   __device__ __forceinline__ bool next(Seg& s) {
     if (pos >= end) return false;
-    while (__ldg(p.prefix + b + 1) <= pos) ++b;
+    while (p1 <= pos) {
+      ++b;
+      ctx = __ldg(p.ctx_lens + b);
+      p0 = p1;
+      p1 = __ldcg(p.prefix + b + 1);
+    }
     s.b = b;
-    s.p0 = __ldg(p.prefix + b);
-    const int64_t p1 = __ldg(p.prefix + b + 1);
-    s.ctx = __ldg(p.ctx_lens + b);
-    s.i0 = (int)(pos - s.p0);
-    s.i1 = (int)(min(end, p1) - s.p0);
-    s.n = (int)(p1 - s.p0);
-    pos = s.p0 + s.i1;
+    s.ctx = ctx;
+    s.i0 = pos - p0;
+    s.i1 = min(end, p1) - p0;
+    s.n = p1 - p0;
+    pos = p0 + s.i1;
     return true;
   }
 };
@@ -334,8 +338,9 @@ __device__ __forceinline__ uint32_t hide_nan(const WindowParams& p, uint32_t w, 
 }
 
 // Where CTA gg of a KV head leaves its part of a request: slot 0 for one it
-// did not begin, slot 1 for one it began. [rows][D] values, then (maximum,
-// sum) of each row.
+// did not begin, slot 1 for one it began. [rows][D] values, divided by their
+// sum (so that V's largest values stay finite), then (maximum, sum) of each
+// row.
 template <int D, int NRB>
 __device__ __forceinline__ float* part_slot(const WindowParams& p, int gg, int which, int kvh, int row_tile) {
   return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * p.row_tiles + row_tile) * ((size_t)NRB * 16 * (D + 2));
@@ -344,7 +349,7 @@ __device__ __forceinline__ float* part_slot(const WindowParams& p, int gg, int w
 // Count this CTA's part as left; true for the last of them. One thread, after
 // all that wrote the part have met it at a barrier.
 __device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& seg, int kvh, int row_tile) {
-  const int2 in = __ldg(p.sharers + seg.b);
+  const int2 in = __ldcg(p.sharers + seg.b);
   const int g0 = in.x, g1 = in.y;
   __threadfence();
   const int before = atomicAdd(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile, 1);
@@ -355,29 +360,29 @@ __device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& se
 // Join the parts of a request, in the order of the CTAs. Thread t of n.
 template <int D, int NRB>
 __device__ void join_parts(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int t, int n) {
-  const int2 in = __ldg(p.sharers + seg.b);
+  const int2 in = __ldcg(p.sharers + seg.b);
   const int g0 = in.x, g1 = in.y;
   const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
   const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
   for (int u = t; u < n_rows * (D / 4); u += n) {
     const int local = u / (D / 4), dim = u % (D / 4) * 4;
-    float m = -INFINITY, l = 0.0f;
-    for (int gg = g0; gg <= g1; ++gg)
-      m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(part_slot<D, NRB>(p, gg, gg == g0, kvh, row_tile) + NRB * 16 * D) + local).x);
+    float m = -INFINITY, l = 0.0f;                             // maximum, sum and mean of the parts so far
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int gg = g0; gg <= g1; ++gg) {
       const float* from = part_slot<D, NRB>(p, gg, gg == g0, kvh, row_tile);
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + NRB * 16 * D) + local);
       const float4 o4 = __ldcg(reinterpret_cast<const float4*>(from + (size_t)local * D + dim));
-      const float c = ml.x == -INFINITY ? 1.0f : ex2(ml.x - m);   // (nothing seen: zeros, or NaN)
-      l += ml.y * c;
-      v.x += o4.x * c, v.y += o4.y * c, v.z += o4.z * c, v.w += o4.w * c;
+      const float top = fmaxf(m, ml.x);                        // (-inf: nothing seen, and sums of 0 or NaN)
+      const float a = m == top ? l : l * ex2(m - top), b = ml.x == top ? ml.y : ml.y * ex2(ml.x - top);
+      m = top;
+      l = a + b;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, ca = a * inv, cb = b * inv;
+      v.x = v.x * ca + o4.x * cb, v.y = v.y * ca + o4.y * cb, v.z = v.z * ca + o4.z * cb, v.w = v.w * ca + o4.w * cb;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int row = first_row + local;
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (out0 + (int64_t)(row / p.group) * p.Hq + row % p.group) * D + dim;
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
   }
 }
 
@@ -414,9 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* seg_full = fac_full + kSegs;    // [kSegRing]
   Seg* ring = reinterpret_cast<Seg*>(smem + S::kRing);
   volatile int* rest = reinterpret_cast<volatile int*>(smem + S::kMisc);   // [kSegs] the third term of Q is needed
-  volatile int* last_flag = rest + kSegs * 2;
+  volatile int* last_flag = rest + kSegs;
   volatile int* abort = last_flag + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc + kSegs * 8 + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc + kSegs * 4 + 8);
 
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int heads = p.Hkv * p.row_tiles;
@@ -435,10 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     sm100::mbar_init(q_full, 128);
     sm100::mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) sm100::mbar_init(&s_full[i], 1);
     for (int i = 0; i < 4; ++i) {
-      if (i < 2) {
-        sm100::mbar_init(&s_full[i], 1);
-      }
       sm100::mbar_init(&p_full[i], 4);
       sm100::mbar_init(&pv_done[i], 1);
     }
@@ -457,13 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *reinterpret_cast<uint4*>(smem + S::kQ + S::kTile + i * 16) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
   // Everything up to here may run while the append still does; what follows
-  // reads what it writes.
+  // reads what it writes (which the read-only path may not: __ldcg).
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (this CTA's share and the next one's begin are read at once; the last begin read is within the array)
-  const int n_shares = __ldg(&p.shares[0].pad);
-  const Share share = p.shares[g_cta];
-  const int64_t t_end = p.shares[g_cta + 1].begin;
-  if (g_cta >= n_shares) return;
+  const Share share = load_share(p.shares, g_cta);
+  const int t_end = share_end(p.shares, g_cta);
+  if (g_cta >= share_count(p.shares)) return;
   if (warp == 0) {
     sm100::tmem_alloc(tmem_slot, 512);
     sm100::tmem_relinquish();
@@ -574,95 +575,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else {
-    // ----------------------------------------------------------------- TMA
-    const uint64_t pol = sm100::l2_policy_evict_first();
-    Walk walk{p, share.begin, t_end, share.b};
-    int g = 0;
-    Seg seg;
-    for (int sn = 0; ok; ++sn) {
-      if (!walk.next(seg)) seg.n = 0;
-      if (lane == 0) {
-        ring[sn % kSegRing] = seg;
-        sm100::mbar_arrive(&seg_full[sn % kSegRing]);
-      }
-      if (seg.n == 0) break;
-      const PageSpan span = page_span(seg.ctx, p.R, p.window, p.sinks);
-      for (int i = seg.i0; i < seg.i1 && ok; i += kWarp) {
-        int blk = -1, page = -1;
-        float sk = 1.0f, lsv = 0.0f;
-        if (i + lane < seg.i1) {
-          page = span.page(i + lane);
-          blk = p.block_table[(int64_t)seg.b * p.max_blocks + page];
-          if (blk < 0 || blk >= p.num_blocks) {
-            raise_error(p.err, MTP_ERR_BLOCK_ID);
-            page = -1;
-          } else {
-            sk = p.k_scale[(int64_t)blk * p.Hkv + kvh];
-            const float sv = p.v_scale[(int64_t)blk * p.Hkv + kvh];
-            if (!scale_ok(sk) || !scale_ok(sv)) {
-              raise_error(p.err, MTP_ERR_SCALE);
+      // ----------------------------------------------------------------- TMA
+      const uint64_t pol = sm100::l2_policy_evict_first();
+      Walk walk{p, share.begin, t_end, share.p0, share.p0 + share.n, share.b, share.ctx};
+      int g = 0;
+      Seg seg;
+      for (int sn = 0; ok; ++sn) {
+        if (!walk.next(seg)) seg.n = 0;
+        if (lane == 0) {
+          ring[sn % kSegRing] = seg;
+          sm100::mbar_arrive(&seg_full[sn % kSegRing]);
+        }
+        if (seg.n == 0) break;
+        const PageSpan span = page_span(seg.ctx, p.R, p.window, p.sinks);
+        for (int i = seg.i0; i < seg.i1 && ok; i += kWarp) {
+          int blk = -1, page = -1;
+          float sk = 1.0f, lsv = 0.0f;
+          if (i + lane < seg.i1) {
+            page = span.page(i + lane);
+            blk = p.block_table[(int64_t)seg.b * p.max_blocks + page];
+            if (blk < 0 || blk >= p.num_blocks) {
+              raise_error(p.err, MTP_ERR_BLOCK_ID);
               page = -1;
-              sk = 1.0f;
             } else {
-              lsv = log2f(sv);
-              if (!page_whole(p, page, seg.ctx)) page = -2 - page;
+              sk = __ldcg(p.k_scale + (int64_t)blk * p.Hkv + kvh);
+              const float sv = __ldcg(p.v_scale + (int64_t)blk * p.Hkv + kvh);
+              if (!scale_ok(sk) || !scale_ok(sv)) {
+                raise_error(p.err, MTP_ERR_SCALE);
+                page = -1;
+                sk = 1.0f;
+              } else {
+                lsv = log2f(sv);
+                if (!page_whole(p, page, seg.ctx)) page = -2 - page;
+              }
             }
           }
-        }
-        const int n = min(kWarp, seg.i1 - i);
-        for (int x = 0; x < n; x += 2, ++g) {
-          TileInfo in;
-          int id[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {        // (lane 31 of an odd rest has page -1)
-            id[y] = __shfl_sync(0xffffffffu, blk, x + y);
-            in.page[y].mark = __shfl_sync(0xffffffffu, page, x + y);
-            in.page[y].sk = __shfl_sync(0xffffffffu, sk, x + y);
-            in.page[y].lsv = __shfl_sync(0xffffffffu, lsv, x + y);
-          }
-          int go = 1;
-          if (lane == 0) {
-            const int s = g % kKStages, vs = g % kVStages;
-            const uint32_t bytes = ((in.page[0].mark != -1) + (in.page[1].mark != -1)) * (uint32_t)(S::kTile / 2);
-            go = sm100::mbar_wait(&k_empty[s], (uint32_t)((g / kKStages) & 1) ^ 1u, abort);
-            if (go) {
-              info[g % kInfo] = in;
-              sm100::mbar_arrive(&info_full[g % kInfo]);
-              if (bytes) sm100::mbar_arrive_expect_tx(&k_full[s], bytes);
-              else sm100::mbar_arrive(&k_full[s]);
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (in.page[y].mark != -1)
-                  sm100::tma_load_4d(smem + S::kK + s * S::kTile + y * (S::kTile / 2), &tm_k, &k_full[s], 0, kvh, 0, id[y], pol);
-              go = sm100::mbar_wait(&v_empty[vs], (uint32_t)((g / kVStages) & 1) ^ 1u, abort);
+          const int n = min(kWarp, seg.i1 - i);
+          for (int x = 0; x < n; x += 2, ++g) {
+            TileInfo in;
+            int id[2];
+  #pragma unroll
+            for (int y = 0; y < 2; ++y) {        // (lane 31 of an odd rest has page -1)
+              id[y] = __shfl_sync(0xffffffffu, blk, x + y);
+              in.page[y].mark = __shfl_sync(0xffffffffu, page, x + y);
+              in.page[y].sk = __shfl_sync(0xffffffffu, sk, x + y);
+              in.page[y].lsv = __shfl_sync(0xffffffffu, lsv, x + y);
             }
-            if (go) {
-              if (bytes) sm100::mbar_arrive_expect_tx(&v_full[vs], bytes);
-              else sm100::mbar_arrive(&v_full[vs]);
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (in.page[y].mark != -1)
-                  sm100::tma_load_4d(smem + S::kV + vs * S::kTile + y * (S::kTile / 2), &tm_v, &v_full[vs], 0, kvh, 0, id[y], pol);
-            } else {
-              *abort = 1;
-              raise_error(p.err, MTP_ERR_TIMEOUT);
+            int go = 1;
+            if (lane == 0) {
+              const int s = g % kKStages, vs = g % kVStages;
+              const uint32_t bytes = ((in.page[0].mark != -1) + (in.page[1].mark != -1)) * (uint32_t)(S::kTile / 2);
+              go = sm100::mbar_wait(&k_empty[s], (uint32_t)((g / kKStages) & 1) ^ 1u, abort);
+              if (go) {
+                info[g % kInfo] = in;
+                sm100::mbar_arrive(&info_full[g % kInfo]);
+                if (bytes) sm100::mbar_arrive_expect_tx(&k_full[s], bytes);
+                else sm100::mbar_arrive(&k_full[s]);
+  #pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  if (in.page[y].mark != -1)
+                    sm100::tma_load_4d(smem + S::kK + s * S::kTile + y * (S::kTile / 2), &tm_k, &k_full[s], 0, kvh, 0, id[y], pol);
+                go = sm100::mbar_wait(&v_empty[vs], (uint32_t)((g / kVStages) & 1) ^ 1u, abort);
+              }
+              if (go) {
+                if (bytes) sm100::mbar_arrive_expect_tx(&v_full[vs], bytes);
+                else sm100::mbar_arrive(&v_full[vs]);
+  #pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  if (in.page[y].mark != -1)
+                    sm100::tma_load_4d(smem + S::kV + vs * S::kTile + y * (S::kTile / 2), &tm_v, &v_full[vs], 0, kvh, 0, id[y], pol);
+              } else {
+                *abort = 1;
+                raise_error(p.err, MTP_ERR_TIMEOUT);
+              }
             }
+            ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+            if (!ok) break;
           }
-          ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-          if (!ok) break;
         }
       }
-    }
-    // Every copy issued lands before the CTA may exit: the last fill of each
-    // stage (after a timeout the K copy of tile g may be on its way too; each
-    // wait is bounded).
-    if (lane == 0) {
-      const int nk = ok ? g : g + 1;
-      for (int x = max(0, nk - kKStages); x < nk; ++x)
-        sm100::mbar_wait_timeout(&k_full[x % kKStages], (uint32_t)((x / kKStages) & 1), ok ? sm100::kWaitTimeoutNs : 1000000);
-      for (int x = max(0, g - kVStages); x < g; ++x)
-        sm100::mbar_wait_timeout(&v_full[x % kVStages], (uint32_t)((x / kVStages) & 1), ok ? sm100::kWaitTimeoutNs : 1000000);
-    }
+      // Every copy issued lands before the CTA may exit: the last fill of each
+      // stage (after a timeout the K copy of tile g may be on its way too; each
+      // wait is bounded).
+      if (lane == 0) {
+        const int nk = ok ? g : g + 1;
+        for (int x = max(0, nk - kKStages); x < nk; ++x)
+          sm100::mbar_wait_timeout(&k_full[x % kKStages], (uint32_t)((x / kKStages) & 1), ok ? sm100::kWaitTimeoutNs : 1000000);
+        for (int x = max(0, g - kVStages); x < g; ++x)
+          sm100::mbar_wait_timeout(&v_full[x % kVStages], (uint32_t)((x / kVStages) & 1), ok ? sm100::kWaitTimeoutNs : 1000000);
+      }
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int mark = in.mark;
         if (mark < 0) {
-          const int slot = (mark < 0 ? -2 - mark : mark) * kBlock + in_page, top = mark == -1 ? INT_MIN : pos;
+          const int slot = (-2 - mark) * kBlock + in_page, top = mark == -1 ? INT_MIN : pos;
 #pragma unroll
           for (int k = 0; k < NK; ++k)
             if (!(slot + k <= top && (slot + k >= low || slot + k < p.sinks))) x[k] = -INFINITY;
@@ -729,8 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // (a row with nothing visible in the tile stays as it is)
         const float to = fmaxf(most - (ref == -INFINITY ? kFirstP : most > ref ? kUpP : kDownP), top_ref - kDown);
-        const bool low = most < ref + kLeastP && most != -INFINITY;
-        low_tiles = low ? low_tiles + 1 : 0;
+        low_tiles = most < ref + kLeastP && most != -INFINITY ? low_tiles + 1 : 0;
         const bool move = most > ref + kMostP || (low_tiles >= kLowTiles && to < ref - 1.0f);
         if (__any_sync(0xffffffffu, move)) {
           const float c = !move ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - to);
@@ -808,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         L += v.y * (v.x == -INFINITY ? 1.0f : ex2(v.x - M));   // (nothing seen: 0, or NaN from K)
       }
       const bool whole = seg.whole();
-      const float own = (ref == -INFINITY ? 0.0f : ex2(ref - M)) * (whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f);
+      // (two factors: V's scale is in the second, and their product may leave fp32's range where a result does not)
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L, own = ex2(ref - M);
       const float poison = sum != sum ? sum : 0.0f;            // NaN in K: every dim of the row
       const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
       const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           // (nothing seen: the lane's O may be anything, so it takes no part)
-          y[k] = own == 0.0f || !ok ? 0.0f : fmaf(y2[k], 1.0f / kLoScale, y[k]) * own;
+          y[k] = ref == -INFINITY || !ok ? 0.0f : fmaf(y2[k], 1.0f / kLoScale, y[k]) * inv * own;
           if ((bits >> k) & 1) y[k] = NAN;
           y[k] += poison;
         }

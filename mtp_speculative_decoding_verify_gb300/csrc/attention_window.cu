@@ -302,9 +302,14 @@ int check_window(const mtp_window_attn_args* a, bool kv8) {
     snprintf(buf, sizeof buf, "%s: head dim must be 64 or 128", name);
     return set_error(MTP_UNSUPPORTED, buf);
   }
-  if ((long long)a->B * (a->D + 1) * a->Hq > (1 << 29) || a->Hq / a->Hkv > (1 << 16)) {
+  if ((long long)a->B * (a->D + 1) * a->Hq > (1 << 29) || a->Hq / a->Hkv > (1 << 15)) {
     char buf[128];
-    snprintf(buf, sizeof buf, "%s: B x R x Hq > 2^29, or Hq / Hkv > 2^16", name);
+    snprintf(buf, sizeof buf, "%s: B x R x Hq > 2^29, or Hq / Hkv > 2^15", name);
+    return set_error(MTP_UNSUPPORTED, buf);
+  }
+  if ((long long)a->B * a->max_blocks > 0x7fffffffll) {
+    char buf[128];
+    snprintf(buf, sizeof buf, "%s: B x max_blocks >= 2^31", name);
     return set_error(MTP_UNSUPPORTED, buf);
   }
   if (a->B == 0) return MTP_OK;
@@ -426,7 +431,7 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
     p.row_warps = pl.row_warps;
     p.key_parts = pl.key_parts;
     p.stages = pl.stages;
-    sch.prefix = reinterpret_cast<int64_t*>(static_cast<char*>(a->workspace) + pl.ws_prefix);
+    sch.prefix = reinterpret_cast<int32_t*>(static_cast<char*>(a->workspace) + pl.ws_prefix);
     sch.shares = reinterpret_cast<Share*>(static_cast<char*>(a->workspace) + pl.ws_shares);
     sch.sharers = reinterpret_cast<int2*>(static_cast<char*>(a->workspace) + pl.ws_sharers);
     sch.arrived = reinterpret_cast<int32_t*>(static_cast<char*>(a->workspace) + pl.ws_arrived);

@@ -19,12 +19,16 @@ struct WindowPlan {
 // its CTAs. Cuts are even, except that those of small shares move to a border
 // of two requests that is near: a request that several CTAs share is joined at
 // the end, which takes about as long as four pages, and so does beginning one
-// (5 windowed requests of 8 pages: 24.6 us with even cuts, 16.4 us so).
+// (5 windowed requests of 8 pages: 24.6 us with even cuts, 16.4 us so). For
+// the same reason each request is a share where there are CTAs for all and the
+// longest is no more than four pages over an even share (16 requests of 17 or
+// 18 pages on 19 CTAs a head: 30.0 us with cuts, 24.4 us so).
 // The append launch works this out in one more CTA (window_schedule) and
 // clears the arrival counters of shared requests.
-struct Share {
-  int64_t begin;                    // its first page of the line
-  int32_t b, pad;                   // (an early bound of) that page's request
+struct alignas(16) Share {
+  int32_t begin, p0;                // its first page of the line; the first one of that page's request,
+  int32_t b, n, ctx;                // .. which has n pages and a context of ctx
+  int32_t count;                    // of shares
 };
 struct WindowParams {
   const void* q;
@@ -33,7 +37,7 @@ struct WindowParams {
   const float *k_scale, *v_scale;   // [num_blocks, Hkv], nullptr: the cache holds the rows' type
   const int32_t *block_table, *ctx_lens;
   float *part_o, *part_lse;         // SIMT: [row][split][d], [row][split] (base 2); tensor cores: see the kernel
-  const int64_t* prefix;            // see WindowSchedule
+  const int32_t* prefix;            // see WindowSchedule
   const Share* shares;
   const int2* sharers;
   int32_t* arrived;                 // [B][Hkv][row blocks] CTAs that have left a partial result
@@ -45,8 +49,8 @@ struct WindowParams {
 };
 
 struct WindowSchedule {
-  int64_t* prefix;                  // [B+1] pages of the requests before each; nullptr: nothing to prepare
-  Share* shares;                    // [ctas + 1]; shares[0].pad is their number G, shares[G].begin the line's end
+  int32_t* prefix;                  // [B+1] pages of the requests before each; nullptr: nothing to prepare
+  Share* shares;                    // [ctas + 1]; the one after the last begins at the line's end
   int2* sharers;                    // [B] first and last share that a request is in
   int32_t* arrived;
   int64_t n_arrived;
@@ -58,7 +62,7 @@ struct WindowSchedule {
 inline size_t plan_schedule(WindowPlan* pl, int B, int Hkv) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   pl->ws_prefix = 0;
-  pl->ws_shares = up((size_t)(B + 1) * sizeof(int64_t));
+  pl->ws_shares = up((size_t)(B + 1) * sizeof(int32_t));
   pl->ws_sharers = pl->ws_shares + up((size_t)(pl->ctas_per_head + 1) * sizeof(Share));
   pl->ws_arrived = pl->ws_sharers + up((size_t)B * sizeof(int2));
   return pl->ws_arrived + up((size_t)B * Hkv * pl->row_tiles * pl->row_warps * sizeof(int32_t));

@@ -104,11 +104,29 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
   // Everything up to here may run while the append still does; what follows
   // reads what it writes.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_shares = __ldg(&p.shares[0].pad);
-  const Share share = p.shares[g_cta];
-  const int64_t t_begin = share.begin, t_end = p.shares[g_cta + 1].begin;
-  if (g_cta >= n_shares) return;
-  int b = share.b;
+  const Share share = load_share(p.shares, g_cta);
+  const int t_end = share_end(p.shares, g_cta);
+  if (g_cta >= share_count(p.shares)) return;
+  // The request that is walked, pages p0 .. p1 - 1 of the line; the next one's
+  // end and context are read while it is.
+  int b = share.b, ctx = share.ctx, pos = share.begin, p0 = share.p0, p1 = p0 + share.n;
+  int next_p1 = 0, next_ctx = 0;
+  auto read_next = [&]() {
+    if (b + 1 < p.B) {
+      next_ctx = __ldg(p.ctx_lens + b + 1);
+      next_p1 = __ldcg(p.prefix + b + 2);
+    }
+  };
+  read_next();
+  auto find = [&]() {
+    while (p1 <= pos) {
+      ++b;
+      p0 = p1;
+      p1 = next_p1;
+      ctx = next_ctx;
+      read_next();
+    }
+  };
 
   int stage = 0;             // of tile n (counted over the CTA's life): n % stages
   uint32_t phase = 0;
@@ -122,12 +140,11 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
 #pragma unroll
     for (int s = 0; s < kMaxStages; ++s) last_parity[s] = -1;
     bool ok = true;
-    for (int64_t pos = t_begin; pos < t_end && ok;) {
-      while (__ldg(p.prefix + b + 1) <= pos) ++b;
-      const int64_t p0 = __ldg(p.prefix + b), p1 = __ldg(p.prefix + b + 1);
-      const int i1 = (int)(min(t_end, p1) - p0);
-      const PageSpan span = page_span(p.ctx_lens[b], p.R, p.window, p.sinks);
-      for (int i = (int)(pos - p0); i < i1 && ok; i += kWarp) {
+    while (pos < t_end && ok) {
+      find();
+      const int i1 = min(t_end, p1) - p0;
+      const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
+      for (int i = pos - p0; i < i1 && ok; i += kWarp) {
         int blk = -1;
         if (i + lane < i1) {
           blk = p.block_table[(int64_t)b * p.max_blocks + span.page(i + lane)];
@@ -351,11 +368,9 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     }
   };
 
-  for (int64_t pos = t_begin; pos < t_end;) {
-    while (__ldg(p.prefix + b + 1) <= pos) ++b;
-    const int64_t p0 = __ldg(p.prefix + b), p1 = __ldg(p.prefix + b + 1);
-    const int i0 = (int)(pos - p0), i1 = (int)(min(t_end, p1) - p0), n_tiles = (int)(p1 - p0);
-    const int ctx = p.ctx_lens[b];
+  while (pos < t_end) {
+    find();
+    const int i0 = pos - p0, i1 = min(t_end, p1) - p0, n_tiles = p1 - p0;
     const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
     const int64_t row0 = (int64_t)b * p.R * p.Hq;
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q);
@@ -402,7 +417,7 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
       // Shared with other CTAs: leave the partial result, and the last to
       // arrive at this (request, KV head, row block) joins them all. Slot 0
       // of a CTA is for a request it did not begin, slot 1 for one it began.
-      const int2 in = __ldg(p.sharers + b);
+      const int2 in = __ldcg(p.sharers + b);
       const int g0 = in.x, g1 = in.y;
       const size_t stride = (size_t)kVals * kWarp;
       auto slot_of = [&](int gg, int which) {
