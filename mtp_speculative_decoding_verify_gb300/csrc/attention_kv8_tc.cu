@@ -828,13 +828,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm100::tmem_ld_wait();
         }
         const int dim0 = half * (D / 2) + c * 16;
-        const uint32_t bits = nanmap[((sn % kNanSegs) * 16 + j) * 4 + (dim0 >> 5)] >> (dim0 & 31);
+        const uint32_t bits = nanmap[((sn % kNanSegs) * 16 + j) * 4 + (dim0 >> 5)] >> (dim0 & 31) & 0xffffu;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           // (nothing seen: the lane's O may be anything, so it takes no part)
           y[k] = ref == -INFINITY || !ok ? 0.0f : fmaf(y2[k], 1.0f / kLoScale, y[k]) * inv * own;
-          if ((bits >> k) & 1) y[k] = NAN;
-          y[k] += poison;
+        }
+        if (__any_sync(0xffffffffu, bits != 0 || poison != 0.0f)) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) y[k] += ((bits >> k) & 1) ? NAN : poison;
         }
       };
       // four dims of a row whose output starts at `to`
