@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               sm100::tc_fence_after();
             }
-#pragma unroll 2
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {               // this thread's half of the row's dims, 16 at a time
               float o[16], o2[16];
               ld_halves<16, D / 2>(o_hi + q * 16, o);
