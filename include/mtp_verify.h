@@ -83,7 +83,7 @@ typedef enum { MTP_F32 = 0, MTP_BF16 = 1 } mtp_dtype;
 #define MTP_ERR_TIMEOUT    0x20u /* a bounded wait inside a kernel gave up */
 #define MTP_ERR_MODE       0x40u /* mode > 2, or mode 2 while relaxed_topk is 0 (decided greedily) */
 #define MTP_ERR_TREE       0x80u /* malformed parents list (that request is treated as a chain) */
-#define MTP_ERR_SCALE      0x100u /* scale of a partly filled 8-bit block is not positive and finite */
+#define MTP_ERR_SCALE      0x100u /* scale of an 8-bit block outside [2^-100, 2^121) */
 
 /* ------------------------------------------------------------------------ */
 /* 1. Verify attention with KV append.
@@ -402,18 +402,20 @@ int kv_rollback(const mtp_rollback_args* args, void* stream);
  *        (exact unless a byte becomes subnormal); slots behind the last
  *        written one keep their bytes, which no row sees.
  * A written byte is e4m3(x / scale), to nearest even; x that is not finite
- * is stored as NaN and reaches the rows that see it. No two requests' slots
- * may share a block that is written.
+ * is stored as NaN and reaches the rows that see it. Scales so made lie in
+ * [2^-100, 2^121). No two requests' slots may share a block that is written.
  *   k_new, v_new [T, Hkv, d] dtype (MTP_F32 or MTP_BF16), d 64 or 128
- *   starts       [B+1] int32, not decreasing, within [0, T]
+ *   starts       [B+1] int32, not decreasing, within [0, T] (else requests
+ *                after a bad one may be left out too)
  *   k_cache, v_cache [num_blocks, 64, Hkv, d] e4m3 bytes
  *   k_scale, v_scale [num_blocks, Hkv] float
  *   block_table [B, max_blocks] int32;  ctx_lens [B] int32
- * k_new, v_new and the caches must be 16-byte aligned. Errors: a request with
- * bad starts or slots beyond max_blocks sets MTP_ERR_LENGTH, a block id
- * outside [0, num_blocks) MTP_ERR_BLOCK_ID, an old scale that is needed and
- * not positive and finite MTP_ERR_SCALE; that request's (block's, head's)
- * tokens are not written. */
+ * k_new, v_new and the caches must be 16-byte aligned; Hkv <= 2^16,
+ * max_blocks <= 2^24, (T/64 + 2B) Hkv <= 2^30. Errors: a request with bad
+ * starts or slots beyond max_blocks sets MTP_ERR_LENGTH, a block id outside
+ * [0, num_blocks) MTP_ERR_BLOCK_ID, an old scale that is needed and outside
+ * that range MTP_ERR_SCALE; that request's (block's, head's) tokens are not
+ * written. */
 typedef struct {
   const void* k_new;
   const void* v_new;
@@ -443,18 +445,25 @@ int mtp_kv8_append(const mtp_kv8_append_args* args, void* stream);
  * tokens. mtp_verify_attention_window is the same over the cache of
  * mtp_verify_attention (K/V in `dtype`, k_scale and v_scale NULL) and needs
  * window >= 1. A block no row sees is not read, and its table entry may be
- * anything (kv_window_release sets it to -1). Sums and softmax statistics are
- * fp32; with bf16 rows the probabilities of a tile are rounded to 16 bits
- * before they meet V.
+ * anything (kv_window_release sets it to -1). Full blocks may be in the tables
+ * of several requests. Sums and softmax statistics are fp32. With bf16 rows a
+ * probability keeps 8 bits, as bf16 or as two e4m3 terms (kv8; those below
+ * 2^-10 of the largest nearby keep fewer); kv8 takes Q as two or three 8-bit
+ * terms, exact to 2^-21 of the row's largest value. Infinities and NaN that a
+ * row sees act as in the formula; those in slots that it does not see do
+ * nothing.
  *   q, out       [B, R, Hq, d] dtype (MTP_F32 or MTP_BF16), d 64 or 128
  *   k_new, v_new [B, R, Hkv, d] dtype
  *   k_cache, v_cache [num_blocks, 64, Hkv, d] e4m3 bytes (kv8) or dtype
  *   k_scale, v_scale [num_blocks, Hkv] float (kv8) or NULL
- * R = D+1 <= 16, Hq % Hkv == 0. q, out, k_new, v_new and the caches must be
- * 16-byte aligned. Errors are those of the append and of
+ * R = D+1 <= 16, Hq % Hkv == 0, Hkv <= 2^16, Hq / Hkv <= 2^15, max_blocks <=
+ * 2^24, B max_blocks < 2^31, B R Hq <= 2^29. q, out, k_new, v_new and the
+ * caches must be 16-byte aligned; a workspace is always needed, and one call at
+ * a time may use it. Errors are those of the append and of
  * mtp_verify_attention: a request of bad length is skipped (its rows of out
- * stay as they were), a block with a bad id takes no part. Trees of drafts and MLA are not
- * provided in these forms. */
+ * stay as they were); a block with a bad id, or (kv8: MTP_ERR_SCALE; for that
+ * head) a scale outside [2^-100, 2^121), takes no part, and a row that sees
+ * nothing else is 0. Trees of drafts and MLA are not provided in these forms. */
 typedef struct {
   const void* q;
   const void* k_new;
@@ -492,6 +501,7 @@ int mtp_verify_attention_window(const mtp_window_attn_args* args, void* stream);
  * kv_rollback, one whose blocks do not fit after those of every earlier
  * request stays as it was and sets MTP_ERR_FREE_LIST. L < 0 or beyond
  * max_blocks sets MTP_ERR_LENGTH and skips the request.
+ * No block may be in two requests' tables.
  *   block_table [B, max_blocks] int32 (in/out); seq_lens [B] int32
  *   free_list [free_capacity] int32; free_count [1] int32 (in/out)
  *   workspace: device, >= mtp_window_release_workspace_size(B) bytes, 256-byte aligned */

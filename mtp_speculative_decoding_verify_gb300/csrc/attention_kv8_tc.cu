@@ -43,12 +43,17 @@
 // buffer, so that one computes while the other waits for its products. With
 // more rows the softmax is the longer part: there each takes a page of every
 // tile, and both S buffers serve the two of them, so that the next S is there
-// before this softmax ends (64 requests x 48 rows, 4096 tokens: 184 us with
-// alternate tiles, 170 us with pages; 16 rows, 1k-32k: 350 us and 372 us).
+// before this softmax ends (64 requests x 48 rows, 4096 tokens: 161 us with
+// alternate tiles, 138 us with pages; 16 rows, 1k-32k: 338 us and 348 us).
 //
 // Hidden slots: only tiles with a slot that not every row sees are masked.
 // There V's bytes that are NaN become 0 in shared memory (0 x NaN), and a
 // bitmap of (verify token, dim) puts NaN back into the rows that do see them.
+//
+// Bound: the read of the cache (it holds at 16 rows: 345 us for 64 requests of
+// 1k-32k tokens, 95 % of the copy rate). At 48 rows the chain of a tile is
+// longer than its read (P V, then S of the tile that takes its buffer, and a
+// softmax of some 1500 cycles): 138 us for 64 requests of 4096 tokens, 59 %.
 //
 // Warps: 0 and 1 P V, 2 TMA (block ids and scales of 32 pages at a time, one a
 // lane), 3 S, 4-11 softmax and output, 12-15 masked V and the next request's
@@ -89,9 +94,9 @@ constexpr uint32_t kColO = 256;        // S (and P) buffers at columns 0 and 128
 template <int D>
 struct Smem {
   static constexpr int kTile = kKeys * D;                 // bytes of K or V of a tile
-  // Even: a stage of V then serves tiles of one softmax group only, whose P V warp meets its phases one after the other
-  // (a wait's parity tells only two apart).
-  // V is held longer (to P V, two tiles behind S).
+  // V is held longer (to P V, two tiles behind S). Its stages are even: where the groups take alternate tiles, a stage
+  // then serves one of them only, whose P V warp meets its phases one after the other (a wait's parity tells only two
+  // apart).
   static constexpr int kKStages = D == 128 ? 4 : 6, kVStages = 6;
   static constexpr int kK = 0, kV = kK + kKStages * kTile;
   static constexpr int kQ = kV + kVStages * kTile;         // hi and lo, rest
@@ -113,10 +118,9 @@ struct Smem {
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "227 KB of shared memory");
 
-struct PageInfo {
+struct alignas(16) PageInfo {
   float sk, lsv;             // scale of K, log2 of the scale of V
   int mark;                  // the page's index in the request; -2 - index: some row does not see all of it; -1: not loaded
-  int pad;
 };
 struct TileInfo {
   PageInfo page[2];
@@ -346,21 +350,9 @@ __device__ __forceinline__ float* part_slot(const WindowParams& p, int gg, int w
   return p.part_o + ((((size_t)gg * 2 + which) * p.Hkv + kvh) * p.row_tiles + row_tile) * ((size_t)NRB * 16 * (D + 2));
 }
 
-// Count this CTA's part as left; true for the last of them. One thread, after
-// all that wrote the part have met it at a barrier.
-__device__ __forceinline__ bool arrive_part(const WindowParams& p, const Seg& seg, int kvh, int row_tile) {
-  const int2 in = __ldcg(p.sharers + seg.b);
-  const int g0 = in.x, g1 = in.y;
-  __threadfence();
-  const int before = atomicAdd(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile, 1);
-  __threadfence();
-  return before == g1 - g0;
-}
-
 // Join the parts of a request, in the order of the CTAs. Thread t of n.
 template <int D, int NRB>
-__device__ void join_parts(const WindowParams& p, const Seg& seg, int kvh, int row_tile, int t, int n) {
-  const int2 in = __ldcg(p.sharers + seg.b);
+__device__ void join_parts(const WindowParams& p, const Seg& seg, int2 in, int kvh, int row_tile, int t, int n) {
   const int g0 = in.x, g1 = in.y;
   const int first_row = row_tile * 64, n_rows = min(NRB * 16, p.rows - first_row);
   const int64_t out0 = (int64_t)seg.b * p.R * p.Hq + kvh * p.group;
@@ -395,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kKStages = S::kKStages, kVStages = S::kVStages;
   constexpr int KG = 4 / NRB;            // key groups: warps that share a row block
   constexpr bool kPages = NRB == 4;      // the groups take pages instead of tiles
-  constexpr int NK = kPages ? 8 * NRB : 16 * NRB;   // keys of a tile that a thread takes
+  constexpr int NK = kPages ? 32 : 16 * NRB;        // keys of a tile that a thread takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* xbuf = reinterpret_cast<float*>(smem + S::kX);
@@ -459,12 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = threadIdx.x; i < S::kTile / 16; i += kThreads)   // the rest term has no second one
     *reinterpret_cast<uint4*>(smem + S::kQ + S::kTile + i * 16) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
-  // Everything up to here may run while the append still does; what follows
-  // reads what it writes (which the read-only path may not: __ldcg).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Share share = load_share(p.shares, g_cta);
-  const int t_end = share_end(p.shares, g_cta);
-  if (g_cta >= share_count(p.shares)) return;
   if (warp == 0) {
     sm100::tmem_alloc(tmem_slot, 512);
     sm100::tmem_relinquish();
@@ -473,6 +459,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Everything up to here may run while the append still does; what follows
+  // reads what it writes (which the read-only path may not: __ldcg).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Share share = load_share(p.shares, g_cta);
+  const int t_end = share_end(p.shares, g_cta);
+  if (g_cta >= share_count(p.shares)) {
+    __syncthreads();
+    if (warp == 0) sm100::tmem_dealloc(tmem, 512);
+    return;
+  }
   const uint32_t sbase = sm100::smem_u32(smem);
 
   // Registers: 128 a thread at launch; the softmax warps take what the others
@@ -697,16 +693,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const PageInfo in = info[g % kInfo].page[page_half];
         float x[NK];
         {
-          constexpr int N = NK < 32 ? NK : 32;
+          float y[NK];
+          ld_halves<NK, NK>(s_hi + kg * 2 * NK, x);
+          ld_halves<NK, NK>(s_lo + kg * 2 * NK, y);
+          sm100::tmem_ld_wait();
 #pragma unroll
-          for (int k0 = 0; k0 < NK; k0 += N) {
-            float y[N];
-            ld_halves<N, NK>(s_hi + kg * 2 * NK + k0, x + k0);
-            ld_halves<N, NK>(s_lo + kg * 2 * NK + k0, y);
-            sm100::tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < N; k += 2) add2(x[k0 + k], x[k0 + k + 1], y[k], y[k + 1]);
-          }
+          for (int k = 0; k < NK; k += 2) add2(x[k], x[k + 1], y[k], y[k + 1]);
         }
         const int mark = in.mark;
         if (mark < 0) {
@@ -808,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         L += v.y * (v.x == -INFINITY ? 1.0f : ex2(v.x - M));   // (nothing seen: 0, or NaN from K)
       }
       const bool whole = seg.whole();
+      const int2 in = whole ? make_int2(0, 0) : __ldcg(p.sharers + seg.b);
       // (two factors: V's scale is in the second, and their product may leave fp32's range where a result does not)
       const float inv = L == 0.0f ? 0.0f : 1.0f / L, own = ex2(ref - M);
       const float poison = sum != sum ? sum : 0.0f;            // NaN in K: every dim of the row
@@ -900,9 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       if (!whole) {
         soft_sync();
-        if (st == 0) *last_flag = arrive_part(p, seg, kvh, row_tile);
+        if (st == 0)
+          *last_flag = arrive_at(p.arrived + ((int64_t)seg.b * p.Hkv + kvh) * p.row_tiles + row_tile) == in.y - in.x;
         soft_sync();
-        if (*last_flag) join_parts<D, NRB>(p, seg, kvh, row_tile, st, 256);
+        if (*last_flag) join_parts<D, NRB>(p, seg, in, kvh, row_tile, st, 256);
       }
       soft_sync();                                             // red, the flag and the bitmap have been read
       if (st < 64) nanmap[(sn % kNanSegs) * 64 + st] = 0;

@@ -28,7 +28,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------- append
 // One CTA per (request, verify token): its K and V rows go to slot ctx+j of
-// the cache, 16 bytes a thread.
+// the cache, 16 bytes a thread. A chain of three loads bounds it, not bytes
+// (about 2 us, as the 8-bit append of such a step).
 __global__ void __launch_bounds__(128) window_append_kernel(const uint4* __restrict__ k_new,
                                                             const uint4* __restrict__ v_new, uint4* __restrict__ k_cache,
                                                             uint4* __restrict__ v_cache,
@@ -65,7 +66,9 @@ __global__ void __launch_bounds__(128) window_append_kernel(const uint4* __restr
 // rows padded by 16 bytes, so that 8 lanes reading 16 bytes of 8 keys hit
 // all banks). A warp owns two rows: for the scores each lane takes two keys,
 // for the output each lane D/32 values of the row. Sums and statistics are
-// fp32; the SIMT rate bounds it (fp32 is the type of checks and small models).
+// fp32; the SIMT rate bounds it (fp32 is the type of checks and small models),
+// and with little work the launches (4 requests of 128 tokens: 11.9 us, of
+// which the append is 4).
 constexpr int kSimtRows = 16, kSimtWarps = 8;
 
 template <typename T> struct KvLoad;
@@ -217,7 +220,8 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
   }
 }
 
-// out = sum_s 2^(lse_s - max) part_s / sum_s 2^(lse_s - max): one warp a row.
+// out = sum_s 2^(lse_s - max) part_s / sum_s 2^(lse_s - max): one warp a row
+// (few rows, a launch's latency bounds it).
 template <typename T, int D>
 __global__ void __launch_bounds__(128) window_merge_kernel(const WindowParams p, int64_t n_rows) {
   constexpr int E = D / kWarp;

@@ -16,13 +16,15 @@ struct WindowPlan {
 
 // How the pages that the requests' rows see are shared out. Request after
 // request they form one line for each KV head, cut into a share for each of
-// its CTAs. Cuts are even, except that those of small shares move to a border
-// of two requests that is near: a request that several CTAs share is joined at
-// the end, which takes about as long as four pages, and so does beginning one
-// (5 windowed requests of 8 pages: 24.6 us with even cuts, 16.4 us so). For
-// the same reason each request is a share where there are CTAs for all and the
-// longest is no more than four pages over an even share (16 requests of 17 or
-// 18 pages on 19 CTAs a head: 30.0 us with cuts, 24.4 us so).
+// its CTAs, of eight pages at least (4 to 16: within 1 us). Cuts are even,
+// except that those of small shares move to a border of two requests that is
+// near: a request that several CTAs share is joined at the end, which takes
+// about as long as four pages, and so does beginning one (5 windowed requests
+// of 8 pages: 20.1 us with even cuts, 12.8 us so). For the same reason each
+// request is a share where there are CTAs for all and the longest is no more
+// than four pages over an even share (16 requests of 17 or 18 pages on 19 CTAs
+// a head: 31.8 us with cuts, 24.4 us so), or has no more than 16 pages (one
+// request of 16 pages: 14.4 us in two shares, 13.7 us in one).
 // The append launch works this out in one more CTA (window_schedule) and
 // clears the arrival counters of shared requests.
 struct alignas(16) Share {

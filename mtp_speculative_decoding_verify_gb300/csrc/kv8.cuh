@@ -106,7 +106,7 @@ __device__ __forceinline__ Cuts make_cuts(int total, int ctas, int B, int longes
   c.size = c.G == 0 ? 0 : total / c.G;
   c.more = total - c.G * c.size;
   c.near = c.size == 0 || c.size > 64 ? 0 : c.size > 8 ? 4 : (c.size - 1) / 2;
-  c.whole = total > 0 && B <= ctas && longest <= c.size + 4;
+  c.whole = total > 0 && B <= ctas && longest <= max(c.size + 4, 16);
   if (c.whole) c.G = B;
   return c;
 }
@@ -142,6 +142,15 @@ __device__ __forceinline__ Share load_share(const Share* shares, int g) {
 }
 __device__ __forceinline__ int share_end(const Share* shares, int g) { return __ldcg(&shares[g + 1].begin); }
 __device__ __forceinline__ int share_count(const Share* shares) { return __ldcg(&shares[0].count); }
+
+// Count a part as left at *arrived; how many were before. One thread: what
+// others wrote before they met it is released with it, and what was left
+// before is there for those that meet it later.
+__device__ __forceinline__ int arrive_at(int32_t* arrived) {
+  int before;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(arrived) : "memory");
+  return before;
+}
 
 // The work of one CTA of THREADS threads (a multiple of 32): see WindowSchedule.
 // It stands between the lengths and the attention, and most of its time is the

@@ -12,7 +12,9 @@
 // (table entries >= 0 in the range), the second sums the counts of the
 // earlier requests to find its place and moves its entries with a scan over
 // each 1024. Both read the range once; the launches and the chain of
-// dependent loads bound it, not bytes.
+// dependent loads bound it, not bytes: 3.3 us for 16 requests of 129 blocks,
+// 10.1 us for 512 of 2048. (One CTA and one launch for small tables: 4.3 us for
+// the 16, 14 us for 63 requests of 130 blocks, which take 4.2 us so.)
 #include <algorithm>
 
 #include "common.cuh"
