@@ -1080,8 +1080,8 @@ WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count) {
   const int nrb = row_blocks(a);
   pl.row_tiles = (a.Hq / a.Hkv * (a.D + 1) + 63) / 64;
   pl.row_warps = 1;                                        // arrival counters per (request, KV head, row tile)
-  pl.ctas_per_head = (int)std::max<long long>(1, sm_count / ((long long)a.Hkv * pl.row_tiles));
   const size_t heads = (size_t)a.Hkv * pl.row_tiles;
+  pl.ctas_per_head = head_ctas(a, sm_count, (long long)heads);
   pl.ws_partial_o = plan_schedule(&pl, a.B, a.Hkv);
   pl.ws_bytes = pl.ws_partial_o + (size_t)pl.ctas_per_head * 2 * heads * nrb * 16 * (a.d + 2) * sizeof(float);
   pl.ws_bytes = (pl.ws_bytes + 255) / 256 * 256;

@@ -2,6 +2,9 @@
 // and the appends that run before them.
 #pragma once
 
+#include <algorithm>
+
+#include "common.cuh"
 #include "kernels.h"
 
 namespace mtp {
@@ -59,6 +62,16 @@ struct WindowSchedule {
   const int32_t* ctx_lens;
   int B, R, max_blocks, window, sinks, ctas;
 };
+
+// CTAs of a head (a KV head's tile of rows): those that fit the device once,
+// as far as the widest table gives them a request or eight pages each.
+inline int head_ctas(const mtp_window_attn_args& a, int sm_count, long long heads) {
+  const long long seen = a.window == 0 ? a.max_blocks   // pages that a request's rows see at most
+                                       : std::min<long long>(a.max_blocks, ((long long)a.window + a.D + 127) / kBlock +
+                                                                               ((long long)a.sinks + kBlock - 1) / kBlock);
+  const long long useful = std::max<long long>(a.B, (a.B * seen + 7) / 8);
+  return (int)std::max<long long>(1, std::min(sm_count / heads, useful));
+}
 
 // Lay the schedule out in the workspace of a plan whose ctas_per_head, row_tiles and row_warps are set.
 inline size_t plan_schedule(WindowPlan* pl, int B, int Hkv) {

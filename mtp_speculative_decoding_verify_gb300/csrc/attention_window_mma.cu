@@ -484,8 +484,7 @@ void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
     pl->smem = pl->stages * T::kStage + fixed;
     if (pl->key_parts == 1 || pl->stages >= 2 * pl->key_parts) break;
   }
-  const long long heads = (long long)a.Hkv * pl->row_tiles;
-  pl->ctas_per_head = (int)std::max<long long>(1, sm_count / heads);
+  pl->ctas_per_head = head_ctas(a, sm_count, (long long)a.Hkv * pl->row_tiles);
 }
 
 template <int D>
