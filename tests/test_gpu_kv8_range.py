@@ -248,3 +248,40 @@ def test_sizes_beyond_the_limits_are_refused(field, value):
         a.Hq, a.Hkv = (value, 2) if field == "Hq" else (value, value)
     assert L.mtp_attention_kv8_workspace_size(ctypes.byref(a)) == 0
     assert L.mtp_verify_attention_kv8(ctypes.byref(a), None) != 0
+
+
+@pytest.mark.parametrize("t,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("kv8", [True, False], ids=["kv8", "window"])
+def test_blocks_whose_offsets_pass_32_bits(kv8, t, d):
+    """The same call with every block moved to the end of a cache of more than 2^32 elements."""
+    c = Case(kv8, t, 2, 3, 16, 8, d, [300, 70], 0 if kv8 else 200, 0, seed=2, drop=False)
+    g, far = c.to_gpu(), c.to_gpu()
+    n = 2 ** 32 // (64 * 8 * d) + c.nb + 1
+    names = ("kc", "vc") + (("ks", "vs") if kv8 else ())
+    for name in names:
+        far[name] = torch.empty((n,) + g[name].shape[1:], dtype=g[name].dtype, device=DEV)
+        as_bytes = (lambda x: x.view(torch.uint8)) if name[1] == "c" and kv8 else (lambda x: x)
+        as_bytes(far[name])[n - c.nb:] = as_bytes(g[name]).flip(0)
+    far["table"] = torch.where(g["table"] < 0, g["table"], n - 1 - g["table"]).int()
+    c.call(g)
+    c.call(far)
+    mv.sync_status()
+    assert torch.equal(far["out"], g["out"])
+    for name in names:
+        x, y = far[name][n - c.nb:], g[name]
+        if name[1] == "c":
+            x, y = x.view(torch.uint8), y.view(torch.uint8)
+        assert torch.equal(x.flip(0), y)
+    c.check(g)
+    if kv8:     # and the append of many tokens
+        m = 130
+        new = [torch.randn(m, 8, d, device=DEV).to(TYPES[t]) for _ in "kv"]
+        starts, ctx = dev(np.array([0, m, m], np.int32)), dev(np.zeros(2, np.int32))
+        for s in (g, far):
+            mv.mtp_kv8_append(new[0], new[1], starts, s["kc"], s["vc"], s["ks"], s["vs"], s["table"], ctx)
+        mv.sync_status()
+        for name in names:
+            x, y = far[name][n - c.nb:], g[name]
+            if name[1] == "c":
+                x, y = x.view(torch.uint8), y.view(torch.uint8)
+            assert torch.equal(x.flip(0), y)
