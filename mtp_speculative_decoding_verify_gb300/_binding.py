@@ -436,6 +436,8 @@ def _on(index, stream, call):
     if stream is None and torch.cuda.current_device() == index:
         _check(call(_raw_stream(index)))
         return
+    if stream is not None and stream.device.index != index:
+        raise ValueError("stream is on cuda:%d, the tensors on cuda:%d" % (stream.device.index, index))
     with torch.cuda.device(index):
         if stream is None:
             _check(call(_raw_stream(index)))
@@ -451,7 +453,11 @@ def _raw_stream(index):
 # torch's own quick form of the same, where this build of it has one
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
-_INT_MAX = 2 ** 31 - 1
+
+def _int32(x):
+    """x in the range of the argument; what is beyond it is as good as its end (a window past every slot, or refused)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
 
 # torch's caching allocator without a tensor around the block (4 us less of a call's 20 on the host)
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc",
@@ -459,10 +465,12 @@ _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc",
 _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", torch.cuda.caching_allocator_delete)
 
 
-def _scratch(a, workspace, n, s, call):
+def _scratch(a, workspace, index, n, s, call):
     """call() with the caller's workspace in `a`, or with n bytes that torch's allocator holds for stream s. Given back
     after the launch, as a tensor would be, they go to later work of that stream only (in a capture: of that graph)."""
     if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on cuda:%d" % index)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         return call()
     p = _raw_alloc(n, s)
@@ -514,7 +522,7 @@ def _window_attention(size, attend, q, k_new, v_new, k_cache, v_cache, k_scale, 
     a = WindowAttnArgs(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                        None if k_scale is None else k_scale.data_ptr(), None if v_scale is None else v_scale.data_ptr(),
                        block_table.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), B, R - 1, Hq, Hkv, d, BLOCK_SIZE,
-                       max_blocks, nb, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
+                       max_blocks, nb, _int32(window), _int32(sinks),
                        d ** -0.5 if sm_scale is None else float(sm_scale), _dtype_code(q))
     ref = ctypes.byref(a)
 
@@ -524,7 +532,7 @@ def _window_attention(size, attend, q, k_new, v_new, k_cache, v_cache, k_scale, 
             n = size(ref)
             if n == 0:
                 _check(MTP_INVALID_ARG)
-        return _scratch(a, workspace, n, s, lambda: attend(ref, s))
+        return _scratch(a, workspace, index, n, s, lambda: attend(ref, s))
 
     _on(index, stream, call)
 
@@ -562,10 +570,10 @@ def kv_window_release(block_table, seq_lens, free_list, free_count, *, window, s
                        (free_list, "free_list", i32, (n_free,)), (free_count, "free_count", i32, (1,))))
     L = lib()
     a = WindowReleaseArgs(block_table.data_ptr(), seq_lens.data_ptr(), free_list.data_ptr(), free_count.data_ptr(), B,
-                          BLOCK_SIZE, max_blocks, n_free, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX))
+                          BLOCK_SIZE, max_blocks, n_free, _int32(window), _int32(sinks))
 
     n = L.mtp_window_release_workspace_size(B) if workspace is None else 0
-    _on(index, stream, lambda s: _scratch(a, workspace, n, s, lambda: L.kv_window_release(ctypes.byref(a), s)))
+    _on(index, stream, lambda s: _scratch(a, workspace, index, n, s, lambda: L.kv_window_release(ctypes.byref(a), s)))
 
 
 def sync_status(stream=None):

@@ -2,6 +2,7 @@
 outliers, sinks whose value is nothing, values that are not finite behind a vanishing weight, more rows than a CTA's,
 ragged batches however their pages are cut into shares, shared prefixes, a workspace used again."""
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -234,6 +235,32 @@ def test_no_requests_and_no_tokens():
     assert L.mtp_last_launch_count() == 0
     mv.kv_window_release(g["table"][:0], g["ctx"][:0], g["ctx"][:0], dev(np.zeros(1, np.int32)), window=5)
     assert L.mtp_last_launch_count() == 0
+
+
+def test_workspaces_and_windows_that_are_refused():
+    """A workspace on the host, with gaps, off its alignment or too small; a window far below zero."""
+    c = Case(True, "bf16", 1, 2, 4, 2, 64, [70], 0, 0)
+    g = c.to_gpu()
+    big = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
+    for ws in (torch.zeros(8 << 20, dtype=torch.uint8), big[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            c.call(g, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            mv.kv_window_release(g["table"], g["ctx"], g["ctx"], g["ctx"], window=5, workspace=ws)
+    for ws, word in ((big[16:], "aligned"), (big[:1024], "workspace")):
+        with pytest.raises(mv.MtpError, match=word):
+            c.call(g, workspace=ws)
+    with pytest.raises(mv.MtpError, match="workspace"):
+        mv.kv_window_release(g["table"], g["ctx"], g["ctx"], g["ctx"], window=5, workspace=big[:4])
+    elsewhere = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream"):
+        c.call(g, stream=elsewhere)
+    c.window = -2 ** 40
+    with pytest.raises(mv.MtpError, match="window"):
+        c.call(g)
+    with pytest.raises(mv.MtpError, match="window"):
+        mv.kv_window_release(g["table"], g["ctx"], g["ctx"], g["ctx"], window=-2 ** 40)
+    assert (g["out"] == 7.0).all()
 
 
 @pytest.mark.parametrize("field,value", [("max_blocks", 2 ** 24 + 1), ("Hq", 2 ** 30), ("Hkv", 2 ** 17), ("B", 2 ** 27), ("d", 96), ("D", 16),
