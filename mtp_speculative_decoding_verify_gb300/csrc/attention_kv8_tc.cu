@@ -88,6 +88,10 @@ constexpr int kSegRing = 16;           // requests announced; the TMA warp is at
 constexpr float kMostP = 8.0f, kLeastP = -4.0f, kFirstP = 1.0f, kUpP = 5.0f, kDownP = -1.0f;
 constexpr int kLowTiles = 3;
 constexpr float kDown = 60.0f;         // ref is never further below the largest there was
+// A probability is never held further below what it adds to the row's sum (2^(score - the sum's maximum, at most 2^20))
+// than this: fp32 has 126 octaves below 1, so weights down to 2^-66 of the largest count, and one so far below rounds
+// to 0 in e4m3 as it did before.
+constexpr float kFarBack = 60.0f;
 constexpr float kLoScale = 16.0f;      // P's second term is held times this
 constexpr uint32_t kColO = 256;        // S (and P) buffers at columns 0 and 128, O at 256 and 384
 
@@ -750,7 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float shift = in.lsv - (ref == -INFINITY ? 0.0f : ref);
+        // The sum is of 2^(score - lref): 2^back times the probabilities, without V's scale. Where this page's scale
+        // is far below what ref follows (zeros of V have 2^-100) both would leave fp32's range, hence the bound.
+        const float lr = lref == -INFINITY ? 0.0f : lref;    // (nothing visible yet: a sum of 0, or NaN from K)
+        const float shift = fmaxf(in.lsv - (ref == -INFINITY ? 0.0f : ref), -kFarBack - lr), back = -shift - lr;
         float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t hi[NK / 4], lo[NK / 4];
 #pragma unroll
@@ -763,9 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           add2(add[2], add[3], x[k + 2], x[k + 3]);
           split4(x[k], x[k + 1], x[k + 2], x[k + 3], hi[k / 4], lo[k / 4]);
         }
-        // 2^(score - lref) in sum: without the scale of V
-        if (lref != -INFINITY) sum += ((add[0] + add[1]) + (add[2] + add[3])) * ex2(-shift - lref);
-        else sum += (add[0] + add[1]) + (add[2] + add[3]);   // nothing visible yet: 0, or NaN from K
+        sum += ((add[0] + add[1]) + (add[2] + add[3])) * ex2(back);
         if constexpr (KG > 1) {                            // columns of the other warps' keys
           const uint32_t z[NK / 4] = {};
 #pragma unroll
