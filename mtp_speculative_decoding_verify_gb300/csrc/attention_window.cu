@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
         see[y] = __ballot_sync(0xffffffffu, vis);
         s[y] = vis ? s[y] * p.sm_scale : -INFINITY;
       }
-      const float mn = fmaxf(m[x], warp_max(fmaxf(s[0], s[1])));
+      const float mn = fmaxf(fmaxf(m[x], (see[0] | see[1]) != 0 ? kNoWeight : -INFINITY), warp_max(fmaxf(s[0], s[1])));
       const float base = mn == -INFINITY ? 0.0f : mn;
       const float c = expf(m[x] - base);
       const float p0 = expf(s[0] - base), p1 = expf(s[1] - base);
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     if (!live[x]) continue;
-    const float inv = l[x] == 0.0f ? 0.0f : 1.0f / l[x];   // nothing seen (bad blocks only): zeros
+    // no weight: nothing seen (bad blocks only), or -inf only
+    const float inv = l[x] != 0.0f ? 1.0f / l[x] : m[x] == -INFINITY || p.n_splits > 1 ? 0.0f : NAN;
     if (p.n_splits == 1) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -224,13 +225,14 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
       float* po = p.part_o + (orow[x] * p.n_splits + split) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) po[e] = o[x][e] * inv;
-      if (lane == 0) p.part_lse[orow[x] * p.n_splits + split] = l[x] == 0.0f ? -INFINITY : (m[x] + logf(l[x])) * kLog2e;
+      if (lane == 0) p.part_lse[orow[x] * p.n_splits + split] = l[x] == 0.0f ? m[x] : (m[x] + logf(l[x])) * kLog2e;
     }
   }
 }
 
 // out = sum_s 2^(lse_s - max) part_s / sum_s 2^(lse_s - max): one warp a row
-// (few rows, a launch's latency bounds it).
+// (few rows, a launch's latency bounds it). A part that saw nothing is left
+// out; one of -inf scores has weight 0, and hands a NaN of V on.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) window_merge_kernel(const WindowParams p, int64_t n_rows) {
   constexpr int E = D / kWarp;
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowParams p,
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] += w * po[e];
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = m == -INFINITY && l == 0.0f ? 0.0f : m == kNoWeight ? NAN : 1.0f / l;
 #pragma unroll
   for (int e = 0; e < E; ++e) static_cast<T*>(p.out)[row * D + lane * E + e] = Num<T>::from_f(o[e] * inv);
 }

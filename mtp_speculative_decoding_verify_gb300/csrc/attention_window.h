@@ -2,12 +2,18 @@
 // and the appends that run before them.
 #pragma once
 
+#include <float.h>
+
 #include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
 
 namespace mtp {
+
+// The running maximum of a row that has seen slots, all with scores of -inf: its softmax is NaN. (-inf: it has seen
+// none, and is 0.)
+constexpr float kNoWeight = -FLT_MAX;
 
 struct WindowPlan {
   int n_splits;                      // SIMT: ranges a request's pages are cut into

@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 2));
     x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 1));
     x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 2));
-    const float n_lo = fmaxf(m_lo, x_lo * f), n_hi = fmaxf(m_hi, x_hi * f);
+    float n_lo = fmaxf(m_lo, x_lo * f), n_hi = fmaxf(m_hi, x_hi * f);
+    if (!kMasked || page_seen(page, ctx + j_lo, p.window, p.sinks)) n_lo = fmaxf(n_lo, kNoWeight);
+    if (!kMasked || page_seen(page, ctx + j_hi, p.window, p.sinks)) n_hi = fmaxf(n_hi, kNoWeight);
     const float z_lo = n_lo == -INFINITY ? 0.0f : n_lo, z_hi = n_hi == -INFINITY ? 0.0f : n_hi;
     const float k_lo = ex2(m_lo - z_lo), k_hi = ex2(m_hi - z_hi);
     m_lo = n_lo;
@@ -461,7 +463,9 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
       l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
       l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
       l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
-      const float v_lo = l_lo == 0.0f ? 0.0f : 1.0f / l_lo, v_hi = l_hi == 0.0f ? 0.0f : 1.0f / l_hi;
+      // no weight: nothing seen (bad blocks only), or -inf only
+      const float v_lo = l_lo != 0.0f ? 1.0f / l_lo : m_lo == -INFINITY ? 0.0f : NAN;
+      const float v_hi = l_hi != 0.0f ? 1.0f / l_hi : m_hi == -INFINITY ? 0.0f : NAN;
       __nv_bfloat16* out_lo = static_cast<__nv_bfloat16*>(p.out) + (row0 + q_lo) * D;
       __nv_bfloat16* out_hi = static_cast<__nv_bfloat16*>(p.out) + (row0 + q_hi) * D;
 #pragma unroll

@@ -66,6 +66,12 @@ __host__ __device__ __forceinline__ bool slot_visible(int t, int p, int window, 
   return t <= p && (window == 0 || t > p - window || t < sinks);
 }
 
+// The row sees a slot of the page.
+__device__ __forceinline__ bool page_seen(int page, int p, int window, int sinks) {
+  const int first = page * kBlock;
+  return first <= p && (window == 0 || first + kBlock - 1 > p - window || first < sinks);
+}
+
 // The blocks that hold a slot some row of the request sees, in order: the
 // sink blocks 0 .. n_sink-1, then w0 .. the block of the last verify token.
 struct PageSpan {
