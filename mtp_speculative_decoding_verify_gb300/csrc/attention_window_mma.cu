@@ -25,7 +25,8 @@
 // Slots that not every row sees occur in the last pages, at the window's edge
 // and behind the sinks. Only those tiles take the masked path: hidden scores
 // become -inf, and values that are not finite are taken out of the product
-// (0 x NaN) and put back into the rows that do see them.
+// (0 x NaN) and put back into the rows that do see them (NaN where the weight is
+// 0).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -324,6 +325,14 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     l_lo = l_lo * k_lo + t_lo;
     l_hi = l_hi * k_hi + t_hi;
     bool out_of = false;
+    uint32_t some = 0;        // probabilities that are not 0: of the i-th word of pa, bits 31 - i (upper half) and 15 - i
+    if constexpr (kMasked) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) some |= ((pa[n >> 1][(n & 1) * 2 + e] + 0x7fff7fffu) & 0x80008000u) >> (2 * n + e);
+      }
+    }
     if (__any_sync(0xffffffffu, k_lo != 1.0f || k_hi != 1.0f)) {
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
@@ -352,7 +361,11 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     if constexpr (kMasked) {
       if (__any_sync(0xffffffffu, out_of)) {       // rare: a NaN or infinity in V
         const uint8_t* vt = smem + stage * T::kStage + T::kBytes;
+#pragma unroll 1
         for (int key = 0; key < kBlock; ++key) {
+          // of the lane that holds the key's probabilities
+          const uint32_t has = __shfl_sync(0xffffffffu, some, (lane & ~3) | (key % 8 / 2)) << (key / 8 * 2 + (key & 1 ? 0 : 16));
+          const float none_lo = has >> 31 ? 0.0f : NAN, none_hi = (has >> 30) & 1 ? 0.0f : NAN;
           const bool see_lo = slot_visible(page * kBlock + key, ctx + j_lo, p.window, p.sinks);
           const bool see_hi = slot_visible(page * kBlock + key, ctx + j_hi, p.window, p.sinks);
           if (!see_lo && !see_hi) continue;
@@ -364,8 +377,8 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
               const int dim = i * 8 + 2 * t + e;
               const float v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt + T::at(key, dim / 8) + dim % 8 * 2));
               if (!(fabsf(v) <= FLT_MAX)) {
-                if (see_lo) o[i][e] += v;
-                if (see_hi) o[i][e + 2] += v;
+                if (see_lo) o[i][e] += v + none_lo;
+                if (see_hi) o[i][e + 2] += v + none_hi;
               }
             }
           }

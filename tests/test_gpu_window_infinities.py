@@ -98,6 +98,19 @@ def test_some_scores_minus_infinity(t, ctx, window, sinks):
     run(c)
 
 
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("at", [3, 290, 1200, 2490, 2501])
+@pytest.mark.parametrize("window,sinks", [(5000, 0), (2300, 10)])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_a_value_behind_a_score_of_minus_infinity(t, window, sinks, at, value):
+    """0 x inf: NaN in that dim of the rows that see the slot, in whole pages and in masked ones."""
+    c = windowed(t, [2500, 130], window, sinks, seed=at)
+    put(c, 0, 0, [at], 1, 5, -np.inf)
+    put(c, 1, 0, [at], 1, 9, value)
+    put(c, 1, 0, [at], 0, 11, value)         # head 0's score is finite
+    assert "nan" in run(c) or at < 2500 - window
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_a_split_of_minus_infinities_hands_its_nan_on(t):
     """A long part of the request without weight, a NaN of V in it."""
