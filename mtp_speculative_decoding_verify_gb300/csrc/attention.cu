@@ -8,6 +8,7 @@
 // with ctx cached tokens therefore attends slots 0 .. ctx+j. With tree drafts
 // ("MTP in TensorRT-LLM on Blackwell", future work) row j attends the context
 // and the slots of the nodes on its root path instead (tree_path_mask).
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -40,7 +41,7 @@ __global__ void kv_append_kernel(const T* __restrict__ k_new, const T* __restric
                                  int max_blocks, int num_blocks, unsigned* err) {
   const int b = blockIdx.x / R, j = blockIdx.x % R;
   const int ctx = ctx_lens[b];
-  if (ctx < 0) {
+  if (ctx < 0 || ctx > INT_MAX - R) {
     if (threadIdx.x == 0) raise_error(err, MTP_ERR_LENGTH);
     return;
   }
@@ -184,11 +185,11 @@ __global__ void __launch_bounds__(256) attention_simt_kernel(
   if (r >= group * R) return;
   const int j = r / group, h = kvh * group + r % group;
   const int ctx = ctx_lens[b];
-  const int L = ctx + j + 1;
-  if (ctx < 0 || ctx + R > max_blocks * kBlock) {
+  if (ctx < 0 || ctx > max_blocks * kBlock - R) {
     if (lane == 0 && split == 0) raise_error(err, MTP_ERR_LENGTH);
     return;
   }
+  const int L = ctx + j + 1;
   const int t0 = split * split_len;
   if (t0 >= L) return;
   const int t1 = min(L, t0 + split_len);
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(
   if (warp >= rows) return;
   const int b = warp / (R * Hq), j = (warp / Hq) % R;
   const int ctx = ctx_lens[b];
-  if (ctx < 0 || ctx + R > max_len) return;
+  if (ctx < 0 || ctx > max_len - R) return;
   const int L = ctx + j + 1;
   const int ns = min(n_splits, (L + split_len - 1) / split_len);
   const float* lse = part_lse + (int64_t)warp * n_splits;

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(1024) gqa_schedule_kernel(const int32_t* __res
   const int n = n_splits * B;   // groups (split, request); group q = split * B + b holds items q * Hkv + h
   auto tiles_of = [&](int q) -> int {
     const int ctx = ctx_lens[q % B];
-    if (ctx < 0 || ctx + R > max_len) {   // the attention kernel skips the request
+    if (ctx < 0 || ctx > max_len - R) {   // the attention kernel skips the request
       raise_error(err, MTP_ERR_LENGTH);
       return 0;
     }
@@ -275,7 +275,7 @@ __device__ __forceinline__ bool next_item(Cursor& c, const Params& p, int n_item
     if (idx >= n_items) return false;
     c.it = decode_item(p.order[idx], p.B, p.Hkv);
     c.ctx = p.ctx_lens[c.it.b];
-    if (c.ctx < 0 || c.ctx + p.R > p.max_blocks * kBlock) continue;   // reported by the schedule kernel
+    if (c.ctx < 0 || c.ctx > p.max_blocks * kBlock - p.R) continue;   // reported by the schedule kernel
     c.t0 = c.it.split * p.split_len;
     c.t_end = min(c.t0 + p.split_len, c.ctx + p.R);
     if (c.t0 >= c.t_end) continue;   // no key of this split is visible: the combine skips it

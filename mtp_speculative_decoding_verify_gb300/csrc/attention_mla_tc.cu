@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(1024) mla_schedule_kernel(const int32_t* __res
   auto tiles_of = [&](int i) -> int {
     const Item it = decode_item(i, B, groups);
     const int ctx = ctx_lens[it.b];
-    if (ctx < 0 || ctx + R > max_len) return 0;   // rejected by the attention kernel itself
+    if (ctx < 0 || ctx > max_len - R) return 0;   // rejected by the attention kernel itself
     const int t0 = it.split * split_len;
     const int t_end = item_key_end(it, ctx, R, Hq, rows, C, split_len);
     return t0 < t_end ? min((t_end - t0 + kKeys - 1) / kKeys, kMaxItemTiles) : 0;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mla_tc_kernel(const __grid_c
   const int rows = p.R * p.Hq;
   const int row_base = item.g * kRows;
   const int ctx = p.ctx_lens[b];
-  if (ctx < 0 || ctx + p.R > p.max_blocks * kBlock) {
+  if (ctx < 0 || ctx > p.max_blocks * kBlock - p.R) {
     if (threadIdx.x == 0 && split == 0 && row_base == 0) raise_error(p.err, MTP_ERR_LENGTH);
     return;
   }
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mla_pair_kernel(const __grid
     w.t0 = it.split * p.split_len;
     w.t_end = w.t0;
     w.n_tiles = 0;
-    w.bad_len = w.ctx < 0 || w.ctx + p.R > p.max_blocks * kBlock;   // uniform over the pair (same request)
+    w.bad_len = w.ctx < 0 || w.ctx > p.max_blocks * kBlock - p.R;   // uniform over the pair (same request)
     if (!w.bad_len) {
       w.t_end = item_key_end(it, w.ctx, p.R, p.Hq, rows, 2, p.split_len);
       if (w.t0 < w.t_end) w.n_tiles = (w.t_end - w.t0 + kKeys - 1) / kKeys;

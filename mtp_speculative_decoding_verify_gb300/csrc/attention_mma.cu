@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kForm == 3 ? 32 * (kGqaConsumersNarrow + 1)
   const int kvh = (item % per) / p.row_tiles;
   const int row_base = (item % p.row_tiles) * kGqaRowsPerCta;
   const int ctx = p.ctx_lens[b];
-  if (ctx < 0 || ctx + p.R > p.max_blocks * kBlock) {
+  if (ctx < 0 || ctx > p.max_blocks * kBlock - p.R) {
     if (threadIdx.x == 0 && split == 0) raise_error(p.err, MTP_ERR_LENGTH);
     return;
   }
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(1024) gqa_mma_schedule_kernel(const int32_t* _
   const int n = n_splits * B;   // groups (split, request); group q = split * B + b holds items q * per + i
   auto tiles_of = [&](int q) -> int {
     const int ctx = ctx_lens[q % B];
-    if (ctx < 0 || ctx + R > max_len) return 0;   // the attention kernel reports and skips the request
+    if (ctx < 0 || ctx > max_len - R) return 0;   // the attention kernel reports and skips the request
     const int t0 = (q / B) * split_len;
     const int t_end = min(t0 + split_len, ctx + R);
     return t0 < t_end ? min((t_end - t0 + kBlock - 1) / kBlock, kMaxOrderTiles) : 0;

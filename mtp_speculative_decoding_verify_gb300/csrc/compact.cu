@@ -10,6 +10,7 @@
 // one CTA per request does the moves in that order, its threads copying one
 // token's K (and V) row together. kv_rollback then trims and frees blocks.
 #include <cuda_runtime.h>
+#include <limits.h>
 
 #include "../../include/mtp_verify.h"
 #include "common.cuh"
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) tree_kv_compact_kernel(
     if (threadIdx.x == 0) raise_error(err, MTP_ERR_ACCEPTED);
     return;
   }
-  if (ctx < 0 || (ctx + D) / kBlock >= max_blocks) {
+  if (ctx < 0 || ctx > INT_MAX - D || (ctx + D) / kBlock >= max_blocks) {
     if (threadIdx.x == 0) raise_error(err, MTP_ERR_LENGTH);
     return;
   }

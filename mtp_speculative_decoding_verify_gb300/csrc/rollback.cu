@@ -17,6 +17,8 @@
 // The running count is monotone, so past the first request that does not fit
 // only requests that free nothing are still rolled back; *free_count ends at
 // the last block actually appended.
+#include <limits.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -44,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) kv_rollback_kernel(int32_t* __restri
     if (b < B) {
       const int ctx = seq_lens[b];
       const int n = num_accepted[b];
-      if (ctx < 0 || (ctx + D) / kBlock >= max_blocks) {
+      if (ctx < 0 || ctx > INT_MAX - D || (ctx + D) / kBlock >= max_blocks) {
         raise_error(err, MTP_ERR_LENGTH);
         kept = -1;
       } else if (n < 0 || n > D) {
