@@ -447,11 +447,16 @@ int mtp_kv8_append(const mtp_kv8_append_args* args, void* stream);
  * window >= 1. A block no row sees is not read, and its table entry may be
  * anything (kv_window_release sets it to -1). Full blocks may be in the tables
  * of several requests. Sums and softmax statistics are fp32. With bf16 rows a
- * probability keeps 8 bits, as bf16 or as two e4m3 terms (kv8; those below
- * 2^-10 of the largest nearby keep fewer); kv8 takes Q as two or three 8-bit
- * terms, exact to 2^-21 of the row's largest value. Infinities and NaN that a
- * row sees act as in the formula; those in slots that it does not see do
- * nothing.
+ * probability is rounded to 8 bits: to bf16, as in mtp_verify_attention, or
+ * (kv8) to two e4m3 terms, of which those keep fewer bits that times V's scale
+ * are below 2^-10 of the largest such nearby. kv8 with bf16 rows holds an
+ * element of Q to 2^-17 of the row's largest value, and to 2^-21 of it in
+ * requests with a row where what that leaves out passes 2^-19 of the row's sum
+ * of magnitudes (where the largest value is below 2^-93, of 2^-93). Scores, and
+ * V's values summed over a row's slots, are expected within fp32's range.
+ * Infinities and NaN that a row sees act as in the formula (0 x inf is NaN, and
+ * a row all of whose scores are -inf is NaN); those in slots that it does not
+ * see do nothing.
  *   q, out       [B, R, Hq, d] dtype (MTP_F32 or MTP_BF16), d 64 or 128
  *   k_new, v_new [B, R, Hkv, d] dtype
  *   k_cache, v_cache [num_blocks, 64, Hkv, d] e4m3 bytes (kv8) or dtype

@@ -9,10 +9,12 @@
 // sums). The other operand is split into e4m3 terms, 4 bits each:
 //   S = Q K^T   a row of Q is scaled by a power of two (largest value in
 //               [2^7, 2^8)) and q = hi + lo holds bf16's 8 bits. What lo
-//               cannot hold (below 2^-18 of the row's largest value) goes
+//               cannot hold (up to 2^-17 of the row's largest value) goes
 //               into a third e5m2 term, used only for requests with a row
 //               where these rests pass 2^-19 of the row's sum.
-//   O += P V    p = hi + lo / 16: 8 bits, as bf16 would keep.
+//   O += P V    p = hi + lo / 16: 8 bits, as bf16 would keep (the rounding of
+//               the other bf16 kernels; rms error of an output 1.7e-3, of which
+//               its own rounding to bf16 makes 1.66e-3).
 // No operand is converted in shared memory, whose bandwidth is what two
 // products with f16 values of V run out of (32 requests x 48 rows, 4096
 // tokens: 112 us with V converted to f16, 68 us with the first form of this).
@@ -44,16 +46,18 @@
 // more rows the softmax is the longer part: there each takes a page of every
 // tile, and both S buffers serve the two of them, so that the next S is there
 // before this softmax ends (64 requests x 48 rows, 4096 tokens: 161 us with
-// alternate tiles, 138 us with pages; 16 rows, 1k-32k: 338 us and 348 us).
+// alternate tiles, 137 us with pages; 16 rows, 1k-32k: 3 % more with pages).
 //
 // Hidden slots: only tiles with a slot that not every row sees are masked.
 // There V's bytes that are NaN become 0 in shared memory (0 x NaN), and a
 // bitmap of (verify token, dim) puts NaN back into the rows that do see them.
 //
-// Bound: the read of the cache (it holds at 16 rows: 345 us for 64 requests of
+// Bound: the read of the cache (it holds at 16 rows: 343 us for 64 requests of
 // 1k-32k tokens, 95 % of the copy rate). At 48 rows the chain of a tile is
 // longer than its read (P V, then S of the tile that takes its buffer, and a
-// softmax of some 1500 cycles): 138 us for 64 requests of 4096 tokens, 59 %.
+// softmax of some 1500 cycles): 137 us for 64 requests of 4096 tokens, 59 %.
+// More than 64 rows read all pages again for each 64 (120 rows, 32 requests of
+// 4096 tokens: 145 us, 64 rows 84 us).
 //
 // Warps: 0 and 1 P V, 2 TMA (block ids and scales of 32 pages at a time, one a
 // lane), 3 S, 4-11 softmax and output, 12-15 masked V and the next request's

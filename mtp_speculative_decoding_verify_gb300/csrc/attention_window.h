@@ -32,8 +32,15 @@ struct WindowPlan {
 // of 8 pages: 20.1 us with even cuts, 12.8 us so). For the same reason each
 // request is a share where there are CTAs for all and the longest is no more
 // than four pages over an even share (16 requests of 17 or 18 pages on 19 CTAs
-// a head: 31.8 us with cuts, 24.4 us so), or has no more than 16 pages (one
-// request of 16 pages: 14.4 us in two shares, 13.7 us in one).
+// a head: 31.8 us with cuts, 24.4 us so), or has no more than 16 pages. One
+// request of n pages, 8 KV heads x 128, in one share / in cuts:
+//   n = 9 / 12 / 16 / 17 / 20 / 24
+//   8-bit, 16 rows   11.5/12.7  12.1/13.1  13.2/13.4  13.9/13.7  14.4/13.8  15.7/14.2 us
+//   8-bit, 48 rows   15.4/19.3  16.4/19.5  17.8/20.1  19.1/21.6  19.6/22.2  21.8/22.4
+//   bf16, 16 rows    11.6/12.9  12.7/13.6  14.4/14.4  14.6/13.6  15.6/14.0  17.3/14.6
+//   bf16, 48 rows    15.6/14.3  17.8/15.8  21.1/17.5  22.2/15.8  24.4/16.3  27.7/18.1
+// (1 row, and head dim 64, as 16 rows; one edge for all forms, which 48 rows
+// would have at 24 pages in 8 bits and at 8 in bf16).
 // The append launch works this out in one more CTA (window_schedule) and
 // clears the arrival counters of shared requests.
 struct alignas(16) Share {
@@ -70,7 +77,10 @@ struct WindowSchedule {
 };
 
 // CTAs of a head (a KV head's tile of rows): those that fit the device once,
-// as far as the widest table gives them a request or eight pages each.
+// as far as the widest table gives them a request or eight pages each. A whole
+// number for each head, so what 152 SMs leave over is idle (the same work as
+// 8 / 32 / 40 / 80 / 160 KV heads, group 1: 8-bit 221 / 243 / 255 / 361 / 385
+// us, windowed bf16 218 / 239 / 235 / 312 / 353 us).
 inline int head_ctas(const mtp_window_attn_args& a, int sm_count, long long heads) {
   const long long seen = a.window == 0 ? a.max_blocks   // pages that a request's rows see at most
                                        : std::min<long long>(a.max_blocks, ((long long)a.window + a.D + 127) / kBlock +

@@ -7,18 +7,24 @@
 //
 // What bounds it is the read of the cache (256 requests of 1k-32k tokens
 // behind a window of 4096: 607 us, the copy rate), or, with little of it, the
-// beginning and the end (16 requests x 48 rows behind 1000: 24 us, of which
+// beginning and the end (16 requests x 48 rows behind 1000: 24.4 us, of which
 // the read is 10). So the work is cut into shares of
 // the same number of pages, whatever the lengths (Share). A CTA crosses from
 // one request to the next without draining its ring. A request that several
 // CTAs share is joined by the last of them to finish, in the order of the
-// pages, so the result does not depend on who that is. CTAs x KV heads fill
-// the device once; the KV heads of the same pages run side by side, which
-// keeps their interleaved rows together in DRAM.
+// pages, so the result does not depend on who that is. Every KV head (and tile
+// of its rows) has the same number of CTAs, as many as fit the device once: 19
+// each for 8 heads, 152 in all, but 128 of the 152 for 32 heads and 80 for 80
+// (their time is in attention_window.h). The KV heads of the same pages run
+// side by side, which keeps their interleaved rows together in DRAM.
 //
 // A warp takes 16 query rows (row warp) and every key_parts-th tile; the
 // parts join in shared memory at the end of a request. Registers hold Q, the
-// scores and the output. A request of one page is left to its part, so that
+// scores and the output. Probabilities are rounded to bf16, the type of V that
+// the product needs, as in mtp_verify_attention (rms error of an output 2.2e-3,
+// of which its own rounding makes 1.66e-3); their sum is of the unrounded ones.
+// Above 48 rows mma.sync bounds it (32 requests behind 4096: 64 rows 147 us of
+// 81 for the read, 120 rows 295 us). A request of one page is left to its part, so that
 // such requests run side by side (113 of them, 16 KV heads: 62 us with a join
 // for each, 28 us so).
 //
