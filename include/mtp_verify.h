@@ -525,6 +525,87 @@ size_t mtp_window_release_workspace_size(int32_t B);
 int kv_window_release(const mtp_window_release_args* args, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* 5. Requests that share a prompt: blocks, slots, appends by slot, and
+ * attention that reads the shared blocks once.
+ *
+ * The pages give none of these. kv_rollback and kv_window_release give blocks
+ * back; 5a hands them out. 5b puts K/V where 5a says (a prompt's, before the
+ * first verify step). 5c is the verify attention of requests whose tables
+ * begin with the same blocks (samples of one prompt, a system prompt): its
+ * read of the cache, which bounds the step, is done once for all of them.
+ *
+ * 5a. Blocks and slots for the tokens about to be appended.
+ *
+ * Request b holds L = seq_lens[b] tokens and is to append the n = starts[b+1]
+ * - starts[b] tokens starts[b] .. starts[b+1]-1 of a ragged batch (as in
+ * mtp_kv8_append; for a verify step, R each). Of the table entries of blocks
+ * ceil(L/64) .. (L+n-1)/64 those that are < 0 take blocks from the end of the
+ * free list (free_list[*free_count - 1] first), requests in order, block
+ * index ascending; entries >= 0 are kept. taken[b] is the number of blocks
+ * taken, and *free_count goes down by their sum.
+ * A request is served whole or not at all, and none overtakes another: one
+ * whose blocks together with those of every earlier request are more than
+ * *free_count is refused (as are then all later ones that need a block).
+ * Running short is an answer, not an error: taken[b] = -1, the request's
+ * slots are -1 and its table row stays as it was; the caller may free blocks
+ * and ask again. slot_map[t], for every token t of a served request, is its
+ * cache slot block * 64 + offset. Entries of slot_map before starts[0] and
+ * from starts[B] on stay as they were.
+ * Errors: L < 0 or L + n beyond max_blocks sets MTP_ERR_LENGTH, L % 64 > 0
+ * with an entry L/64 < 0 MTP_ERR_BLOCK_ID; that request is refused and counts
+ * no block. starts that decrease or leave [0, T] set MTP_ERR_LENGTH: every
+ * taken[b] is -1 and all else stays as it was. *free_count outside [0,
+ * free_capacity] sets MTP_ERR_FREE_LIST and counts as 0. An entry < 0 of the
+ * free list sets MTP_ERR_BLOCK_ID; it goes into the table, with slots of -1.
+ * seq_lens is read only (advance it once the tokens are in the cache). No
+ * two requests' ranges of new blocks may share a table row.
+ *   block_table [B, max_blocks] int32 (in/out); seq_lens [B] int32
+ *   starts [B+1] int32; free_list [free_capacity] int32; free_count [1] int32 (in/out)
+ *   slot_map [T] int64 (out); taken [B] int32 (out)
+ *   workspace: device, >= mtp_block_assign_workspace_size(B, T) bytes, 256-byte aligned
+ * B <= 2^20, max_blocks <= 2^24. */
+typedef struct {
+  int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* starts;
+  const int32_t* free_list;
+  int32_t* free_count;
+  int64_t* slot_map;
+  int32_t* taken;
+  int32_t B, T, block_size, max_blocks, free_capacity;
+  void* workspace;
+  size_t workspace_bytes;
+} mtp_block_assign_args;
+
+size_t mtp_block_assign_workspace_size(int32_t B, int32_t T);
+int kv_block_assign(const mtp_block_assign_args* args, void* stream);
+
+/* 5b. K/V of new tokens into the cache, by slot.
+ *
+ * Token t's K and V rows are copied to slot slot_map[t] of the cache (block
+ * slot / 64, offset slot % 64). A slot < 0 is skipped (a padded token, a
+ * refused request); one beyond the cache sets MTP_ERR_BLOCK_ID and is skipped.
+ * Two tokens with the same slot leave that slot's values undefined.
+ *   k_new [T, Hkv, d_qk], v_new [T, Hkv, d_v] dtype, the tokens k_stride and
+ *         v_stride elements apart (>= Hkv d; a view of a fused projection's
+ *         output will do), a token's values contiguous
+ *   slot_map [T] int64; caches as in mtp_verify_attention (MLA: is_mla = 1, Hkv = 1, v_new = v_cache = NULL, d_v unused)
+ * All pointers, the strides and a token's rows must be multiples of 16 bytes. */
+typedef struct {
+  const void* k_new;
+  const void* v_new;
+  const int64_t* slot_map;
+  void* k_cache;
+  void* v_cache;
+  int64_t k_stride, v_stride;
+  int32_t T, Hkv, d_qk, d_v;
+  int32_t block_size, num_blocks, is_mla;
+  int32_t dtype;             /* mtp_dtype */
+} mtp_kv_append_args;
+
+int mtp_kv_append(const mtp_kv_append_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Bounded-wait check (validation only, not on the verify path).
  *
  * The tensor-core kernels wait on shared-memory mbarriers (TMA copies, MMA
@@ -588,7 +669,8 @@ int mtp_last_launch_count(void);
 /* ABI version (MTP_ABI_VERSION) and sizeof of the argument structs
  * (0 = mtp_attn_args, 1 = mtp_lmhead_args, 2 = mtp_rollback_args,
  * 3 = mtp_draft_args, 4 = mtp_kv_compact_args, 5 = mtp_kv8_append_args,
- * 6 = mtp_window_attn_args, 7 = mtp_window_release_args), for
+ * 6 = mtp_window_attn_args, 7 = mtp_window_release_args,
+ * 8 = mtp_block_assign_args, 9 = mtp_kv_append_args), for
  * bindings to check their struct layouts against. */
 int mtp_abi_version(void);
 size_t mtp_abi_struct_size(int which);

@@ -6,10 +6,12 @@ seeded synthetic-workload generators used by the tests and the benchmark.
 """
 from ._binding import (  # noqa: F401
     MtpError,
+    kv_block_assign,
     kv_rollback,
     kv_window_release,
     lib,
     mtp_draft_argmax,
+    mtp_kv_append,
     mtp_kv8_append,
     mtp_tree_kv_compact,
     mtp_verify_attention,

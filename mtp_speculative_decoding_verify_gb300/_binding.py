@@ -80,6 +80,18 @@ class WindowReleaseArgs(ctypes.Structure):
                 ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class BlockAssignArgs(ctypes.Structure):
+    _fields_ = [("block_table", _P), ("seq_lens", _P), ("starts", _P), ("free_list", _P), ("free_count", _P),
+                ("slot_map", _P), ("taken", _P), ("B", _I), ("T", _I), ("block_size", _I), ("max_blocks", _I),
+                ("free_capacity", _I), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("k_new", _P), ("v_new", _P), ("slot_map", _P), ("k_cache", _P), ("v_cache", _P),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("T", _I), ("Hkv", _I), ("d_qk", _I),
+                ("d_v", _I), ("block_size", _I), ("num_blocks", _I), ("is_mla", _I), ("dtype", _I)]
+
+
 class MtpError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__("mtp status %d: %s" % (code, msg))
@@ -140,6 +152,12 @@ def lib():
         L.mtp_window_release_workspace_size.restype = ctypes.c_size_t
         L.kv_window_release.argtypes = [ctypes.POINTER(WindowReleaseArgs), _P]
         L.kv_window_release.restype = ctypes.c_int
+        L.mtp_block_assign_workspace_size.argtypes = [ctypes.c_int32, ctypes.c_int32]
+        L.mtp_block_assign_workspace_size.restype = ctypes.c_size_t
+        L.kv_block_assign.argtypes = [ctypes.POINTER(BlockAssignArgs), _P]
+        L.kv_block_assign.restype = ctypes.c_int
+        L.mtp_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), _P]
+        L.mtp_kv_append.restype = ctypes.c_int
         L.mtp_hbm_read_probe.argtypes = [_P, ctypes.c_size_t, _P, ctypes.c_int32, ctypes.c_int32, _P]
         L.mtp_hbm_read_probe.restype = ctypes.c_int
         L.mtp_abi_version.argtypes = []
@@ -149,7 +167,7 @@ def lib():
         if L.mtp_abi_version() != ABI_VERSION:
             raise RuntimeError("library ABI version %d, binding expects %d" % (L.mtp_abi_version(), ABI_VERSION))
         for which, st in enumerate((AttnArgs, LmArgs, RollbackArgs, DraftArgs, KvCompactArgs, Kv8AppendArgs,
-                                    WindowAttnArgs, WindowReleaseArgs)):
+                                    WindowAttnArgs, WindowReleaseArgs, BlockAssignArgs, KvAppendArgs)):
             if L.mtp_abi_struct_size(which) != ctypes.sizeof(st):
                 raise RuntimeError("ABI mismatch for %s" % st.__name__)
         _lib = L
@@ -574,6 +592,65 @@ def kv_window_release(block_table, seq_lens, free_list, free_count, *, window, s
 
     n = L.mtp_window_release_workspace_size(B) if workspace is None else 0
     _on(index, stream, lambda s: _scratch(a, workspace, index, n, s, lambda: L.kv_window_release(ctypes.byref(a), s)))
+
+
+def kv_block_assign(block_table, seq_lens, starts, free_list, free_count, slot_map, taken, *, workspace=None, stream=None):
+    """Take blocks for the tokens about to be appended from the free list, and map those tokens to cache slots.
+
+    Request b holds seq_lens[b] tokens and appends tokens starts[b] .. starts[b+1]-1 of a ragged batch (starts [B+1]
+    int32). Table entries < 0 that they need take blocks from the end of free_list[:free_count] (block_table [B,
+    max_blocks], free_count [1] int32, updated). slot_map [T] int64: each token's slot, block * 64 + offset. taken [B]
+    int32: blocks taken, or -1 for a request that the list has too few blocks for (its slots are -1, its table row as it
+    was, and later requests do not overtake it).
+    """
+    B, max_blocks = block_table.shape
+    index, i32 = _cuda_index(block_table, "block_table"), torch.int32
+    n_free, T = free_list.numel(), slot_map.numel()
+    _check_all(index, ((block_table, "block_table", i32, (B, max_blocks)), (seq_lens, "seq_lens", i32, (B,)),
+                       (starts, "starts", i32, (B + 1,)), (free_list, "free_list", i32, (n_free,)),
+                       (free_count, "free_count", i32, (1,)), (slot_map, "slot_map", torch.int64, (T,)),
+                       (taken, "taken", i32, (B,))))
+    L = lib()
+    a = BlockAssignArgs(block_table.data_ptr(), seq_lens.data_ptr(), starts.data_ptr(), free_list.data_ptr(),
+                        free_count.data_ptr(), slot_map.data_ptr(), taken.data_ptr(), B, T, BLOCK_SIZE, max_blocks, n_free)
+    n = max(256, L.mtp_block_assign_workspace_size(B, T)) if workspace is None else 0
+    _on(index, stream, lambda s: _scratch(a, workspace, index, n, s, lambda: L.kv_block_assign(ctypes.byref(a), s)))
+
+
+def _refuse_rows(t, name, index, dtype, shape):
+    """Say what is wrong with a [T, Hkv, d] tensor whose tokens may lie apart."""
+    if t.is_cuda and t.get_device() == index and t.dtype is dtype and t.shape == shape:
+        raise ValueError("%s: a token's values must be contiguous" % name)
+    _refuse(t, name, index, dtype, shape)
+
+
+def mtp_kv_append(k_new, v_new, slot_map, k_cache, v_cache, *, stream=None):
+    """Copy the K/V of new tokens to the slots of the paged cache that slot_map [T] int64 gives (< 0: skipped).
+
+    k_new, v_new [T, Hkv, d] (float32 or bfloat16; views with tokens apart will do, a token's values contiguous), caches
+    [blocks, 64, Hkv, d] of the same type. Absorbed MLA: k_new [T, 576] or [T, 1, 576], v_new = v_cache = None.
+    """
+    if k_new.dim() == 2 and v_new is None:
+        k_new = k_new.unsqueeze(1)
+    T, Hkv, d = k_new.shape
+    nb, dt, index = k_cache.shape[0], k_new.dtype, _cuda_index(k_new, "k_new")
+    rows = [(k_new, "k_new", d)]
+    _check_all(index, ((slot_map, "slot_map", torch.int64, (T,)), (k_cache, "k_cache", dt, (nb, BLOCK_SIZE, Hkv, d))))
+    d_v, v_stride = 0, 0
+    if v_new is not None or v_cache is not None:
+        if v_new is None or v_cache is None:
+            raise ValueError("v_new and v_cache go together")
+        d_v, v_stride = v_new.shape[-1], v_new.stride(0) if T > 1 else Hkv * v_new.shape[-1]
+        rows.append((v_new, "v_new", d_v))
+        _check_all(index, ((v_cache, "v_cache", dt, (nb, BLOCK_SIZE, Hkv, d_v)),))
+    for t, name, n in rows:
+        if t.get_device() != index or t.dtype is not dt or t.shape != (T, Hkv, n) or \
+                (t.numel() and ((t.stride(2) != 1 and n > 1) or (t.stride(1) != n and Hkv > 1))):
+            _refuse_rows(t, name, index, dt, (T, Hkv, n))
+    a = KvAppendArgs(k_new.data_ptr(), None if v_new is None else v_new.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
+                     None if v_cache is None else v_cache.data_ptr(), k_new.stride(0) if T > 1 else Hkv * d, v_stride, T,
+                     Hkv, d, d_v, BLOCK_SIZE, nb, int(v_new is None), _dtype_code(k_new))
+    _on(index, stream, lambda s: lib().mtp_kv_append(ctypes.byref(a), s))
 
 
 def sync_status(stream=None):

@@ -216,6 +216,8 @@ size_t mtp_abi_struct_size(int which) {
     case 5: return sizeof(mtp_kv8_append_args);
     case 6: return sizeof(mtp_window_attn_args);
     case 7: return sizeof(mtp_window_release_args);
+    case 8: return sizeof(mtp_block_assign_args);
+    case 9: return sizeof(mtp_kv_append_args);
     default: return 0;
   }
 }
