@@ -605,6 +605,61 @@ typedef struct {
 
 int mtp_kv_append(const mtp_kv_append_args* args, void* stream);
 
+/* 5c. Verify attention of requests that share a prefix.
+ *
+ * mtp_verify_attention for GQA/MHA (chains, or trees with `parents`), with the
+ * same result, where the tables of several requests begin with the same
+ * blocks. Requests group_starts[g] .. group_starts[g+1]-1 form group g; blocks
+ * 0 .. prefix_blocks[g]-1 of all of them are those of the group's first
+ * request, whose table row names them: they are read once for the group, and
+ * these entries of the others' rows are not looked at. ctx_lens and block
+ * indices count from the sequence's beginning, prefix included, so kv_rollback,
+ * kv_block_assign and mtp_verify_attention go on with the same tables and
+ * lengths. A prefix ends with a full block (a prompt's last tokens that fill
+ * none are each request's own). Groups may be empty, have one request or no
+ * prefix; requests in no group attend all by themselves. G = 0: no groups.
+ * Own blocks of a request must not be other requests' (they are written).
+ * Sums and softmax statistics are fp32; with bf16 rows a probability is
+ * rounded to bf16, as in mtp_verify_attention. Infinities and NaN act as in
+ * mtp_verify_attention_window.
+ *   layouts as in mtp_verify_attention; group_starts [G+1] int32,
+ *   prefix_blocks [G] int32
+ * R = D+1 <= 16, d 64 or 128, Hq % Hkv == 0, Hkv <= 2^16, Hq / Hkv <= 2^15,
+ * max_blocks <= 2^24, B max_blocks < 2^31, B R Hq <= 2^29, (B R Hq / 64 + 2 G
+ * Hkv) max_blocks < 2^31. q, out, k_new, v_new and the caches must be 16-byte
+ * aligned; a workspace is always needed, and one call at a time may use it.
+ * Errors: MTP_ERR_LENGTH for a bad length (as in mtp_verify_attention), a
+ * prefix outside [0, max_blocks] and a context shorter than the prefix: that
+ * request is skipped (nothing is appended, its rows of out stay as they were);
+ * and for group_starts that decrease or leave [0, B]: every request then
+ * attends all blocks of its own row by itself. A block with a bad id sets
+ * MTP_ERR_BLOCK_ID and takes no part; a row that sees nothing else is 0. MLA
+ * is not provided: its 128 query heads share one latent row a token, so
+ * products bound it, not the read. */
+typedef struct {
+  const void* q;
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  const int32_t* group_starts;
+  const int32_t* prefix_blocks;
+  void* out;
+  int32_t B, D, G, Hq, Hkv, d;
+  int32_t block_size, max_blocks, num_blocks;
+  float sm_scale;
+  int32_t dtype;             /* mtp_dtype */
+  const int32_t* parents;    /* [B, R] tree drafts, NULL: chains */
+  void* workspace;           /* device, >= mtp_attention_prefix_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* timing_events[2];    /* as in mtp_attn_args */
+} mtp_prefix_attn_args;
+
+size_t mtp_attention_prefix_workspace_size(const mtp_prefix_attn_args* args);
+int mtp_verify_attention_prefix(const mtp_prefix_attn_args* args, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Bounded-wait check (validation only, not on the verify path).
  *
@@ -670,8 +725,9 @@ int mtp_last_launch_count(void);
  * (0 = mtp_attn_args, 1 = mtp_lmhead_args, 2 = mtp_rollback_args,
  * 3 = mtp_draft_args, 4 = mtp_kv_compact_args, 5 = mtp_kv8_append_args,
  * 6 = mtp_window_attn_args, 7 = mtp_window_release_args,
- * 8 = mtp_block_assign_args, 9 = mtp_kv_append_args), for
- * bindings to check their struct layouts against. */
+ * 8 = mtp_block_assign_args, 9 = mtp_kv_append_args,
+ * 10 = mtp_prefix_attn_args), for bindings to check their struct layouts
+ * against. */
 int mtp_abi_version(void);
 size_t mtp_abi_struct_size(int which);
 

@@ -16,6 +16,7 @@ from ._binding import (  # noqa: F401
     mtp_tree_kv_compact,
     mtp_verify_attention,
     mtp_verify_attention_kv8,
+    mtp_verify_attention_prefix,
     mtp_verify_attention_window,
     mtp_verify_logits_accept,
     mtp_verify_logits_accept_noalloc,

@@ -92,6 +92,14 @@ class KvAppendArgs(ctypes.Structure):
                 ("d_v", _I), ("block_size", _I), ("num_blocks", _I), ("is_mla", _I), ("dtype", _I)]
 
 
+class PrefixAttnArgs(ctypes.Structure):
+    _fields_ = [("q", _P), ("k_new", _P), ("v_new", _P), ("k_cache", _P), ("v_cache", _P), ("block_table", _P),
+                ("ctx_lens", _P), ("group_starts", _P), ("prefix_blocks", _P), ("out", _P), ("B", _I), ("D", _I),
+                ("G", _I), ("Hq", _I), ("Hkv", _I), ("d", _I), ("block_size", _I), ("max_blocks", _I),
+                ("num_blocks", _I), ("sm_scale", ctypes.c_float), ("dtype", _I), ("parents", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("timing_events", _P * 2)]
+
+
 class MtpError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__("mtp status %d: %s" % (code, msg))
@@ -158,6 +166,10 @@ def lib():
         L.kv_block_assign.restype = ctypes.c_int
         L.mtp_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), _P]
         L.mtp_kv_append.restype = ctypes.c_int
+        L.mtp_attention_prefix_workspace_size.argtypes = [ctypes.POINTER(PrefixAttnArgs)]
+        L.mtp_attention_prefix_workspace_size.restype = ctypes.c_size_t
+        L.mtp_verify_attention_prefix.argtypes = [ctypes.POINTER(PrefixAttnArgs), _P]
+        L.mtp_verify_attention_prefix.restype = ctypes.c_int
         L.mtp_hbm_read_probe.argtypes = [_P, ctypes.c_size_t, _P, ctypes.c_int32, ctypes.c_int32, _P]
         L.mtp_hbm_read_probe.restype = ctypes.c_int
         L.mtp_abi_version.argtypes = []
@@ -167,7 +179,8 @@ def lib():
         if L.mtp_abi_version() != ABI_VERSION:
             raise RuntimeError("library ABI version %d, binding expects %d" % (L.mtp_abi_version(), ABI_VERSION))
         for which, st in enumerate((AttnArgs, LmArgs, RollbackArgs, DraftArgs, KvCompactArgs, Kv8AppendArgs,
-                                    WindowAttnArgs, WindowReleaseArgs, BlockAssignArgs, KvAppendArgs)):
+                                    WindowAttnArgs, WindowReleaseArgs, BlockAssignArgs, KvAppendArgs,
+                                    PrefixAttnArgs)):
             if L.mtp_abi_struct_size(which) != ctypes.sizeof(st):
                 raise RuntimeError("ABI mismatch for %s" % st.__name__)
         _lib = L
@@ -651,6 +664,47 @@ def mtp_kv_append(k_new, v_new, slot_map, k_cache, v_cache, *, stream=None):
                      None if v_cache is None else v_cache.data_ptr(), k_new.stride(0) if T > 1 else Hkv * d, v_stride, T,
                      Hkv, d, d_v, BLOCK_SIZE, nb, int(v_new is None), _dtype_code(k_new))
     _on(index, stream, lambda s: lib().mtp_kv_append(ctypes.byref(a), s))
+
+
+def mtp_verify_attention_prefix(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, group_starts, prefix_blocks, out,
+                                *, sm_scale=None, parents=None, workspace=None, stream=None):
+    """mtp_verify_attention (GQA/MHA) of groups of requests whose tables begin with the same blocks, which are read once.
+
+    q, out [B, R, Hq, d], k_new, v_new [B, R, Hkv, d], caches [blocks, 64, Hkv, d] (float32 or bfloat16, d 64 or 128),
+    block_table [B, max_blocks] int32, ctx_lens [B] int32 (prefix included); group_starts [G+1] int32: group g is requests
+    group_starts[g] .. group_starts[g+1]-1; prefix_blocks [G] int32: full blocks that they share, those of the row of the
+    group's first request. parents [B, R] int32 (tree drafts) or None (chains).
+    """
+    B, R, Hq, d = q.shape
+    nb, _, Hkv, _ = k_cache.shape
+    max_blocks, G = block_table.shape[-1], prefix_blocks.shape[0]
+    dt, i32 = q.dtype, torch.int32
+    index = _cuda_index(q, "q")
+    new, cache = (B, R, Hkv, d), (nb, BLOCK_SIZE, Hkv, d)
+    _check_all(index, ((q, "q", dt, (B, R, Hq, d)), (k_new, "k_new", dt, new), (v_new, "v_new", dt, new),
+                       (k_cache, "k_cache", dt, cache), (v_cache, "v_cache", dt, cache),
+                       (block_table, "block_table", i32, (B, max_blocks)), (ctx_lens, "ctx_lens", i32, (B,)),
+                       (group_starts, "group_starts", i32, (G + 1,)), (prefix_blocks, "prefix_blocks", i32, (G,)),
+                       (out, "out", dt, (B, R, Hq, d))))
+    if parents is not None:
+        _check_all(index, ((parents, "parents", i32, (B, R)),))
+    L = lib()
+    a = PrefixAttnArgs(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                       block_table.data_ptr(), ctx_lens.data_ptr(), group_starts.data_ptr(), prefix_blocks.data_ptr(),
+                       out.data_ptr(), B, R - 1, G, Hq, Hkv, d, BLOCK_SIZE, max_blocks, nb,
+                       d ** -0.5 if sm_scale is None else float(sm_scale), _dtype_code(q),
+                       None if parents is None else parents.data_ptr())
+    ref = ctypes.byref(a)
+
+    def call(s):
+        n = 0
+        if workspace is None:
+            n = L.mtp_attention_prefix_workspace_size(ref)
+            if n == 0:
+                _check(MTP_INVALID_ARG)
+        return _scratch(a, workspace, index, n, s, lambda: L.mtp_verify_attention_prefix(ref, s))
+
+    _on(index, stream, call)
 
 
 def sync_status(stream=None):

@@ -1,0 +1,532 @@
+// mtp_verify_attention_prefix: verify attention of requests whose tables begin
+// with the same blocks. The C entry, the append, the plan, and the kernels of
+// fp32 rows.
+//
+// "Multi Token Prediction" note, overall flow for K=3 draft tokens, step 2, as
+// in mtp_verify_attention: the R verify rows of a request attend the reused
+// cache and each other. A softmax over slots falls into one over the group's
+// prefix and one over the request's own slots,
+//   o = (o_p 2^(m_p - m) + o_w 2^(m_w - m)) / (l_p 2^(m_p - m) + l_w 2^(m_w - m)),
+// m the larger maximum. Over the prefix the rows of all requests of the group
+// are one matrix, so K and V are read once for all of them and the product
+// is as tall as the group is large; the own slots go as in
+// mtp_verify_attention_window, each request starting from its rows' (o_p, m_p,
+// l_p).
+//
+// Launches: the append, which also works out both schedules in one more CTA;
+// the prefix; the own pages. (fp32: and the merge.)
+#include <math.h>
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "attention_window.h"
+#include "kv8.cuh"
+
+namespace mtp {
+int device_context(unsigned** err, int* sm_count);
+int set_error(int code, const char* msg);
+int set_cuda_error(cudaError_t e, const char* what);
+void set_launch_count(int n);
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------- append
+// One CTA per (request, verify token), as window_append_kernel; a request that
+// its group's prefix rules out is left alone.
+__global__ void __launch_bounds__(128) prefix_append_kernel(const uint4* __restrict__ k_new,
+                                                            const uint4* __restrict__ v_new, uint4* __restrict__ k_cache,
+                                                            uint4* __restrict__ v_cache,
+                                                            const int32_t* __restrict__ block_table, int vecs, int num_blocks,
+                                                            const PrefixSchedule prefix, const WindowSchedule own) {
+  asm volatile("griddepcontrol.launch_dependents;");   // (the kernels behind it may set up)
+  if (blockIdx.x == gridDim.x - 1) {
+    prefix_schedule<128>(prefix);
+    if (own.prefix != nullptr) window_schedule<128>(own);
+    return;
+  }
+  const int R = prefix.R, b = blockIdx.x / R, j = blockIdx.x % R;
+  const int ctx = prefix.ctx_lens[b];
+  bool bad;
+  const int g = find_group(prefix.group_starts, prefix.G, prefix.B, b, &bad);
+  const int first = own_first(g < 0 ? 0 : prefix.prefix_blocks[g], ctx, prefix.max_blocks, R);
+  if (first < 0) {
+    if (threadIdx.x == 0) raise_error(prefix.err, MTP_ERR_LENGTH);
+    return;
+  }
+  const int blk = block_table[(int64_t)b * prefix.max_blocks + (ctx + j) / kBlock];
+  if (blk < 0 || blk >= num_blocks) {
+    if (threadIdx.x == 0) raise_error(prefix.err, MTP_ERR_BLOCK_ID);
+    return;
+  }
+  const int64_t from = (int64_t)blockIdx.x * vecs, to = ((int64_t)blk * kBlock + (ctx + j) % kBlock) * vecs;
+  for (int i = threadIdx.x; i < vecs; i += 128) {
+    k_cache[to + i] = k_new[from + i];
+    v_cache[to + i] = v_new[from + i];
+  }
+}
+
+// --------------------------------------------------------------- fp32 prefix
+// A CTA walks its share of the line (attention_prefix.h): for each item 64 rows
+// of one KV head, page after page. A thread holds 4 rows x 4 keys of the
+// scores and 4 rows x D/16 dims of the output, so that a value from shared
+// memory serves four or more products; P takes K's place once the scores are
+// there, which lets two CTAs share an SM, one loading while the other computes.
+constexpr int kRows = 64, kThreads = 256;
+
+template <int D>
+struct SimtSmem {
+  static constexpr int kQ = 0, kK = kQ + kRows * (D + 4), kV = kK + kBlock * (D + 4), kFloats = kV + kBlock * D;
+  static constexpr int kBytes = kFloats * (int)sizeof(float);
+  static_assert(kRows * (kBlock + 4) <= kBlock * (D + 4), "P fits in K's place");
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowParams p) {
+  using S = SimtSmem<D>;
+  constexpr int QS = D + 4, PS = kBlock + 4, E = D / 16;   // row strides; output dims of a thread
+  extern __shared__ float smem[];
+  float *qs = smem + S::kQ, *ks = smem + S::kK, *vs = smem + S::kV, *ps = ks;
+  const PrefixView& v = p.prefix_view;
+  const PrefixHead head = load_head(v.head);
+  if ((int)blockIdx.x >= head.ctas) return;
+  int pos = prefix_cut(head, blockIdx.x);
+  const int end = prefix_cut(head, blockIdx.x + 1);
+  int gi = v.cta_group[blockIdx.x];
+  PrefixGroup g = load_group(v.groups + gi);
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const float f = p.sm_scale * kLog2e;
+  const T *q = static_cast<const T*>(p.q), *kc = static_cast<const T*>(p.k_cache), *vc = static_cast<const T*>(p.v_cache);
+
+  while (pos < end) {
+    while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(v.groups + ++gi);
+    const int k = (pos - g.line) / g.units, u0 = pos - g.line - k * g.units, u1 = min(g.units, u0 + end - pos);
+    const int kvh = k / g.tiles, tile = k % g.tiles;
+    const int item = g.item + k;
+    pos += u1 - u0;
+    __syncthreads();                           // the last item's Q has been read
+    for (int x = tid; x < kRows * (D / 4); x += kThreads) {
+      const int r = x / (D / 4), c = x % (D / 4) * 4;
+      const int token = v.shape.chunks > 1 ? tile / v.shape.chunks : tile * v.shape.tokens + r / p.group;
+      const int hh = v.shape.chunks > 1 ? tile % v.shape.chunks * kRows + r : r % p.group;
+      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // rows behind the group's compute on 0
+      if ((int64_t)g.first * p.R + token < (int64_t)p.B * p.R && hh < p.group && (v.shape.chunks > 1 || r < v.shape.tokens * p.group))
+        w = load4<T>(q + (((int64_t)g.first * p.R + token) * p.Hq + kvh * p.group + hh) * D + c);
+      *reinterpret_cast<float4*>(qs + r * QS + c) = w;
+    }
+    float m[4], l[4], o[4][E];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
+    }
+    for (int u = u0; u < u1; ++u) {
+      const int blk = p.block_table[(int64_t)g.first * p.max_blocks + u];
+      if (blk < 0 || blk >= p.num_blocks) {    // the same for every thread
+        if (tid == 0) raise_error(p.err, MTP_ERR_BLOCK_ID);
+        continue;
+      }
+      __syncthreads();                         // the last page's P and V have been read
+      for (int x = tid; x < kBlock * (D / 4); x += kThreads) {
+        const int key = x / (D / 4), c = x % (D / 4) * 4;
+        const int64_t at = (((int64_t)blk * kBlock + key) * p.Hkv + kvh) * D + c;
+        *reinterpret_cast<float4*>(ks + key * QS + c) = load4<T>(kc + at);
+        *reinterpret_cast<float4*>(vs + key * D + c) = load4<T>(vc + at);
+      }
+      __syncthreads();
+      float s[4][4];                           // rows 4 ty + i, keys tx + 16 x
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * QS + c);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float4*>(ks + (tx + 16 * x) * QS + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[i][x] += a[i].x * b[x].x + a[i].y * b[x].y + a[i].z * b[x].z + a[i].w * b[x].w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[i][x] *= f;
+          top = fmaxf(top, s[i][x]);
+        }
+#pragma unroll
+        for (int z = 8; z > 0; z >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+        const float n = fmaxf(fmaxf(m[i], top), kNoWeight);
+        const float a = m[i] == -INFINITY ? 0.0f : exp2f(m[i] - n);
+        m[i] = n;
+        l[i] *= a;                             // (of this thread's keys; joined at the end)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[i][x] = exp2f(s[i][x] - n);
+          l[i] += s[i][x];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[i][e] *= a;
+      }
+      __syncthreads();                         // K has been read
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ps[(4 * ty + i) * PS + tx + 16 * x] = s[i][x];
+      }
+      __syncwarp();                            // (a row's P is written and read by one warp)
+#pragma unroll 2
+      for (int key = 0; key < kBlock; key += 4) {
+        float a[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * PS + key);
+          a[i][0] = w.x, a[i][1] = w.y, a[i][2] = w.z, a[i][3] = w.w;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float b[E];                          // dims 4 tx + 64 (e / 4) + e % 4
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(vs + (key + y) * D + 4 * tx + e * 16);
+            b[e] = w.x, b[e + 1] = w.y, b[e + 2] = w.z, b[e + 3] = w.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[i][e] += a[i][y] * b[e];
+          }
+        }
+      }
+    }
+    const int64_t part = (int64_t)item + blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int z = 8; z > 0; z >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], z);
+      const int r = 4 * ty + i;
+      if (tx == 0) v.stats[part * kRows + r] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4*>(v.parts + part * kRows * D + ((tx + e * 4) * kRows + r) * 4) =
+            make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
+    }
+  }
+}
+
+// out = (sum of o 2^(m - top)) / (sum of l 2^(m - top)) over a row's partial
+// results: those of the prefix (o, m, l) and the own ones (o / l, m + log2 l),
+// in this order. One warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) prefix_merge_kernel(const WindowParams p, int64_t n_rows) {
+  const PrefixView& v = p.prefix_view;
+  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / kWarp;
+  if (row >= n_rows) return;
+  const int lane = threadIdx.x % kWarp;
+  const int b = (int)(row / ((int64_t)p.R * p.Hq)), jh = (int)(row % ((int64_t)p.R * p.Hq)), h = jh % p.Hq;
+  if (v.first[b] < 0) return;                  // flagged; its rows stay as they were
+  const bool on = lane < D / 4;                // a lane takes 4 dims
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto fold = [&](float pm, float pl, float4 po) {
+    const float n = fmaxf(m, pm);
+    const float a = m == -INFINITY ? 0.0f : exp2f(m - n), x = pm == -INFINITY ? 0.0f : exp2f(pm - n);
+    l = l * a + pl * x;
+    o.x = o.x * a + po.x * x, o.y = o.y * a + po.y * x, o.z = o.z * a + po.z * x, o.w = o.w * a + po.w * x;
+    m = n;
+  };
+  const int gi = v.group_of[b];
+  if (gi >= 0) {
+    const PrefixRow r = prefix_row(v, load_head(v.head), load_group(v.groups + gi), p.R, p.group, b, h / p.group,
+                                   jh / p.Hq * p.group + h % p.group, D);
+    for (int k = 0; k < r.n; ++k) {
+      const float2 ml = r.ml[(int64_t)k * r.step * v.shape.rows];
+      const float* from = r.o + (int64_t)k * r.step * v.shape.rows * D + lane * v.shape.rows * 4;
+      fold(ml.x, ml.y, on ? *reinterpret_cast<const float4*>(from) : o);
+    }
+  }
+  for (int s = 0; s < p.n_splits; ++s) {
+    const float lse = p.part_lse[row * p.n_splits + s];
+    const float4 w = on ? *reinterpret_cast<const float4*>(p.part_o + (row * p.n_splits + s) * D + lane * 4) : o;
+    fold(lse, lse == -INFINITY || lse == kNoWeight ? 0.0f : 1.0f, w);
+  }
+  // no weight: nothing seen (bad blocks only), or -inf only
+  const float inv = l != 0.0f ? 1.0f / l : m == -INFINITY ? 0.0f : NAN;
+  if (on)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + lane * 4) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+// ----------------------------------------------------------- checks and plan
+int fail(const char* msg) {
+  char buf[256];
+  snprintf(buf, sizeof buf, "mtp_verify_attention_prefix: %s", msg);
+  return set_error(MTP_INVALID_ARG, buf);
+}
+int unsupported(const char* msg) {
+  char buf[256];
+  snprintf(buf, sizeof buf, "mtp_verify_attention_prefix: %s", msg);
+  return set_error(MTP_UNSUPPORTED, buf);
+}
+
+int check_prefix(const mtp_prefix_attn_args* a) {
+  if (!a) return fail("args is NULL");
+  if (a->B < 0 || a->G < 0) return fail("B and G must be >= 0");
+  if (a->D < 0 || a->D > MTP_MAX_DRAFTS) return fail("D outside [0, 15]");
+  if (a->block_size != MTP_BLOCK_SIZE) return fail("block_size must be 64");
+  if (a->max_blocks <= 0 || a->max_blocks > (1 << 24) || a->num_blocks <= 0)
+    return fail("max_blocks outside [1, 2^24], or num_blocks <= 0");
+  if (a->Hq <= 0 || a->Hkv <= 0 || a->Hkv > (1 << 16) || a->Hq % a->Hkv) return fail("Hkv outside [1, 2^16], or Hq % Hkv != 0");
+  if (a->dtype != MTP_F32 && a->dtype != MTP_BF16) return fail("dtype");
+  if (!(a->sm_scale > 0.0f && a->sm_scale <= 1e30f)) return fail("sm_scale must be > 0 and finite");
+  if (a->d != 64 && a->d != 128) return unsupported("head dim must be 64 or 128");
+  if ((long long)a->B * (a->D + 1) * a->Hq > (1 << 29) || a->Hq / a->Hkv > (1 << 15))
+    return unsupported("B x R x Hq > 2^29, or Hq / Hkv > 2^15");
+  if ((long long)a->B * a->max_blocks > 0x7fffffffll) return unsupported("B x max_blocks >= 2^31");
+  if (a->G > (1 << 20)) return unsupported("G > 2^20");
+  if (a->B == 0) return MTP_OK;
+  if (!a->q || !a->k_new || !a->v_new || !a->k_cache || !a->v_cache || !a->block_table || !a->ctx_lens || !a->out)
+    return fail("a required pointer is NULL");
+  if (a->G > 0 && (!a->group_starts || !a->prefix_blocks)) return fail("group_starts / prefix_blocks is NULL");
+  const uintptr_t any = (uintptr_t)a->q | (uintptr_t)a->k_new | (uintptr_t)a->v_new | (uintptr_t)a->k_cache |
+                        (uintptr_t)a->v_cache | (uintptr_t)a->out;
+  if (any % 16) return fail("q, out, k_new, v_new and the caches must be 16-byte aligned");
+  return MTP_OK;
+}
+
+struct PrefixPlan {
+  WindowPlan own;
+  PrefixShape shape;
+  int ctas;
+  size_t head, groups, group_of, first, cta_group, parts, stats, own_ws, bytes;
+};
+
+bool fp32_rows(const mtp_prefix_attn_args& a) { return a.dtype == MTP_F32; }
+
+mtp_window_attn_args own_args(const mtp_prefix_attn_args& a) {
+  mtp_window_attn_args w{};
+  w.q = a.q;
+  w.k_cache = a.k_cache;
+  w.v_cache = a.v_cache;
+  w.out = a.out;
+  w.B = a.B;
+  w.D = a.D;
+  w.Hq = a.Hq;
+  w.Hkv = a.Hkv;
+  w.d = a.d;
+  w.block_size = a.block_size;
+  w.max_blocks = a.max_blocks;
+  w.num_blocks = a.num_blocks;
+  w.sm_scale = a.sm_scale;
+  w.dtype = a.dtype;
+  return w;
+}
+
+// False: more items or units than 31 bits count.
+bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
+  const int group = a.Hq / a.Hkv, R = a.D + 1;
+  const mtp_window_attn_args w = own_args(a);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  pl->shape = prefix_shape(kRows, 1, 1, group);
+  pl->ctas = 2 * sm_count;
+  // Items of all groups: whole ones of all rows, and one more for each group's end.
+  const long long tiles = ((long long)a.B * R / pl->shape.tokens + std::min(a.G, a.B)) * pl->shape.chunks;
+  const long long items = a.G == 0 ? 0 : (tiles / pl->shape.subs + std::min(a.G, a.B)) * a.Hkv;
+  if (items * ((a.max_blocks + pl->shape.pages - 1) / pl->shape.pages) > 0x7fffffffll - 0x10000) return false;
+  const size_t results = a.G == 0 ? 0 : (size_t)items + pl->ctas;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t was = at;
+    at += up(n);
+    return was;
+  };
+  pl->head = take(sizeof(PrefixHead));
+  pl->groups = take((size_t)a.G * sizeof(PrefixGroup));
+  pl->group_of = take((size_t)a.B * sizeof(int32_t));
+  pl->first = take((size_t)a.B * sizeof(int32_t));
+  pl->cta_group = take((size_t)pl->ctas * sizeof(int32_t));
+  pl->stats = take(results * pl->shape.subs * pl->shape.rows * sizeof(float2));
+  pl->parts = take(results * pl->shape.subs * pl->shape.rows * a.d * sizeof(float));
+  pl->own_ws = at;
+  if (fp32_rows(a)) {
+    pl->own = WindowPlan{};
+    pl->own.n_splits = window_simt_splits(w, sm_count);
+    const size_t n = (size_t)a.B * R * a.Hq * pl->own.n_splits;
+    pl->own.ws_partial_o = 0;
+    pl->own.ws_partial_lse = up(n * a.d * sizeof(float));
+    pl->own.ws_bytes = pl->own.ws_partial_lse + up(n * sizeof(float));
+  } else {
+    pl->own = plan_window_mma(w, sm_count);
+  }
+  pl->bytes = at + up(pl->own.ws_bytes);
+  return true;
+}
+
+template <typename T, int D>
+cudaError_t launch_prefix_simt(const WindowParams& p, int ctas, cudaStream_t s) {
+  const int smem = SimtSmem<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  prefix_simt_kernel<T, D><<<ctas, kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_merge(const WindowParams& p, cudaStream_t s) {
+  const int64_t rows = (int64_t)p.B * p.R * p.Hq;
+  prefix_merge_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p, rows);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace mtp
+
+extern "C" {
+
+size_t mtp_attention_prefix_workspace_size(const mtp_prefix_attn_args* a) {
+  using namespace mtp;
+  if (check_prefix(a) != MTP_OK) return 0;
+  unsigned* err = nullptr;
+  int sm_count = 0;
+  if (device_context(&err, &sm_count) != MTP_OK) return 0;
+  PrefixPlan pl;
+  if (!plan_prefix(*a, sm_count, &pl)) {
+    unsupported("(B R Hq / 64 + 2 G Hkv) max_blocks >= 2^31");
+    return 0;
+  }
+  return pl.bytes;
+}
+
+int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
+  using namespace mtp;
+  int rc = check_prefix(a);
+  if (rc != MTP_OK) return rc;
+  set_launch_count(0);
+  if (a->B == 0) return MTP_OK;
+  unsigned* err = nullptr;
+  int sm_count = 0;
+  if ((rc = device_context(&err, &sm_count)) != MTP_OK) return rc;
+  PrefixPlan pl;
+  if (!plan_prefix(*a, sm_count, &pl)) return unsupported("(B R Hq / 64 + 2 G Hkv) max_blocks >= 2^31");
+  if (!a->workspace || a->workspace_bytes < pl.bytes) {
+    char buf[160];
+    snprintf(buf, sizeof buf, "workspace of %zu bytes needed, %zu given", pl.bytes, a->workspace ? a->workspace_bytes : (size_t)0);
+    return set_error(MTP_INVALID_ARG, buf);
+  }
+  if ((uintptr_t)a->workspace % 256) return set_error(MTP_INVALID_ARG, "workspace must be 256-byte aligned");
+  const bool fp32 = fp32_rows(*a);
+  const mtp_window_attn_args w = own_args(*a);
+  char* ws = static_cast<char*>(a->workspace);
+  auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+  PrefixSchedule ps{};
+  ps.head = reinterpret_cast<PrefixHead*>(ws + pl.head);
+  ps.groups = reinterpret_cast<PrefixGroup*>(ws + pl.groups);
+  ps.group_of = i32(pl.group_of);
+  ps.first = i32(pl.first);
+  ps.cta_group = i32(pl.cta_group);
+  ps.group_starts = a->group_starts;
+  ps.prefix_blocks = a->prefix_blocks;
+  ps.ctx_lens = a->ctx_lens;
+  ps.G = a->G;
+  ps.B = a->B;
+  ps.R = a->D + 1;
+  ps.group = a->Hq / a->Hkv;
+  ps.Hkv = a->Hkv;
+  ps.max_blocks = a->max_blocks;
+  ps.ctas = pl.ctas;
+  ps.shape = pl.shape;
+  ps.err = err;
+  WindowParams p{};
+  p.q = a->q;
+  p.out = a->out;
+  p.k_cache = a->k_cache;
+  p.v_cache = a->v_cache;
+  p.block_table = a->block_table;
+  p.ctx_lens = a->ctx_lens;
+  p.err = err;
+  p.B = a->B;
+  p.R = ps.R;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.group = ps.group;
+  p.rows = p.group * p.R;
+  p.max_blocks = a->max_blocks;
+  p.num_blocks = a->num_blocks;
+  p.n_splits = pl.own.n_splits;
+  p.row_tiles = pl.own.row_tiles;
+  p.row_warps = pl.own.row_warps;
+  p.key_parts = pl.own.key_parts;
+  p.stages = pl.own.stages;
+  p.sm_scale = a->sm_scale;
+  p.part_o = reinterpret_cast<float*>(ws + pl.own_ws + pl.own.ws_partial_o);
+  p.part_lse = reinterpret_cast<float*>(ws + pl.own_ws + pl.own.ws_partial_lse);
+  p.prefix_view = PrefixView{ps.head, ps.groups, ps.group_of, ps.first, ps.cta_group, reinterpret_cast<float*>(ws + pl.parts),
+                             reinterpret_cast<float2*>(ws + pl.stats), a->parents, pl.shape};
+  WindowSchedule own{};
+  if (!fp32) {
+    own.prefix = i32(pl.own_ws + pl.own.ws_prefix);
+    own.shares = reinterpret_cast<Share*>(ws + pl.own_ws + pl.own.ws_shares);
+    own.sharers = reinterpret_cast<int2*>(ws + pl.own_ws + pl.own.ws_sharers);
+    own.arrived = i32(pl.own_ws + pl.own.ws_arrived);
+    own.ctas = pl.own.ctas_per_head;
+    own.n_arrived = (int64_t)p.B * p.Hkv * pl.own.row_tiles * pl.own.row_warps;
+    own.ctx_lens = p.ctx_lens;
+    own.B = p.B;
+    own.R = p.R;
+    own.max_blocks = p.max_blocks;
+    own.first = ps.first;
+    p.prefix = own.prefix;
+    p.shares = own.shares;
+    p.sharers = own.sharers;
+    p.arrived = own.arrived;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto record = [&](void* ev) { return ev ? cudaEventRecord(static_cast<cudaEvent_t>(ev), s) : cudaSuccess; };
+  const int vecs = a->Hkv * a->d * (fp32 ? 4 : 2) / 16;
+  prefix_append_kernel<<<a->B * p.R + 1, 128, 0, s>>>((const uint4*)a->k_new, (const uint4*)a->v_new, (uint4*)a->k_cache,
+                                                     (uint4*)a->v_cache, a->block_table, vecs, a->num_blocks, ps, own);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return set_cuda_error(e, "kv append launch");
+  if ((e = record(a->timing_events[0])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
+  int launches = 1;
+  if (a->G > 0) {
+    ++launches;
+    if (fp32) e = a->d == 128 ? launch_prefix_simt<float, 128>(p, pl.ctas, s) : launch_prefix_simt<float, 64>(p, pl.ctas, s);
+    else e = a->d == 128 ? launch_prefix_simt<__nv_bfloat16, 128>(p, pl.ctas, s) : launch_prefix_simt<__nv_bfloat16, 64>(p, pl.ctas, s);
+    if (e != cudaSuccess) return set_cuda_error(e, "prefix attention launch");
+  }
+  e = fp32 ? launch_window_simt_own(p, a->d, s) : launch_window_mma_own(w, pl.own, p, s);
+  if (e != cudaSuccess) return set_cuda_error(e, "attention launch");
+  ++launches;
+  if (fp32) {
+    e = a->d == 128 ? launch_merge<128>(p, s) : launch_merge<64>(p, s);
+    if (e != cudaSuccess) return set_cuda_error(e, "attention merge launch");
+    ++launches;
+  }
+  if ((e = record(a->timing_events[1])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
+  set_launch_count(launches);
+  return MTP_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,204 @@
+// Launch parameters and the shares of work of mtp_verify_attention_prefix,
+// between attention_prefix.cu, attention_prefix_tc.cu and the kernels that do
+// the requests' own pages (attention_window.cu, attention_window_mma.cu).
+//
+// The query rows of a group that share a KV head are numbered token after
+// token (request, verify token), the heads of a token side by side, and cut
+// into tiles of kRows rows that hold whole tokens (kRows / group of them; of
+// a token with more heads than that, kRows heads at a time). An item is
+// `subs` such tiles of one group and KV head against all of the group's
+// prefix. The items form a line in units of `pages` pages of keys, cut into
+// an even share for each CTA. Item i's part from CTA c is partial result i + c:
+// along the line, i and c never go down together, so the number is its own.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace mtp {
+
+struct alignas(16) PrefixGroup {
+  int32_t first;                    // its first request: whose table row names the prefix's blocks
+  int32_t blocks;                   // of the prefix
+  int32_t units, tiles;             // of an item; items of a KV head
+  int32_t line, item;               // its first unit of the line and its first item
+  int32_t pad[2];
+};
+struct alignas(16) PrefixHead {
+  int32_t total, ctas;              // units of the line, shares
+  int32_t size, more;               // units of a share; the first `more` have one more
+};
+
+// Of one launch, the same on the host and on the device.
+struct PrefixShape {
+  int rows, subs, pages;            // rows of a tile, tiles of an item, pages of a unit
+  int tokens, chunks;               // tokens that a tile holds; tiles that a token needs
+};
+__host__ __device__ inline PrefixShape prefix_shape(int rows, int subs, int pages, int group) {
+  PrefixShape s{rows, subs, pages, 0, 0};
+  s.tokens = group <= rows ? rows / group : 1;
+  s.chunks = group <= rows ? 1 : (group + rows - 1) / rows;
+  return s;
+}
+
+struct PrefixView {
+  const PrefixHead* head;
+  const PrefixGroup* groups;
+  const int32_t* group_of;          // [B] group of a request that has a prefix, else -1
+  const int32_t* first;             // [B] first page of a request's own; -1: the request is skipped
+  const int32_t* cta_group;         // [ctas] group in which a CTA's share begins
+  float* parts;                     // [partial result][sub][d/4][rows][4]: sums of p v, not divided
+  float2* stats;                    // [partial result][sub][rows]: maximum (log2 units), sum of p
+  const int32_t* parents;           // [B, R] or NULL
+  PrefixShape shape;
+};
+
+// Written by one more CTA of the append.
+struct PrefixSchedule {
+  PrefixHead* head;                 // nullptr: nothing to prepare
+  PrefixGroup* groups;
+  int32_t *group_of, *first, *cta_group;
+  const int32_t *group_starts, *prefix_blocks, *ctx_lens;
+  int G, B, R, group, Hkv, max_blocks, ctas;
+  PrefixShape shape;
+  unsigned* err;
+};
+
+__device__ __forceinline__ int prefix_cut(const PrefixHead& h, int c) { return c * h.size + min(c, h.more); }
+__device__ __forceinline__ int prefix_cta_of(const PrefixHead& h, int unit) {
+  const int split = h.more * (h.size + 1);
+  return unit < split ? unit / (h.size + 1) : h.more + (unit - split) / h.size;
+}
+
+__device__ __forceinline__ PrefixHead load_head(const PrefixHead* at) {
+  const int4 v = __ldcg(reinterpret_cast<const int4*>(at));
+  return PrefixHead{v.x, v.y, v.z, v.w};
+}
+__device__ __forceinline__ PrefixGroup load_group(const PrefixGroup* at) {
+  const int4 v = __ldcg(reinterpret_cast<const int4*>(at));
+  const int2 w = __ldcg(reinterpret_cast<const int2*>(&at->line));
+  return PrefixGroup{v.x, v.y, v.z, v.w, w.x, w.y, {0, 0}};
+}
+
+// Where the partial results of a row over its group's prefix lie: n of them,
+// the first at `o` and `ml`, each next one `step` tiles on.
+struct PrefixRow {
+  const float* o;
+  const float2* ml;
+  int n, step;
+};
+
+// Row r (verify token r / group, head r % group of KV head kvh) of request b.
+__device__ __forceinline__ PrefixRow prefix_row(const PrefixView& v, const PrefixHead& h, const PrefixGroup& g, int R, int group,
+                                                int b, int kvh, int r, int d) {
+  const PrefixShape& s = v.shape;
+  const int token = (b - g.first) * R + r / group, head = r % group;
+  const int tile = token / s.tokens * s.chunks + head / s.rows;
+  const int row = s.chunks > 1 ? head % s.rows : token % s.tokens * group + head;
+  const int k = kvh * g.tiles + tile / s.subs;
+  const int u0 = g.line + k * g.units, c0 = prefix_cta_of(h, u0), c1 = prefix_cta_of(h, u0 + g.units - 1);
+  const int64_t at = (int64_t)(g.item + k + c0) * s.subs + tile % s.subs;
+  return PrefixRow{v.parts + at * s.rows * d + row * 4, v.stats + at * s.rows + row, c1 - c0 + 1, s.subs};
+}
+
+// --------------------------------------------------------------- scheduling
+// The group of request b, for a CTA of any size: -1 none, and *bad (for all of
+// the CTA the same) when the starts decrease or leave [0, B].
+__device__ __forceinline__ int find_group(const int32_t* starts, int G, int B, int b, bool* bad) {
+  __shared__ int s_found;
+  int wrong = 0;
+  if (threadIdx.x == 0) s_found = -1;
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += blockDim.x) {
+    const int s0 = starts[g], s1 = starts[g + 1];
+    wrong |= s0 < 0 || s1 < s0 || s1 > B;
+    if (s0 <= b && b < s1) s_found = g;        // (one at most, where the starts are right)
+  }
+  *bad = __syncthreads_or(wrong) != 0;
+  return *bad ? -1 : s_found;
+}
+
+// The first page of request b's own, -1 when the request cannot be done.
+__device__ __forceinline__ int own_first(int blocks, int ctx, int max_blocks, int R) {
+  if (ctx < 0 || ctx > max_blocks * kBlock - R) return -1;
+  return blocks < 0 || blocks > max_blocks || ctx < blocks * kBlock ? -1 : blocks;
+}
+
+template <int THREADS>
+__device__ void prefix_schedule(const PrefixSchedule& w) {
+  constexpr int kWarps = THREADS / kWarp;
+  __shared__ int2 s_sum[kWarps];
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  bool bad;
+  find_group(w.group_starts, w.G, w.B, -1, &bad);
+  if (bad && threadIdx.x == 0) raise_error(w.err, MTP_ERR_LENGTH);
+  const int G = bad ? 0 : w.G;                 // every request by itself
+  int2 base = make_int2(0, 0);                 // units of the line, items
+  for (int g0 = 0; g0 < G; g0 += THREADS) {
+    const int g = g0 + threadIdx.x;
+    PrefixGroup e{0, 0, 0, 0, 0, 0, {0, 0}};
+    int2 mine = make_int2(0, 0);
+    if (g < G) {
+      e.first = w.group_starts[g];
+      const int n = w.group_starts[g + 1] - e.first;
+      e.blocks = w.prefix_blocks[g];
+      if (n > 0 && e.blocks > 0 && e.blocks <= w.max_blocks) {
+        e.units = (e.blocks + w.shape.pages - 1) / w.shape.pages;
+        const int tiles = (n * w.R + w.shape.tokens - 1) / w.shape.tokens * w.shape.chunks;
+        e.tiles = (tiles + w.shape.subs - 1) / w.shape.subs;
+        mine = make_int2(e.tiles * w.Hkv * e.units, e.tiles * w.Hkv);
+      } else if (n > 0 && e.blocks != 0) {
+        raise_error(w.err, MTP_ERR_LENGTH);
+      }
+    }
+    int2 incl = mine;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) incl.x += x, incl.y += y;
+    }
+    __syncthreads();                           // the last chunk's totals have been read
+    if (lane == kWarp - 1) s_sum[warp] = incl;
+    __syncthreads();
+    e.line = base.x + incl.x - mine.x;
+    e.item = base.y + incl.y - mine.y;
+    for (int i = 0; i < kWarps; ++i) {
+      const int2 t = s_sum[i];
+      if (i < warp) e.line += t.x, e.item += t.y;
+      base.x += t.x, base.y += t.y;
+    }
+    if (g < G) w.groups[g] = e;
+  }
+  PrefixHead h;
+  h.total = base.x;
+  h.ctas = min(w.ctas, base.x);
+  h.size = h.ctas == 0 ? 1 : h.total / h.ctas;
+  h.more = h.ctas == 0 ? 0 : h.total - h.ctas * h.size;
+  if (threadIdx.x == 0) *w.head = h;
+  __syncthreads();                             // (writes to global memory too, for this CTA)
+  for (int c = threadIdx.x; c < h.ctas; c += THREADS) {
+    const int cut = prefix_cut(h, c);
+    int lo = 0, hi = G;                        // the last group whose line begins at or before the cut
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      (w.groups[mid].line <= cut ? lo : hi) = mid;
+    }
+    w.cta_group[c] = lo;
+  }
+  for (int b = threadIdx.x; b < w.B; b += THREADS) {
+    int lo = 0, hi = G, g = -1;                // the last group that begins at or before b, if b is in it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      (w.group_starts[mid] <= b ? lo : hi) = mid;
+    }
+    if (G > 0 && w.group_starts[lo] <= b && b < w.group_starts[lo + 1]) g = lo;
+    const int blocks = g < 0 ? 0 : w.prefix_blocks[g];
+    const int first = own_first(blocks, w.ctx_lens[b], w.max_blocks, w.R);
+    w.first[b] = first;
+    w.group_of[b] = first > 0 ? g : -1;
+  }
+  __syncthreads();                             // before window_schedule reads them
+}
+
+}  // namespace mtp

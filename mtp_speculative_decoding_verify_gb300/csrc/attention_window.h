@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "attention_prefix.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -64,6 +65,7 @@ struct WindowParams {
   int max_blocks, num_blocks, window, sinks, n_splits;
   int row_tiles, row_warps, key_parts, stages;
   float sm_scale;
+  PrefixView prefix_view;           // mtp_verify_attention_prefix: pages are a request's own, rows begin with these
 };
 
 struct WindowSchedule {
@@ -74,6 +76,7 @@ struct WindowSchedule {
   int64_t n_arrived;
   const int32_t* ctx_lens;
   int B, R, max_blocks, window, sinks, ctas;
+  const int32_t* first;             // [B] first page of a request's own, -1: none are; nullptr: from the window
 };
 
 // CTAs of a head (a KV head's tile of rows): those that fit the device once,
@@ -101,6 +104,11 @@ inline size_t plan_schedule(WindowPlan* pl, int B, int Hkv) {
 
 WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
+// The same over the pages from WindowParams::prefix_view.first on, beginning with the partial results over the pages before.
+cudaError_t launch_window_mma_own(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
+int window_simt_splits(const mtp_window_attn_args& a, int sm_count);
+// fp32 rows: partial results over the own pages, n_splits of a row.
+cudaError_t launch_window_simt_own(const WindowParams& p, int d, cudaStream_t s);
 WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_kv8_tc(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, const WindowSchedule& sch, unsigned* err,

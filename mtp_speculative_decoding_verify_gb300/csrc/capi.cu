@@ -218,6 +218,7 @@ size_t mtp_abi_struct_size(int which) {
     case 7: return sizeof(mtp_window_release_args);
     case 8: return sizeof(mtp_block_assign_args);
     case 9: return sizeof(mtp_kv_append_args);
+    case 10: return sizeof(mtp_prefix_attn_args);
     default: return 0;
   }
 }

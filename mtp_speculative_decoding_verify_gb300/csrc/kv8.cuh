@@ -90,6 +90,11 @@ __host__ __device__ __forceinline__ PageSpan page_span(int ctx, int R, int windo
   return s;
 }
 
+// A request's own pages behind a prefix of `first` pages.
+__host__ __device__ __forceinline__ PageSpan own_span(int ctx, int R, int first) {
+  return PageSpan{0, first, (ctx + R + kBlock - 1) / kBlock - first};
+}
+
 // ----------------------------------------------------------- shares of work
 struct Cuts {
   int total;       // pages of the line
@@ -173,7 +178,10 @@ __device__ void window_schedule(const WindowSchedule& w) {
     n = 0;
     if (b < w.B) {
       ctx = w.ctx_lens[b];                // a bad length has no pages: its rows stay as they were
-      if (ctx >= 0 && ctx <= w.max_blocks * kBlock - w.R) n = page_span(ctx, w.R, w.window, w.sinks).n;
+      if (ctx >= 0 && ctx <= w.max_blocks * kBlock - w.R) {
+        n = page_span(ctx, w.R, w.window, w.sinks).n;
+        if (w.first != nullptr) n = w.first[b] < 0 ? 0 : n - w.first[b];
+      }
     }
     most = max(most, n);
     p1 = n;

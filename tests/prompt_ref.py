@@ -44,16 +44,16 @@ def attention(q, k, v, ctx, scale, parents=None):
     error bounds, sum_t p_t |v_t| of every output and the largest sum |q k| scale of every row. A key that a row does not
     see takes no part, whatever it holds."""
     R, Hq, d = q.shape
-    g = Hq // k.shape[1]
+    Hkv = k.shape[1]
     see = np.concatenate([np.ones((R, ctx), bool), path_rows(parents, R)], 1)
     out, absolute, score = np.empty((R, Hq, d)), np.empty((R, Hq, d)), np.empty((R, Hq, 1))
     with np.errstate(invalid="ignore", over="ignore"):
         for j in range(R):
-            for h in range(Hq):
-                kh, vh, qh = k[see[j], h // g], v[see[j], h // g], np.asarray(q[j, h], np.float64)
-                x = kh @ qh * scale
-                w = np.exp(x - x.max())
-                w /= w.sum()
-                out[j, h], absolute[j, h] = w @ vh, w @ np.abs(vh)
-                score[j, h] = (np.abs(kh) @ np.abs(qh)).max() * scale
+            kj, vj, qj = k[see[j]].astype(np.float64), v[see[j]].astype(np.float64), q[j].reshape(Hkv, -1, d).astype(np.float64)
+            x = np.einsum("hgd,thd->hgt", qj, kj) * scale
+            w = np.exp(x - x.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            out[j] = np.einsum("hgt,thd->hgd", w, vj).reshape(Hq, d)
+            absolute[j] = np.einsum("hgt,thd->hgd", w, np.abs(vj)).reshape(Hq, d)
+            score[j] = np.einsum("hgd,thd->hgt", np.abs(qj), np.abs(kj)).max(-1).reshape(Hq, 1) * scale
     return out, absolute, score

@@ -19,7 +19,7 @@ def mtplib():
 
 def test_struct_layouts(mtplib):
     L = mtplib.lib()
-    for which, st in ((8, mtplib.BlockAssignArgs), (9, mtplib.KvAppendArgs)):
+    for which, st in ((8, mtplib.BlockAssignArgs), (9, mtplib.KvAppendArgs), (10, mtplib.PrefixAttnArgs)):
         assert L.mtp_abi_struct_size(which) == ctypes.sizeof(st)
 
 
@@ -69,8 +69,36 @@ def test_append_refuses(mtplib, kw, code):
     assert L.mtp_last_error()
 
 
+def _attn(m, **kw):
+    a = m.PrefixAttnArgs()
+    for n in ("q", "k_new", "v_new", "k_cache", "v_cache", "block_table", "ctx_lens", "group_starts", "prefix_blocks", "out"):
+        setattr(a, n, 16)
+    a.B, a.D, a.G, a.Hq, a.Hkv, a.d, a.block_size, a.max_blocks, a.num_blocks = 4, 3, 2, 8, 2, 128, 64, 8, 16
+    a.sm_scale, a.dtype = 0.088, 1
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), 1), (dict(G=-1), 1), (dict(D=16), 1), (dict(D=-1), 1), (dict(block_size=32), 1), (dict(max_blocks=0), 1),
+    (dict(max_blocks=(1 << 24) + 1), 1), (dict(num_blocks=-1), 1), (dict(Hkv=3), 1), (dict(Hq=0), 1), (dict(dtype=7), 1),
+    (dict(sm_scale=0.0), 1), (dict(sm_scale=float("nan")), 1), (dict(sm_scale=float("inf")), 1), (dict(d=96), 2),
+    (dict(d=576), 2), (dict(q=None), 1), (dict(out=None), 1), (dict(ctx_lens=None), 1), (dict(group_starts=None), 1),
+    (dict(prefix_blocks=None), 1), (dict(q=8), 1), (dict(v_cache=24), 1), (dict(B=1 << 25), 2), (dict(G=(1 << 20) + 1), 2),
+    (dict(B=1 << 10, max_blocks=1 << 21), 2),
+])
+def test_attention_refuses(mtplib, kw, code):
+    L = mtplib.lib()
+    a = _attn(mtplib, **kw)
+    assert L.mtp_verify_attention_prefix(ctypes.byref(a), None) == code
+    assert L.mtp_last_error()
+    assert L.mtp_attention_prefix_workspace_size(ctypes.byref(a)) == 0
+
+
 def test_empty_calls_do_nothing(mtplib):
     L = mtplib.lib()
+    assert L.mtp_verify_attention_prefix(ctypes.byref(_attn(mtplib, B=0, q=None)), None) == 0
     assert L.kv_block_assign(ctypes.byref(_assign(mtplib, B=0, workspace=None)), None) == 0
     assert L.mtp_kv_append(ctypes.byref(_append(mtplib, T=0, k_new=None)), None) == 0
     assert L.mtp_block_assign_workspace_size(-1, 4) == 0 and L.mtp_block_assign_workspace_size(4, -1) == 0
