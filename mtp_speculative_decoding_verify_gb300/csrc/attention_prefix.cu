@@ -83,20 +83,7 @@ struct SimtSmem {
   static_assert(kRows * (kBlock + 4) <= kBlock * (D + 4), "P fits in K's place");
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowParams p) {
   using S = SimtSmem<D>;
   constexpr int QS = D + 4, PS = kBlock + 4, E = D / 16;   // row strides; output dims of a thread
@@ -111,7 +98,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowPa
   PrefixGroup g = load_group(v.groups + gi);
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const float f = p.sm_scale * kLog2e;
-  const T *q = static_cast<const T*>(p.q), *kc = static_cast<const T*>(p.k_cache), *vc = static_cast<const T*>(p.v_cache);
+  const float *q = static_cast<const float*>(p.q), *kc = static_cast<const float*>(p.k_cache), *vc = static_cast<const float*>(p.v_cache);
+  auto load4 = [](const float* at) { return __ldg(reinterpret_cast<const float4*>(at)); };
 
   while (pos < end) {
     while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(v.groups + ++gi);
@@ -126,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowPa
       const int hh = v.shape.chunks > 1 ? tile % v.shape.chunks * kRows + r : r % p.group;
       float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // rows behind the group's compute on 0
       if ((int64_t)g.first * p.R + token < (int64_t)p.B * p.R && hh < p.group && (v.shape.chunks > 1 || r < v.shape.tokens * p.group))
-        w = load4<T>(q + (((int64_t)g.first * p.R + token) * p.Hq + kvh * p.group + hh) * D + c);
+        w = load4(q + (((int64_t)g.first * p.R + token) * p.Hq + kvh * p.group + hh) * D + c);
       *reinterpret_cast<float4*>(qs + r * QS + c) = w;
     }
     float m[4], l[4], o[4][E];
@@ -147,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowPa
       for (int x = tid; x < kBlock * (D / 4); x += kThreads) {
         const int key = x / (D / 4), c = x % (D / 4) * 4;
         const int64_t at = (((int64_t)blk * kBlock + key) * p.Hkv + kvh) * D + c;
-        *reinterpret_cast<float4*>(ks + key * QS + c) = load4<T>(kc + at);
-        *reinterpret_cast<float4*>(vs + key * D + c) = load4<T>(vc + at);
+        *reinterpret_cast<float4*>(ks + key * QS + c) = load4(kc + at);
+        *reinterpret_cast<float4*>(vs + key * D + c) = load4(vc + at);
       }
       __syncthreads();
       float s[4][4];                           // rows 4 ty + i, keys tx + 16 x
@@ -348,8 +336,8 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   const int group = a.Hq / a.Hkv, R = a.D + 1;
   const mtp_window_attn_args w = own_args(a);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  pl->shape = prefix_shape(kRows, 1, 1, group);
-  pl->ctas = 2 * sm_count;
+  pl->shape = fp32_rows(a) ? prefix_shape(kRows, 1, 1, group) : prefix_shape(kPrefixTcRows, 2, 2, group);
+  pl->ctas = fp32_rows(a) ? 2 * sm_count : sm_count;
   // Items of all groups: whole ones of all rows, and one more for each group's end.
   const long long tiles = ((long long)a.B * R / pl->shape.tokens + std::min(a.G, a.B)) * pl->shape.chunks;
   const long long items = a.G == 0 ? 0 : (tiles / pl->shape.subs + std::min(a.G, a.B)) * a.Hkv;
@@ -383,12 +371,12 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   return true;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_prefix_simt(const WindowParams& p, int ctas, cudaStream_t s) {
   const int smem = SimtSmem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prefix_simt_kernel<T, D><<<ctas, kThreads, smem, s>>>(p);
+  prefix_simt_kernel<D><<<ctas, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -512,8 +500,8 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   int launches = 1;
   if (a->G > 0) {
     ++launches;
-    if (fp32) e = a->d == 128 ? launch_prefix_simt<float, 128>(p, pl.ctas, s) : launch_prefix_simt<float, 64>(p, pl.ctas, s);
-    else e = a->d == 128 ? launch_prefix_simt<__nv_bfloat16, 128>(p, pl.ctas, s) : launch_prefix_simt<__nv_bfloat16, 64>(p, pl.ctas, s);
+    if (fp32) e = a->d == 128 ? launch_prefix_simt<128>(p, pl.ctas, s) : launch_prefix_simt<64>(p, pl.ctas, s);
+    else e = launch_prefix_tc(*a, p, pl.ctas, s);
     if (e != cudaSuccess) return set_cuda_error(e, "prefix attention launch");
   }
   e = fp32 ? launch_window_simt_own(p, a->d, s) : launch_window_mma_own(w, pl.own, p, s);

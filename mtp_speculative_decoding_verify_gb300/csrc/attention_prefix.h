@@ -23,12 +23,14 @@ struct alignas(16) PrefixGroup {
   int32_t blocks;                   // of the prefix
   int32_t units, tiles;             // of an item; items of a KV head
   int32_t line, item;               // its first unit of the line and its first item
-  int32_t pad[2];
+  int32_t sub_tiles, pad;           // tiles of rows of a KV head
 };
 struct alignas(16) PrefixHead {
   int32_t total, ctas;              // units of the line, shares
   int32_t size, more;               // units of a share; the first `more` have one more
 };
+
+constexpr int kPrefixTcRows = 128;  // of a tile on the tensor cores: two tiles an item, two pages a unit
 
 // Of one launch, the same on the host and on the device.
 struct PrefixShape {
@@ -77,8 +79,8 @@ __device__ __forceinline__ PrefixHead load_head(const PrefixHead* at) {
 }
 __device__ __forceinline__ PrefixGroup load_group(const PrefixGroup* at) {
   const int4 v = __ldcg(reinterpret_cast<const int4*>(at));
-  const int2 w = __ldcg(reinterpret_cast<const int2*>(&at->line));
-  return PrefixGroup{v.x, v.y, v.z, v.w, w.x, w.y, {0, 0}};
+  const int4 w = __ldcg(reinterpret_cast<const int4*>(&at->line));
+  return PrefixGroup{v.x, v.y, v.z, v.w, w.x, w.y, w.z, 0};
 }
 
 // Where the partial results of a row over its group's prefix lie: n of them,
@@ -137,7 +139,7 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
   int2 base = make_int2(0, 0);                 // units of the line, items
   for (int g0 = 0; g0 < G; g0 += THREADS) {
     const int g = g0 + threadIdx.x;
-    PrefixGroup e{0, 0, 0, 0, 0, 0, {0, 0}};
+    PrefixGroup e{0, 0, 0, 0, 0, 0, 0, 0};
     int2 mine = make_int2(0, 0);
     if (g < G) {
       e.first = w.group_starts[g];
@@ -145,8 +147,8 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
       e.blocks = w.prefix_blocks[g];
       if (n > 0 && e.blocks > 0 && e.blocks <= w.max_blocks) {
         e.units = (e.blocks + w.shape.pages - 1) / w.shape.pages;
-        const int tiles = (n * w.R + w.shape.tokens - 1) / w.shape.tokens * w.shape.chunks;
-        e.tiles = (tiles + w.shape.subs - 1) / w.shape.subs;
+        e.sub_tiles = (n * w.R + w.shape.tokens - 1) / w.shape.tokens * w.shape.chunks;
+        e.tiles = (e.sub_tiles + w.shape.subs - 1) / w.shape.subs;
         mine = make_int2(e.tiles * w.Hkv * e.units, e.tiles * w.Hkv);
       } else if (n > 0 && e.blocks != 0) {
         raise_error(w.err, MTP_ERR_LENGTH);

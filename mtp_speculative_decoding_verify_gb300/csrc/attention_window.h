@@ -106,6 +106,8 @@ WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
 // The same over the pages from WindowParams::prefix_view.first on, beginning with the partial results over the pages before.
 cudaError_t launch_window_mma_own(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
+// bf16 rows: the prefix.
+cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const WindowParams& p, int ctas, cudaStream_t s);
 int window_simt_splits(const mtp_window_attn_args& a, int sm_count);
 // fp32 rows: partial results over the own pages, n_splits of a row.
 cudaError_t launch_window_simt_own(const WindowParams& p, int d, cudaStream_t s);
