@@ -9,19 +9,17 @@
 //   o = (o_p 2^(m_p - m) + o_w 2^(m_w - m)) / (l_p 2^(m_p - m) + l_w 2^(m_w - m)),
 // m the larger maximum. Over the prefix the rows of all requests of the group
 // are one matrix, so K and V are read once for all of them and the product
-// is as tall as the group is large; the own slots go as in
-// mtp_verify_attention_window, each request starting from its rows' (o_p, m_p,
-// l_p).
+// is as tall as the group is large.
 //
-// Launches: the append, which also works out both schedules in one more CTA;
-// the prefix; the own pages. (fp32: and the merge.)
+// Launches: the append, which also works out the shares of work in one more
+// CTA; the prefix; the own pages; the join of the two.
 #include <math.h>
 #include <stdio.h>
 
 #include <algorithm>
 
+#include "attention_prefix.h"
 #include "attention_window.h"
-#include "kv8.cuh"
 
 namespace mtp {
 int device_context(unsigned** err, int* sm_count);
@@ -40,11 +38,10 @@ __global__ void __launch_bounds__(128) prefix_append_kernel(const uint4* __restr
                                                             const uint4* __restrict__ v_new, uint4* __restrict__ k_cache,
                                                             uint4* __restrict__ v_cache,
                                                             const int32_t* __restrict__ block_table, int vecs, int num_blocks,
-                                                            const PrefixSchedule prefix, const WindowSchedule own) {
+                                                            const PrefixSchedule prefix) {
   asm volatile("griddepcontrol.launch_dependents;");   // (the kernels behind it may set up)
   if (blockIdx.x == gridDim.x - 1) {
     prefix_schedule<128>(prefix);
-    if (own.prefix != nullptr) window_schedule<128>(own);
     return;
   }
   const int R = prefix.R, b = blockIdx.x / R, j = blockIdx.x % R;
@@ -84,12 +81,12 @@ struct SimtSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowParams p) {
+__global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const PrefixParams p) {
   using S = SimtSmem<D>;
   constexpr int QS = D + 4, PS = kBlock + 4, E = D / 16;   // row strides; output dims of a thread
   extern __shared__ float smem[];
   float *qs = smem + S::kQ, *ks = smem + S::kK, *vs = smem + S::kV, *ps = ks;
-  const PrefixView& v = p.prefix_view;
+  const PrefixView& v = p.view;
   const PrefixHead head = load_head(v.head);
   if ((int)blockIdx.x >= head.ctas) return;
   int pos = prefix_cut(head, blockIdx.x);
@@ -223,49 +220,6 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const WindowPa
   }
 }
 
-// out = (sum of o 2^(m - top)) / (sum of l 2^(m - top)) over a row's partial
-// results: those of the prefix (o, m, l) and the own ones (o / l, m + log2 l),
-// in this order. One warp a row.
-template <int D>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const WindowParams p, int64_t n_rows) {
-  const PrefixView& v = p.prefix_view;
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / kWarp;
-  if (row >= n_rows) return;
-  const int lane = threadIdx.x % kWarp;
-  const int b = (int)(row / ((int64_t)p.R * p.Hq)), jh = (int)(row % ((int64_t)p.R * p.Hq)), h = jh % p.Hq;
-  if (v.first[b] < 0) return;                  // flagged; its rows stay as they were
-  const bool on = lane < D / 4;                // a lane takes 4 dims
-  float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto fold = [&](float pm, float pl, float4 po) {
-    const float n = fmaxf(m, pm);
-    const float a = m == -INFINITY ? 0.0f : exp2f(m - n), x = pm == -INFINITY ? 0.0f : exp2f(pm - n);
-    l = l * a + pl * x;
-    o.x = o.x * a + po.x * x, o.y = o.y * a + po.y * x, o.z = o.z * a + po.z * x, o.w = o.w * a + po.w * x;
-    m = n;
-  };
-  const int gi = v.group_of[b];
-  if (gi >= 0) {
-    const PrefixRow r = prefix_row(v, load_head(v.head), load_group(v.groups + gi), p.R, p.group, b, h / p.group,
-                                   jh / p.Hq * p.group + h % p.group, D);
-    for (int k = 0; k < r.n; ++k) {
-      const float2 ml = r.ml[(int64_t)k * r.step * v.shape.rows];
-      const float* from = r.o + (int64_t)k * r.step * v.shape.rows * D + lane * v.shape.rows * 4;
-      fold(ml.x, ml.y, on ? *reinterpret_cast<const float4*>(from) : o);
-    }
-  }
-  for (int s = 0; s < p.n_splits; ++s) {
-    const float lse = p.part_lse[row * p.n_splits + s];
-    const float4 w = on ? *reinterpret_cast<const float4*>(p.part_o + (row * p.n_splits + s) * D + lane * 4) : o;
-    fold(lse, lse == -INFINITY || lse == kNoWeight ? 0.0f : 1.0f, w);
-  }
-  // no weight: nothing seen (bad blocks only), or -inf only
-  const float inv = l != 0.0f ? 1.0f / l : m == -INFINITY ? 0.0f : NAN;
-  if (on)
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + lane * 4) =
-        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-}
-
 // ----------------------------------------------------------- checks and plan
 int fail(const char* msg) {
   char buf[256];
@@ -303,50 +257,46 @@ int check_prefix(const mtp_prefix_attn_args* a) {
   return MTP_OK;
 }
 
-struct PrefixPlan {
-  WindowPlan own;
-  PrefixShape shape;
-  int ctas;
-  size_t head, groups, group_of, first, cta_group, parts, stats, own_ws, bytes;
-};
-
 bool fp32_rows(const mtp_prefix_attn_args& a) { return a.dtype == MTP_F32; }
 
+// What window_simt_kernel (fp32 rows) has to know.
 mtp_window_attn_args own_args(const mtp_prefix_attn_args& a) {
   mtp_window_attn_args w{};
-  w.q = a.q;
-  w.k_cache = a.k_cache;
-  w.v_cache = a.v_cache;
-  w.out = a.out;
   w.B = a.B;
   w.D = a.D;
   w.Hq = a.Hq;
   w.Hkv = a.Hkv;
   w.d = a.d;
-  w.block_size = a.block_size;
   w.max_blocks = a.max_blocks;
-  w.num_blocks = a.num_blocks;
-  w.sm_scale = a.sm_scale;
   w.dtype = a.dtype;
   return w;
 }
 
+struct PrefixPlan {
+  PrefixShape shape;
+  int ctas;                            // shares of the prefix
+  OwnPlan own;                         // bf16
+  int n_splits;                        // fp32
+  // byte offsets in the workspace
+  size_t head, groups, group_of, first, cta_group, parts, stats, own_head, pages, own_parts, own_stats, bytes;
+};
+
 // False: more items or units than 31 bits count.
 bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
-  const int group = a.Hq / a.Hkv, R = a.D + 1;
-  const mtp_window_attn_args w = own_args(a);
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  pl->shape = fp32_rows(a) ? prefix_shape(kRows, 1, 1, group) : prefix_shape(kPrefixTcRows, 2, 2, group);
-  pl->ctas = fp32_rows(a) ? 2 * sm_count : sm_count;
-  // Items of all groups: whole ones of all rows, and one more for each group's end.
-  const long long tiles = ((long long)a.B * R / pl->shape.tokens + std::min(a.G, a.B)) * pl->shape.chunks;
-  const long long items = a.G == 0 ? 0 : (tiles / pl->shape.subs + std::min(a.G, a.B)) * a.Hkv;
-  if (items * ((a.max_blocks + pl->shape.pages - 1) / pl->shape.pages) > 0x7fffffffll - 0x10000) return false;
-  const size_t results = a.G == 0 ? 0 : (size_t)items + pl->ctas;
+  const int group = a.Hq / a.Hkv, R = a.D + 1, G = std::min(a.G, a.B);   // (empty groups have no items)
+  const bool fp32 = fp32_rows(a);
+  pl->shape = fp32 ? prefix_shape(kRows, 1, 1, group) : prefix_shape(kPrefixTcRows, 2, 2, group);
+  pl->ctas = fp32 ? 2 * sm_count : sm_count;
+  const long long limit = 0x7fffffffll - 0x10000;
+  // Items of all groups: the tiles of all rows, and the ones that each group leaves part of empty.
+  const long long tiles = ((long long)a.B * R / pl->shape.tokens + G) * pl->shape.chunks;
+  const long long items = G == 0 ? 0 : (tiles / pl->shape.subs + G) * a.Hkv;
+  if (items * a.max_blocks > limit) return false;
+  const size_t results = G == 0 ? 0 : ((size_t)items + pl->ctas) * pl->shape.subs * pl->shape.rows;   // rows of partial results
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t was = at;
-    at += up(n);
+    at += (n + 255) / 256 * 256;
     return was;
   };
   pl->head = take(sizeof(PrefixHead));
@@ -354,36 +304,33 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   pl->group_of = take((size_t)a.B * sizeof(int32_t));
   pl->first = take((size_t)a.B * sizeof(int32_t));
   pl->cta_group = take((size_t)pl->ctas * sizeof(int32_t));
-  pl->stats = take(results * pl->shape.subs * pl->shape.rows * sizeof(float2));
-  pl->parts = take(results * pl->shape.subs * pl->shape.rows * a.d * sizeof(float));
-  pl->own_ws = at;
-  if (fp32_rows(a)) {
-    pl->own = WindowPlan{};
-    pl->own.n_splits = window_simt_splits(w, sm_count);
-    const size_t n = (size_t)a.B * R * a.Hq * pl->own.n_splits;
-    pl->own.ws_partial_o = 0;
-    pl->own.ws_partial_lse = up(n * a.d * sizeof(float));
-    pl->own.ws_bytes = pl->own.ws_partial_lse + up(n * sizeof(float));
+  pl->stats = take(results * sizeof(float2));
+  pl->parts = take(results * a.d * sizeof(float));
+  if (fp32) {
+    pl->n_splits = window_simt_splits(own_args(a), sm_count);
+    const size_t n = (size_t)a.B * R * a.Hq * pl->n_splits;
+    pl->own_stats = take(n * sizeof(float));
+    pl->own_parts = take(n * a.d * sizeof(float));
   } else {
-    pl->own = plan_window_mma(w, sm_count);
+    pl->own = plan_prefix_own(a, sm_count);
+    const long long own_items = (long long)a.B * a.Hkv * pl->own.row_tiles;
+    if (own_items * a.max_blocks > limit) return false;
+    const size_t n = ((size_t)own_items + (size_t)pl->own.ctas * pl->own.teams) * pl->own.row_warps * 16;
+    pl->own_head = take(sizeof(PrefixHead));
+    pl->pages = take(((size_t)a.B + 1) * sizeof(int32_t));
+    pl->own_stats = take(n * sizeof(float2));
+    pl->own_parts = take(n * a.d * sizeof(float));
   }
-  pl->bytes = at + up(pl->own.ws_bytes);
+  pl->bytes = at;
   return true;
 }
 
 template <int D>
-cudaError_t launch_prefix_simt(const WindowParams& p, int ctas, cudaStream_t s) {
+cudaError_t launch_prefix_simt(const PrefixParams& p, int ctas, cudaStream_t s) {
   const int smem = SimtSmem<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   prefix_simt_kernel<D><<<ctas, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_merge(const WindowParams& p, cudaStream_t s) {
-  const int64_t rows = (int64_t)p.B * p.R * p.Hq;
-  prefix_merge_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p, rows);
   return cudaGetLastError();
 }
 
@@ -424,7 +371,6 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   }
   if ((uintptr_t)a->workspace % 256) return set_error(MTP_INVALID_ARG, "workspace must be 256-byte aligned");
   const bool fp32 = fp32_rows(*a);
-  const mtp_window_attn_args w = own_args(*a);
   char* ws = static_cast<char*>(a->workspace);
   auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
   PrefixSchedule ps{};
@@ -439,13 +385,12 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   ps.G = a->G;
   ps.B = a->B;
   ps.R = a->D + 1;
-  ps.group = a->Hq / a->Hkv;
   ps.Hkv = a->Hkv;
   ps.max_blocks = a->max_blocks;
   ps.ctas = pl.ctas;
   ps.shape = pl.shape;
   ps.err = err;
-  WindowParams p{};
+  PrefixParams p{};
   p.q = a->q;
   p.out = a->out;
   p.k_cache = a->k_cache;
@@ -457,63 +402,78 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   p.R = ps.R;
   p.Hq = a->Hq;
   p.Hkv = a->Hkv;
-  p.group = ps.group;
+  p.group = a->Hq / a->Hkv;
   p.rows = p.group * p.R;
   p.max_blocks = a->max_blocks;
   p.num_blocks = a->num_blocks;
-  p.n_splits = pl.own.n_splits;
-  p.row_tiles = pl.own.row_tiles;
-  p.row_warps = pl.own.row_warps;
-  p.key_parts = pl.own.key_parts;
-  p.stages = pl.own.stages;
   p.sm_scale = a->sm_scale;
-  p.part_o = reinterpret_cast<float*>(ws + pl.own_ws + pl.own.ws_partial_o);
-  p.part_lse = reinterpret_cast<float*>(ws + pl.own_ws + pl.own.ws_partial_lse);
-  p.prefix_view = PrefixView{ps.head, ps.groups, ps.group_of, ps.first, ps.cta_group, reinterpret_cast<float*>(ws + pl.parts),
-                             reinterpret_cast<float2*>(ws + pl.stats), a->parents, pl.shape};
-  WindowSchedule own{};
-  if (!fp32) {
-    own.prefix = i32(pl.own_ws + pl.own.ws_prefix);
-    own.shares = reinterpret_cast<Share*>(ws + pl.own_ws + pl.own.ws_shares);
-    own.sharers = reinterpret_cast<int2*>(ws + pl.own_ws + pl.own.ws_sharers);
-    own.arrived = i32(pl.own_ws + pl.own.ws_arrived);
-    own.ctas = pl.own.ctas_per_head;
-    own.n_arrived = (int64_t)p.B * p.Hkv * pl.own.row_tiles * pl.own.row_warps;
-    own.ctx_lens = p.ctx_lens;
-    own.B = p.B;
-    own.R = p.R;
-    own.max_blocks = p.max_blocks;
-    own.first = ps.first;
-    p.prefix = own.prefix;
-    p.shares = own.shares;
-    p.sharers = own.sharers;
-    p.arrived = own.arrived;
+  p.behind_prefix = a->G > 0;
+  p.view.head = ps.head;
+  p.view.groups = ps.groups;
+  p.view.group_of = ps.group_of;
+  p.view.first = ps.first;
+  p.view.cta_group = ps.cta_group;
+  p.view.parts = reinterpret_cast<float*>(ws + pl.parts);
+  p.view.stats = reinterpret_cast<float2*>(ws + pl.stats);
+  p.view.parents = a->parents;
+  p.view.shape = pl.shape;
+  WindowParams w{};
+  if (fp32) {
+    w.q = a->q;
+    w.k_cache = a->k_cache;
+    w.v_cache = a->v_cache;
+    w.block_table = a->block_table;
+    w.ctx_lens = a->ctx_lens;
+    w.err = err;
+    w.B = p.B;
+    w.R = p.R;
+    w.Hq = p.Hq;
+    w.Hkv = p.Hkv;
+    w.group = p.group;
+    w.rows = p.rows;
+    w.max_blocks = p.max_blocks;
+    w.num_blocks = p.num_blocks;
+    w.sm_scale = p.sm_scale;
+    w.n_splits = p.n_splits = pl.n_splits;
+    w.part_o = reinterpret_cast<float*>(ws + pl.own_parts);
+    w.part_lse = reinterpret_cast<float*>(ws + pl.own_stats);
+    p.part_o = w.part_o;
+    p.part_lse = w.part_lse;
+    w.own_first = ps.first;
+    w.parents = a->parents;
+  } else {
+    ps.own = reinterpret_cast<PrefixHead*>(ws + pl.own_head);
+    ps.pages = i32(pl.pages);
+    ps.own_heads = p.Hkv * pl.own.row_tiles;
+    ps.own_teams = pl.own.ctas * pl.own.teams;
+    p.row_tiles = pl.own.row_tiles;
+    p.row_warps = pl.own.row_warps;
+    p.teams = pl.own.teams;
+    p.stages = pl.own.stages;
+    p.view.own = ps.own;
+    p.view.pages = ps.pages;
+    p.view.own_parts = reinterpret_cast<float*>(ws + pl.own_parts);
+    p.view.own_stats = reinterpret_cast<float2*>(ws + pl.own_stats);
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto record = [&](void* ev) { return ev ? cudaEventRecord(static_cast<cudaEvent_t>(ev), s) : cudaSuccess; };
   const int vecs = a->Hkv * a->d * (fp32 ? 4 : 2) / 16;
   prefix_append_kernel<<<a->B * p.R + 1, 128, 0, s>>>((const uint4*)a->k_new, (const uint4*)a->v_new, (uint4*)a->k_cache,
-                                                     (uint4*)a->v_cache, a->block_table, vecs, a->num_blocks, ps, own);
+                                                     (uint4*)a->v_cache, a->block_table, vecs, a->num_blocks, ps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return set_cuda_error(e, "kv append launch");
   if ((e = record(a->timing_events[0])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
-  int launches = 1;
   if (a->G > 0) {
-    ++launches;
     if (fp32) e = a->d == 128 ? launch_prefix_simt<128>(p, pl.ctas, s) : launch_prefix_simt<64>(p, pl.ctas, s);
     else e = launch_prefix_tc(*a, p, pl.ctas, s);
     if (e != cudaSuccess) return set_cuda_error(e, "prefix attention launch");
   }
-  e = fp32 ? launch_window_simt_own(p, a->d, s) : launch_window_mma_own(w, pl.own, p, s);
+  e = fp32 ? launch_window_simt_own(w, a->d, s) : launch_prefix_own(*a, p, pl.own, s);
   if (e != cudaSuccess) return set_cuda_error(e, "attention launch");
-  ++launches;
-  if (fp32) {
-    e = a->d == 128 ? launch_merge<128>(p, s) : launch_merge<64>(p, s);
-    if (e != cudaSuccess) return set_cuda_error(e, "attention merge launch");
-    ++launches;
-  }
+  e = launch_prefix_join(*a, p, s);
+  if (e != cudaSuccess) return set_cuda_error(e, "attention join launch");
   if ((e = record(a->timing_events[1])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
-  set_launch_count(launches);
+  set_launch_count(a->G > 0 ? 4 : 3);
   return MTP_OK;
 }
 

@@ -10,11 +10,15 @@
 // prefix. The items form a line in units of `pages` pages of keys, cut into
 // an even share for each CTA. Item i's part from CTA c is partial result i + c:
 // along the line, i and c never go down together, so the number is its own.
+//
+// The own pages of the requests form a line the same way, in pages, with
+// (request, KV head, tile of rows) for items and warp teams for CTAs.
 #pragma once
 
 #include <stdint.h>
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace mtp {
 
@@ -54,7 +58,37 @@ struct PrefixView {
   float2* stats;                    // [partial result][sub][rows]: maximum (log2 units), sum of p
   const int32_t* parents;           // [B, R] or NULL
   PrefixShape shape;
+  // bf16 rows: the own pages
+  const PrefixHead* own;
+  const int32_t* pages;             // [B+1] own pages of the requests before each
+  float* own_parts;                 // [partial result][rows of a tile][d]
+  float2* own_stats;                // [partial result][rows of a tile]
 };
+
+struct PrefixParams {
+  const void* q;
+  void* out;
+  const void *k_cache, *v_cache;
+  const int32_t *block_table, *ctx_lens;
+  unsigned* err;
+  int B, R, Hq, Hkv, group, rows;   // rows = query rows per (request, KV head)
+  int max_blocks, num_blocks;
+  float sm_scale;
+  int n_splits;                     // fp32: own partial results of a row, as window_simt_kernel leaves them
+  const float *part_o, *part_lse;
+  // bf16: the kernel of the own pages
+  int row_tiles, row_warps, teams, stages;   // tiles of 16 row_warps rows; teams of a CTA, stages of a team
+  int behind_prefix;                // it is launched behind the prefix's kernel (else behind the append)
+  PrefixView view;
+};
+
+struct OwnPlan {
+  int row_tiles, row_warps, teams, stages, ctas;
+};
+OwnPlan plan_prefix_own(const mtp_prefix_attn_args& a, int sm_count);
+cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s);
+cudaError_t launch_prefix_own(const mtp_prefix_attn_args& a, const PrefixParams& p, const OwnPlan& pl, cudaStream_t s);
+cudaError_t launch_prefix_join(const mtp_prefix_attn_args& a, const PrefixParams& p, cudaStream_t s);
 
 // Written by one more CTA of the append.
 struct PrefixSchedule {
@@ -62,8 +96,11 @@ struct PrefixSchedule {
   PrefixGroup* groups;
   int32_t *group_of, *first, *cta_group;
   const int32_t *group_starts, *prefix_blocks, *ctx_lens;
-  int G, B, R, group, Hkv, max_blocks, ctas;
+  int G, B, R, Hkv, max_blocks, ctas;
   PrefixShape shape;
+  PrefixHead* own;                  // nullptr: no line of own pages
+  int32_t* pages;
+  int own_heads, own_teams;         // items of a request, shares
   unsigned* err;
 };
 
@@ -200,7 +237,37 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
     w.first[b] = first;
     w.group_of[b] = first > 0 ? g : -1;
   }
-  __syncthreads();                             // before window_schedule reads them
+  if (w.own == nullptr) return;
+  __syncthreads();
+  int at = 0;                                  // own pages of the requests so far
+  for (int b0 = 0; b0 < w.B; b0 += THREADS) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < w.B && w.first[b] >= 0) n = (w.ctx_lens[b] + w.R + kBlock - 1) / kBlock - w.first[b];
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    __syncthreads();                           // the last chunk's totals have been read
+    if (lane == kWarp - 1) s_sum[warp].x = incl;
+    __syncthreads();
+    incl += at;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) incl += s_sum[i].x;
+      at += s_sum[i].x;
+    }
+    if (b < w.B) w.pages[b + 1] = incl;
+  }
+  if (threadIdx.x == 0) {
+    w.pages[0] = 0;
+    h.total = at * w.own_heads;
+    h.ctas = min(w.own_teams, h.total);
+    h.size = h.ctas == 0 ? 1 : h.total / h.ctas;
+    h.more = h.ctas == 0 ? 0 : h.total - h.ctas * h.size;
+    *w.own = h;
+  }
 }
 
 }  // namespace mtp

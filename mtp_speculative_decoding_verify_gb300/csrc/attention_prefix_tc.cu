@@ -27,6 +27,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include "attention_prefix.h"
 #include "attention_window.h"
 #include "sm100.cuh"
 
@@ -136,22 +137,22 @@ struct Seg {
 };
 
 struct Walk {
-  const WindowParams& p;
+  const PrefixParams& p;
   PrefixHead head;
   PrefixGroup g;
   int pos, end, gi, cta;
-  __device__ __forceinline__ explicit Walk(const WindowParams& params) : p(params), cta(blockIdx.x) {
-    head = load_head(p.prefix_view.head);
+  __device__ __forceinline__ explicit Walk(const PrefixParams& params) : p(params), cta(blockIdx.x) {
+    head = load_head(p.view.head);
     pos = end = 0;
     if (cta >= head.ctas) return;
     pos = prefix_cut(head, cta);
     end = prefix_cut(head, cta + 1);
-    gi = __ldcg(p.prefix_view.cta_group + cta);
-    g = load_group(p.prefix_view.groups + gi);
+    gi = __ldcg(p.view.cta_group + cta);
+    g = load_group(p.view.groups + gi);
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (pos >= end) return false;
-    while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(p.prefix_view.groups + ++gi);
+    while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(p.view.groups + ++gi);
     const int k = (pos - g.line) / g.units, rt = k % g.tiles;
     s.first = g.first;
     s.blocks = g.blocks;
@@ -169,7 +170,7 @@ struct Walk {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const WindowParams p) {
+                     const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
   using S = Smem<D>;
   constexpr int kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA
       const uint64_t keep = sm100::l2_policy_evict_last();
-      const PrefixShape& shape = p.prefix_view.shape;
+      const PrefixShape& shape = p.view.shape;
       const int heads = min(p.group, kRows);
       int n = 0, tile = 0, sn = 0;               // tiles filled, tiles of keys, segments
       while (ok && walk.next(seg)) {
@@ -471,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       o_phase ^= 1u;
       sm100::tc_fence_after();
       const int64_t at = seg.part * 2 + x;
-      p.prefix_view.stats[at * kRows + row] = make_float2(m, l0 + l1);
-      float4* parts = reinterpret_cast<float4*>(p.prefix_view.parts + at * kRows * D) + row;
+      p.view.stats[at * kRows + row] = make_float2(m, l0 + l1);
+      float4* parts = reinterpret_cast<float4*>(p.view.parts + at * kRows * D) + row;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
@@ -499,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch(const mtp_prefix_attn_args& a, const WindowParams& p, int ctas, cudaStream_t s) {
-  const PrefixShape& shape = p.prefix_view.shape;
+cudaError_t launch(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s) {
+  const PrefixShape& shape = p.view.shape;
   CUtensorMap tq, tk, tv;
   const cuuint64_t group = (cuuint64_t)p.group, Hkv = (cuuint64_t)a.Hkv;
   const cuuint64_t qdims[4] = {(cuuint64_t)D, group, Hkv, (cuuint64_t)a.B * p.R};
@@ -519,7 +520,7 @@ cudaError_t launch(const mtp_prefix_attn_args& a, const WindowParams& p, int cta
 
 }  // namespace
 
-cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const WindowParams& p, int ctas, cudaStream_t s) {
+cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s) {
   return a.d == 128 ? launch<128>(a, p, ctas, s) : launch<64>(a, p, ctas, s);
 }
 

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
   }
   PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
   if constexpr (kOwn) {
-    const int first = p.prefix_view.first[b];
+    const int first = p.own_first[b];
     if (first < 0) return;                     // flagged by the append
     span = own_span(ctx, p.R, first);
   }
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
     live[x] = r < p.rows;
     const int rc = min(r, p.rows - 1);
     pos[x] = ctx + rc / p.group;
-    path[x] = kOwn ? tree_path_mask(p.prefix_view.parents, b, p.R, rc / p.group, p.err) : 0;
+    path[x] = kOwn ? tree_path_mask(p.parents, b, p.R, rc / p.group, p.err) : 0;
     orow[x] = ((int64_t)b * p.R + rc / p.group) * p.Hq + kvh * p.group + rc % p.group;
     for (int e = lane; e < D; e += kWarp)
       qs[(warp + x * kSimtWarps) * D + e] = Num<T>::to_f(static_cast<const T*>(p.q)[orow[x] * D + e]);

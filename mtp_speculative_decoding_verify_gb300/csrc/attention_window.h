@@ -6,7 +6,6 @@
 
 #include <algorithm>
 
-#include "attention_prefix.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -65,7 +64,7 @@ struct WindowParams {
   int max_blocks, num_blocks, window, sinks, n_splits;
   int row_tiles, row_warps, key_parts, stages;
   float sm_scale;
-  PrefixView prefix_view;           // mtp_verify_attention_prefix: pages are a request's own, rows begin with these
+  const int32_t *own_first, *parents;   // mtp_verify_attention_prefix: [B] first page of a request's own, -1: none; trees
 };
 
 struct WindowSchedule {
@@ -76,7 +75,6 @@ struct WindowSchedule {
   int64_t n_arrived;
   const int32_t* ctx_lens;
   int B, R, max_blocks, window, sinks, ctas;
-  const int32_t* first;             // [B] first page of a request's own, -1: none are; nullptr: from the window
 };
 
 // CTAs of a head (a KV head's tile of rows): those that fit the device once,
@@ -104,12 +102,8 @@ inline size_t plan_schedule(WindowPlan* pl, int B, int Hkv) {
 
 WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
-// The same over the pages from WindowParams::prefix_view.first on, beginning with the partial results over the pages before.
-cudaError_t launch_window_mma_own(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
-// bf16 rows: the prefix.
-cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const WindowParams& p, int ctas, cudaStream_t s);
 int window_simt_splits(const mtp_window_attn_args& a, int sm_count);
-// fp32 rows: partial results over the own pages, n_splits of a row.
+// mtp_verify_attention_prefix, fp32 rows: partial results over the own pages, n_splits of a row.
 cudaError_t launch_window_simt_own(const WindowParams& p, int d, cudaStream_t s);
 WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_kv8_tc(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);

@@ -82,10 +82,7 @@ __device__ __forceinline__ bool take_out(uint32_t& w) {
   return keep != 0xffffffffu;
 }
 
-// kOwn: the pages are those of a request's own behind its group's prefix, and
-// the first of its parts begin with the partial results over the prefix
-// (mtp_verify_attention_prefix); no window, but maybe trees of drafts.
-template <int D, bool kOwn>
+template <int D>
 __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     window_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const WindowParams p) {
@@ -156,7 +153,7 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     while (pos < t_end && ok) {
       find();
       const int i1 = min(t_end, p1) - p0;
-      const PageSpan span = kOwn ? own_span(ctx, p.R, __ldcg(p.prefix_view.first + b)) : page_span(ctx, p.R, p.window, p.sinks);
+      const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
       for (int i = pos - p0; i < i1 && ok; i += kWarp) {
         int blk = -1;
         if (i + lane < i1) {
@@ -229,19 +226,6 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
   const float f = p.sm_scale * kLog2e;
   int tile = 0;                           // n % key_parts == kp: this part's tiles
 
-  // What the rows see: of the verify keys, those of their paths (kOwn).
-  uint32_t path_lo = 0, path_hi = 0;
-  auto sees = [&](int slot, int ctx, bool hi) -> bool {
-    if constexpr (kOwn) return !tree_hidden(slot, ctx, hi ? path_hi : path_lo);
-    return slot_visible(slot, ctx + (hi ? j_hi : j_lo), p.window, p.sinks);
-  };
-  auto sees_page = [&](int page, int ctx, bool hi) -> bool {
-    if constexpr (kOwn) {
-      const int rel = page * kBlock - ctx;             // (node 0 is on every path)
-      return rel <= 0 || (rel < 32 && ((hi ? path_hi : path_lo) >> rel) != 0);
-    }
-    return page_seen(page, ctx + (hi ? j_hi : j_lo), p.window, p.sinks);
-  };
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
@@ -312,7 +296,7 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int slot = page * kBlock + n * 8 + 2 * t + (e & 1);
-          if (!sees(slot, ctx, e >= 2)) s[n][e] = -INFINITY;
+          if (!slot_visible(slot, ctx + (e < 2 ? j_lo : j_hi), p.window, p.sinks)) s[n][e] = -INFINITY;
         }
       }
     }
@@ -327,8 +311,8 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
     x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 1));
     x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 2));
     float n_lo = fmaxf(m_lo, x_lo * f), n_hi = fmaxf(m_hi, x_hi * f);
-    if (!kMasked || sees_page(page, ctx, false)) n_lo = fmaxf(n_lo, kNoWeight);
-    if (!kMasked || sees_page(page, ctx, true)) n_hi = fmaxf(n_hi, kNoWeight);
+    if (!kMasked || page_seen(page, ctx + j_lo, p.window, p.sinks)) n_lo = fmaxf(n_lo, kNoWeight);
+    if (!kMasked || page_seen(page, ctx + j_hi, p.window, p.sinks)) n_hi = fmaxf(n_hi, kNoWeight);
     const float z_lo = n_lo == -INFINITY ? 0.0f : n_lo, z_hi = n_hi == -INFINITY ? 0.0f : n_hi;
     const float k_lo = ex2(m_lo - z_lo), k_hi = ex2(m_hi - z_hi);
     m_lo = n_lo;
@@ -388,8 +372,8 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
           // of the lane that holds the key's probabilities
           const uint32_t has = __shfl_sync(0xffffffffu, some, (lane & ~3) | (key % 8 / 2)) << (key / 8 * 2 + (key & 1 ? 0 : 16));
           const float none_lo = has >> 31 ? 0.0f : NAN, none_hi = (has >> 30) & 1 ? 0.0f : NAN;
-          const bool see_lo = sees(page * kBlock + key, ctx, false);
-          const bool see_hi = sees(page * kBlock + key, ctx, true);
+          const bool see_lo = slot_visible(page * kBlock + key, ctx + j_lo, p.window, p.sinks);
+          const bool see_hi = slot_visible(page * kBlock + key, ctx + j_hi, p.window, p.sinks);
           if (!see_lo && !see_hi) continue;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
@@ -412,7 +396,7 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
   while (pos < t_end) {
     find();
     const int i0 = pos - p0, i1 = min(t_end, p1) - p0, n_tiles = p1 - p0;
-    const PageSpan span = kOwn ? own_span(ctx, p.R, __ldcg(p.prefix_view.first + b)) : page_span(ctx, p.R, p.window, p.sinks);
+    const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
     const bool alone = n_tiles == 1;      // its part does the request by itself, and the others go on
     if (alone && tile != kp) {
       if (++tile == p.key_parts) tile = 0;
@@ -435,39 +419,6 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
       qa[kk][3] = __ldg(hi + kk * 8 + 4 + t);
     }
     clear();
-    if constexpr (kOwn) {
-      path_lo = tree_path_mask(p.prefix_view.parents, b, p.R, j_lo, p.err);
-      path_hi = tree_path_mask(p.prefix_view.parents, b, p.R, j_hi, p.err);
-      const int gi = __ldcg(p.prefix_view.group_of + b);
-      if (i0 == 0 && gi >= 0) {
-        // The prefix, as if it were this request's: each part takes every key_parts-th partial result.
-        const PrefixHead head = load_head(p.prefix_view.head);
-        const PrefixGroup grp = load_group(p.prefix_view.groups + gi);
-        const int at = alone ? 0 : kp, step = alone ? 1 : p.key_parts;
-        const PrefixRow lo = prefix_row(p.prefix_view, head, grp, p.R, p.group, b, kvh, c_lo, D);
-        const PrefixRow hi = prefix_row(p.prefix_view, head, grp, p.R, p.group, b, kvh, c_hi, D);
-        const int rows = p.prefix_view.shape.rows;
-        // (o of this lane: dims 8 i + 2 t and the next)
-        auto take = [&](const PrefixRow& r, float& m, float& l, int e) {
-          for (int k = at; k < r.n; k += step) {
-            const float2 ml = __ldcg(r.ml + (int64_t)k * r.step * rows);
-            const float* from = r.o + (int64_t)k * r.step * rows * D + (t >> 1) * rows * 4 + (t & 1) * 2;
-            const float n = fmaxf(m, ml.x);
-            const float a = m == -INFINITY ? 0.0f : ex2(m - n), x = ml.x == -INFINITY ? 0.0f : ex2(ml.x - n);
-            l = l * a + (t == 0 ? ml.y * x : 0.0f);    // the four lanes of a row add up
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(from + i * 2 * rows * 4));
-              o[i][e] = o[i][e] * a + v.x * x;
-              o[i][e + 1] = o[i][e + 1] * a + v.y * x;
-            }
-            m = n;
-          }
-        };
-        take(lo, m_lo, l_lo, 0);
-        take(hi, m_hi, l_hi, 2);
-      }
-    }
 
     for (int i = i0; i < i1; ++i) {
       if (tile == kp) {
@@ -480,7 +431,7 @@ __global__ void __launch_bounds__(kMaxWarps* kWarp, 1)
         } else {
           if (stage_valid[stage]) {
             const int page = span.page(i), first = page * kBlock, last = first + kBlock - 1;
-            const bool whole = last <= ctx && (kOwn || p.window == 0 || first > ctx + p.R - 1 - p.window || last < p.sinks);
+            const bool whole = last <= ctx && (p.window == 0 || first > ctx + p.R - 1 - p.window || last < p.sinks);
             if (whole) consume(page, ctx, std::false_type());
             else consume(page, ctx, std::true_type());
           }
@@ -570,7 +521,7 @@ void layout(const mtp_window_attn_args& a, int sm_count, WindowPlan* pl) {
   pl->ctas_per_head = head_ctas(a, sm_count, (long long)a.Hkv * pl->row_tiles);
 }
 
-template <int D, bool kOwn>
+template <int D>
 cudaError_t launch(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
   auto encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
@@ -587,10 +538,10 @@ cudaError_t launch(const mtp_window_attn_args& a, const WindowPlan& pl, const Wi
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+  cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(pl.ctas_per_head * a.Hkv * pl.row_tiles);
-  return launch_behind_append(window_mma_kernel<D, kOwn>, grid, (pl.row_warps * pl.key_parts + 1) * kWarp, pl.smem, s, maps[0],
+  return launch_behind_append(window_mma_kernel<D>, grid, (pl.row_warps * pl.key_parts + 1) * kWarp, pl.smem, s, maps[0],
                               maps[1], p);
 }
 
@@ -607,11 +558,7 @@ WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count) {
 }
 
 cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
-  return a.d == 128 ? launch<128, false>(a, pl, p, s) : launch<64, false>(a, pl, p, s);
-}
-
-cudaError_t launch_window_mma_own(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s) {
-  return a.d == 128 ? launch<128, true>(a, pl, p, s) : launch<64, true>(a, pl, p, s);
+  return a.d == 128 ? launch<128>(a, pl, p, s) : launch<64>(a, pl, p, s);
 }
 
 }  // namespace mtp

@@ -178,10 +178,7 @@ __device__ void window_schedule(const WindowSchedule& w) {
     n = 0;
     if (b < w.B) {
       ctx = w.ctx_lens[b];                // a bad length has no pages: its rows stay as they were
-      if (ctx >= 0 && ctx <= w.max_blocks * kBlock - w.R) {
-        n = page_span(ctx, w.R, w.window, w.sinks).n;
-        if (w.first != nullptr) n = w.first[b] < 0 ? 0 : n - w.first[b];
-      }
+      if (ctx >= 0 && ctx <= w.max_blocks * kBlock - w.R) n = page_span(ctx, w.R, w.window, w.sinks).n;
     }
     most = max(most, n);
     p1 = n;
