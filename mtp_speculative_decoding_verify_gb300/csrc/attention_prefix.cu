@@ -312,10 +312,10 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
     pl->own_stats = take(n * sizeof(float));
     pl->own_parts = take(n * a.d * sizeof(float));
   } else {
-    pl->own = plan_prefix_own(a, sm_count);
+    pl->own = plan_prefix_own(a);
     const long long own_items = (long long)a.B * a.Hkv * pl->own.row_tiles;
     if (own_items * a.max_blocks > limit) return false;
-    const size_t n = ((size_t)own_items + (size_t)pl->own.ctas * pl->own.teams) * pl->own.row_warps * 16;
+    const size_t n = ((size_t)own_items + (size_t)pl->ctas * pl->own.teams) * pl->own.row_warps * 16;
     pl->own_head = take(sizeof(PrefixHead));
     pl->pages = take(((size_t)a.B + 1) * sizeof(int32_t));
     pl->own_stats = take(n * sizeof(float2));
@@ -407,7 +407,6 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   p.max_blocks = a->max_blocks;
   p.num_blocks = a->num_blocks;
   p.sm_scale = a->sm_scale;
-  p.behind_prefix = a->G > 0;
   p.view.head = ps.head;
   p.view.groups = ps.groups;
   p.view.group_of = ps.group_of;
@@ -445,7 +444,9 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
     ps.own = reinterpret_cast<PrefixHead*>(ws + pl.own_head);
     ps.pages = i32(pl.pages);
     ps.own_heads = p.Hkv * pl.own.row_tiles;
-    ps.own_teams = pl.own.ctas * pl.own.teams;
+    ps.teams = pl.own.teams;
+    ps.unit_cost = a->d == 128 ? 1800 : 1400;
+    ps.page_cost = 3300 / pl.own.teams;
     p.row_tiles = pl.own.row_tiles;
     p.row_warps = pl.own.row_warps;
     p.teams = pl.own.teams;
@@ -463,17 +464,18 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return set_cuda_error(e, "kv append launch");
   if ((e = record(a->timing_events[0])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
-  if (a->G > 0) {
-    if (fp32) e = a->d == 128 ? launch_prefix_simt<128>(p, pl.ctas, s) : launch_prefix_simt<64>(p, pl.ctas, s);
-    else e = launch_prefix_tc(*a, p, pl.ctas, s);
-    if (e != cudaSuccess) return set_cuda_error(e, "prefix attention launch");
+  if (fp32) {
+    if (a->G > 0 && (e = a->d == 128 ? launch_prefix_simt<128>(p, pl.ctas, s) : launch_prefix_simt<64>(p, pl.ctas, s)) != cudaSuccess)
+      return set_cuda_error(e, "prefix attention launch");
+    e = launch_window_simt_own(w, a->d, s);
+  } else {
+    e = launch_prefix_tc(*a, p, pl.ctas, s);
   }
-  e = fp32 ? launch_window_simt_own(w, a->d, s) : launch_prefix_own(*a, p, pl.own, s);
   if (e != cudaSuccess) return set_cuda_error(e, "attention launch");
   e = launch_prefix_join(*a, p, s);
   if (e != cudaSuccess) return set_cuda_error(e, "attention join launch");
   if ((e = record(a->timing_events[1])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
-  set_launch_count(a->G > 0 ? 4 : 3);
+  set_launch_count(fp32 && a->G > 0 ? 4 : 3);
   return MTP_OK;
 }
 

@@ -78,16 +78,15 @@ struct PrefixParams {
   const float *part_o, *part_lse;
   // bf16: the kernel of the own pages
   int row_tiles, row_warps, teams, stages;   // tiles of 16 row_warps rows; teams of a CTA, stages of a team
-  int behind_prefix;                // it is launched behind the prefix's kernel (else behind the append)
   PrefixView view;
 };
 
 struct OwnPlan {
-  int row_tiles, row_warps, teams, stages, ctas;
+  int row_tiles, row_warps, teams, stages;
 };
-OwnPlan plan_prefix_own(const mtp_prefix_attn_args& a, int sm_count);
+OwnPlan plan_prefix_own(const mtp_prefix_attn_args& a);
+// bf16 rows: prefix and own pages.
 cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s);
-cudaError_t launch_prefix_own(const mtp_prefix_attn_args& a, const PrefixParams& p, const OwnPlan& pl, cudaStream_t s);
 cudaError_t launch_prefix_join(const mtp_prefix_attn_args& a, const PrefixParams& p, cudaStream_t s);
 
 // Written by one more CTA of the append.
@@ -100,7 +99,8 @@ struct PrefixSchedule {
   PrefixShape shape;
   PrefixHead* own;                  // nullptr: no line of own pages
   int32_t* pages;
-  int own_heads, own_teams;         // items of a request, shares
+  int own_heads, teams;             // items of a request; teams of a CTA that does own pages
+  int unit_cost, page_cost;         // of a CTA, for a unit of the prefix and a page of a request's own (ns)
   unsigned* err;
 };
 
@@ -209,22 +209,6 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
     }
     if (g < G) w.groups[g] = e;
   }
-  PrefixHead h;
-  h.total = base.x;
-  h.ctas = min(w.ctas, base.x);
-  h.size = h.ctas == 0 ? 1 : h.total / h.ctas;
-  h.more = h.ctas == 0 ? 0 : h.total - h.ctas * h.size;
-  if (threadIdx.x == 0) *w.head = h;
-  __syncthreads();                             // (writes to global memory too, for this CTA)
-  for (int c = threadIdx.x; c < h.ctas; c += THREADS) {
-    const int cut = prefix_cut(h, c);
-    int lo = 0, hi = G;                        // the last group whose line begins at or before the cut
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      (w.groups[mid].line <= cut ? lo : hi) = mid;
-    }
-    w.cta_group[c] = lo;
-  }
   for (int b = threadIdx.x; b < w.B; b += THREADS) {
     int lo = 0, hi = G, g = -1;                // the last group that begins at or before b, if b is in it
     while (hi - lo > 1) {
@@ -237,36 +221,57 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
     w.first[b] = first;
     w.group_of[b] = first > 0 ? g : -1;
   }
-  if (w.own == nullptr) return;
-  __syncthreads();
-  int at = 0;                                  // own pages of the requests so far
-  for (int b0 = 0; b0 < w.B; b0 += THREADS) {
-    const int b = b0 + threadIdx.x;
-    int n = 0;
-    if (b < w.B && w.first[b] >= 0) n = (w.ctx_lens[b] + w.R + kBlock - 1) / kBlock - w.first[b];
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    __syncthreads();                           // the last chunk's totals have been read
-    if (lane == kWarp - 1) s_sum[warp].x = incl;
+  int own = 0;                                 // own pages of the requests so far
+  if (w.own != nullptr) {
     __syncthreads();
-    incl += at;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) incl += s_sum[i].x;
-      at += s_sum[i].x;
+    for (int b0 = 0; b0 < w.B; b0 += THREADS) {
+      const int b = b0 + threadIdx.x;
+      int n = 0;
+      if (b < w.B && w.first[b] >= 0) n = (w.ctx_lens[b] + w.R + kBlock - 1) / kBlock - w.first[b];
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < kWarp; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      __syncthreads();                         // the last chunk's totals have been read
+      if (lane == kWarp - 1) s_sum[warp].x = incl;
+      __syncthreads();
+      incl += own;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) incl += s_sum[i].x;
+        own += s_sum[i].x;
+      }
+      if (b < w.B) w.pages[b + 1] = incl;
     }
-    if (b < w.B) w.pages[b + 1] = incl;
+    if (threadIdx.x == 0) w.pages[0] = 0;
   }
+  // CTAs for the prefix and for the own pages: so that both should end at once.
+  own *= w.own_heads;
+  int ctas = w.ctas;
+  if (own > 0 && base.x > 0) {
+    const float a = (float)base.x * w.unit_cost, z = (float)own * w.page_cost;
+    ctas = max(1, min(w.ctas - 1, (int)(w.ctas * a / (a + z) + 0.5f)));
+  }
+  auto shares = [](int total, int ctas) {
+    PrefixHead h{total, min(ctas, total), 1, 0};
+    if (h.ctas > 0) h.size = total / h.ctas, h.more = total - h.ctas * h.size;
+    return h;
+  };
+  const PrefixHead h = shares(base.x, ctas);
   if (threadIdx.x == 0) {
-    w.pages[0] = 0;
-    h.total = at * w.own_heads;
-    h.ctas = min(w.own_teams, h.total);
-    h.size = h.ctas == 0 ? 1 : h.total / h.ctas;
-    h.more = h.ctas == 0 ? 0 : h.total - h.ctas * h.size;
-    *w.own = h;
+    *w.head = h;
+    if (w.own != nullptr) *w.own = shares(own, (w.ctas - h.ctas) * w.teams);
+  }
+  __syncthreads();                             // (writes to global memory too, for this CTA)
+  for (int c = threadIdx.x; c < h.ctas; c += THREADS) {
+    const int cut = prefix_cut(h, c);
+    int lo = 0, hi = G;                        // the last group whose line begins at or before the cut
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      (w.groups[mid].line <= cut ? lo : hi) = mid;
+    }
+    w.cta_group[c] = lo;
   }
 }
 

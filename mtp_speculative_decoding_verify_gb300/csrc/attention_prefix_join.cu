@@ -1,0 +1,158 @@
+// The join of mtp_verify_attention_prefix: the results over the group's prefix
+// and over the request's own slots become the output.
+#include <math.h>
+
+#include "attention_prefix.h"
+#include "attention_window.h"
+#include "mma_sync.cuh"
+
+namespace mtp {
+namespace {
+
+constexpr int kJoinThreads = 128;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// out = (sum of o 2^(m - top)) / (sum of l 2^(m - top)) over a row's partial
+// results, the prefix's and then its own. A warp takes 8 rows of one KV head,
+// as they lie in the results, and SLICES x 16 dims, 4 of each a lane: all dims
+// where there are rows enough to fill the device, so that the finding of the
+// results is paid once a row; else a slice, for which more warps share the work.
+// Up to eight results are read as one batch. Bound by what it reads, out of L2
+// mostly, and by four dependent reads where that is little.
+template <typename T>
+__device__ __forceinline__ void store4(T* to, float4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float* to, float4 v) {
+  *reinterpret_cast<float4*>(to) = v;
+}
+template <>
+__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* to, float4 v) {
+  *reinterpret_cast<uint2*>(to) = make_uint2(mma::pack_bf16(v.x, v.y), mma::pack_bf16(v.z, v.w));
+}
+
+template <typename T, int D, int SLICES>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p, unsigned n_rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr bool kFp32 = sizeof(T) == 4;
+  constexpr unsigned kUnits = D / 16 / SLICES;   // warps that share a row
+  constexpr int kMost = 8;
+  const unsigned lane = threadIdx.x % kWarp, unit = blockIdx.x * (kJoinThreads / kWarp) + threadIdx.x / kWarp;
+  const unsigned idx = unit / kUnits * 8 + lane / 4;
+  const int dim4 = unit % kUnits * SLICES * 4 + lane % 4;   // 4 dims from 4 dim4 + 16 x on
+  if (idx >= n_rows) return;
+  const unsigned rows = p.rows, bh = idx / rows, r = idx - bh * rows, b = bh / (unsigned)p.Hkv, kvh = bh - b * p.Hkv;
+  const PrefixView& v = p.view;
+  const int first = __ldcg(v.first + b), gi = __ldcg(v.group_of + b);
+  const PrefixHead head = load_head(v.head);
+  const unsigned j = r / (unsigned)p.group, h = kvh * p.group + (r - j * p.group);
+  const int64_t row = ((int64_t)b * p.R + j) * p.Hq + h;
+  // The own results: n1 of them.
+  const float *o1, *m1;                      // (fp32 rows: o / l and log2 of the weight)
+  int n1;
+  int64_t step1;                             // rows from one to the next
+  if constexpr (kFp32) {
+    n1 = p.n_splits;
+    step1 = 1;
+    o1 = p.part_o + row * n1 * D;
+    m1 = p.part_lse + row * n1;
+  } else {
+    const PrefixHead own = load_head(v.own);
+    const int before = __ldcg(v.pages + b), pages = __ldcg(v.pages + b + 1) - before;
+    const unsigned tile_rows = p.row_warps * 16, tile = r / tile_rows;
+    const int heads = p.Hkv * p.row_tiles, hr = kvh * p.row_tiles + tile, u0 = before * heads + hr * pages;
+    const int c0 = prefix_cta_of(own, u0), c1 = prefix_cta_of(own, u0 + pages - 1);
+    const int64_t at = ((int64_t)b * heads + hr + c0) * tile_rows + (r - tile * tile_rows);
+    n1 = c1 - c0 + 1;
+    step1 = tile_rows;
+    o1 = v.own_parts + at * D;
+    m1 = reinterpret_cast<const float*>(v.own_stats + at);
+  }
+  if (first < 0) return;                     // flagged; its rows stay as they were
+  PrefixRow pre{nullptr, nullptr, 0, 0};
+  if (gi >= 0) pre = prefix_row(v, head, load_group(v.groups + gi), p.R, p.group, b, kvh, r, D);
+  const int n = pre.n + n1, rows0 = v.shape.rows;
+
+  float m = -INFINITY, l = 0.0f;
+  float4 o[SLICES];
+#pragma unroll
+  for (int x = 0; x < SLICES; ++x) o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k0 = 0; k0 < n; k0 += kMost) {
+    float2 ml[kMost];
+    const float* from[kMost];
+    int step[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      from[k] = nullptr;
+      step[k] = 0;
+      const int i = k0 + k;
+      if (i < pre.n) {
+        const int64_t at = (int64_t)i * pre.step * rows0;
+        ml[k] = __ldcg(pre.ml + at);
+        from[k] = pre.o + at * D + dim4 * rows0 * 4;
+        step[k] = rows0 * 16;                // from 4 dims to those 16 on
+      } else if (i < n) {
+        const int64_t at = (i - pre.n) * step1;
+        if constexpr (kFp32) {
+          const float w = __ldcg(m1 + at);
+          ml[k] = make_float2(w, w == -INFINITY || w == kNoWeight ? 0.0f : 1.0f);
+        } else {
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(m1) + at);
+        }
+        from[k] = o1 + at * D + dim4 * 4;
+        step[k] = 16;
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) top = fmaxf(top, ml[k].x);
+    const float a = m == -INFINITY ? 0.0f : ex2(m - top);
+    m = top;
+    l *= a;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      ml[k].x = ml[k].x == -INFINITY ? 0.0f : ex2(ml[k].x - top);
+      l += ml[k].y * ml[k].x;
+    }
+#pragma unroll
+    for (int x = 0; x < SLICES; ++x) {
+      float4 w[kMost];
+#pragma unroll
+      for (int k = 0; k < kMost; ++k)
+        w[k] = from[k] != nullptr ? __ldcg(reinterpret_cast<const float4*>(from[k] + x * step[k])) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      o[x].x *= a, o[x].y *= a, o[x].z *= a, o[x].w *= a;
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        if (k0 + k >= n) break;              // (0 x NaN of a part that is none)
+        const float c = ml[k].x;
+        o[x].x += w[k].x * c, o[x].y += w[k].y * c, o[x].z += w[k].z * c, o[x].w += w[k].w * c;
+      }
+    }
+  }
+  // no weight: nothing seen (bad blocks only), or -inf only
+  const float inv = l != 0.0f ? 1.0f / l : m == -INFINITY ? 0.0f : NAN;
+#pragma unroll
+  for (int x = 0; x < SLICES; ++x)
+    store4<T>(static_cast<T*>(p.out) + row * D + dim4 * 4 + x * 16, make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv));
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const PrefixParams& p, cudaStream_t s) {
+  const unsigned rows = (unsigned)p.B * p.Hkv * p.rows, groups = (rows + 7) / 8, warps = kJoinThreads / kWarp;
+  if (rows >= 8192) return launch_behind_append(prefix_join_kernel<T, D, D / 16>, (groups + warps - 1) / warps, kJoinThreads, 0, s, p, rows);
+  return launch_behind_append(prefix_join_kernel<T, D, 1>, (groups * (D / 16) + warps - 1) / warps, kJoinThreads, 0, s, p, rows);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_join(const mtp_prefix_attn_args& a, const PrefixParams& p, cudaStream_t s) {
+  if (a.dtype == MTP_F32) return a.d == 128 ? launch_join<float, 128>(p, s) : launch_join<float, 64>(p, s);
+  return a.d == 128 ? launch_join<__nv_bfloat16, 128>(p, s) : launch_join<__nv_bfloat16, 64>(p, s);
+}
+
+}  // namespace mtp

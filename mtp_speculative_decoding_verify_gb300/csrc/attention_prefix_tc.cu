@@ -1,7 +1,11 @@
-// The prefix of mtp_verify_attention_prefix for bf16 rows, on the
-// 5th-generation tensor cores.
+// mtp_verify_attention_prefix for bf16 rows: the groups' prefixes on the
+// 5th-generation tensor cores, and beside them, on other CTAs of the same
+// launch, the requests' own pages (attention_prefix_own.cuh). The first is bound by
+// products and the second by the read of the cache, and neither needs the whole
+// device for that: side by side they take less than one after the other. How many
+// CTAs do which is worked out with the shares (prefix_schedule).
 //
-// For every item (attention_prefix.h: up to 256 rows of a group and KV head)
+// The prefix. For every item (attention_prefix.h: up to 256 rows of a group and KV head)
 // and the tiles of 128 keys in this CTA's share of it,
 //   S = Q K^T,  P = 2^(scale log2e S - m),  O += P V,  l += sum P,
 // left as partial results (O, m, l). The rows of all requests of a group are
@@ -27,7 +31,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include "attention_prefix.h"
+#include "attention_prefix_own.cuh"
 #include "attention_window.h"
 #include "sm100.cuh"
 
@@ -52,11 +56,14 @@ struct Smem {
   static constexpr int kTile = D / 64 * kChunk;                 // Q of 128 rows, K or V of 128 keys
   static constexpr int kQ = 0, kRing = 2 * kTile;
   static constexpr int kSlots = D == 128 ? 5 : 12;              // K and V tiles in turn
-  static constexpr int kBar = kRing + kSlots * kTile;
+  static constexpr int kBar = kRing + kSlots * kTile;           // behind the stages of the own pages, too
   static constexpr int kBars = 2 * kSlots + 2 + 6 + kInfo + 1;
   static constexpr int kMisc = kBar + kBars * 8;                // marks [kInfo], abort, TMEM base
-  static constexpr int kBytes = kMisc + kInfo * 4 + 8 + 1024;
+  static constexpr int kOwnStages = kBar / own::Stage<D>::kBytes;
+  static constexpr int kOwn = kMisc + kInfo * 4 + 8;            // own::Control
+  static constexpr int kBytes = kOwn + kOwnStages * 20 + 1024;
   static_assert(kBytes <= 232448, "227 KB of shared memory");
+  static_assert(kOwn % 8 == 0, "barriers are 8 bytes");
 };
 
 // ------------------------------------------------------------- instructions
@@ -144,7 +151,6 @@ struct Walk {
   __device__ __forceinline__ explicit Walk(const PrefixParams& params) : p(params), cta(blockIdx.x) {
     head = load_head(p.view.head);
     pos = end = 0;
-    if (cta >= head.ctas) return;
     pos = prefix_cut(head, cta);
     end = prefix_cut(head, cta + 1);
     gi = __ldcg(p.view.cta_group + cta);
@@ -169,8 +175,9 @@ struct Walk {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_own_k,
+                  const __grid_constant__ CUtensorMap tm_own_v, const PrefixParams p) {
   using S = Smem<D>;
   constexpr int kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -188,7 +195,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMisc + kInfo * 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc + kInfo * 4 + 4);
 
+  const int n_own = p.teams * p.stages;
+  own::Control oc;
+  oc.full = reinterpret_cast<uint64_t*>(smem + S::kOwn);
+  oc.empty = oc.full + n_own;
+  oc.valid = reinterpret_cast<volatile int*>(oc.empty + n_own);
+  oc.abort = abort;
+
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  if (warp == 2) {
+    for (int i = lane; i < n_own; i += kWarp) {
+      sm100::mbar_init(&oc.full[i], 1);
+      sm100::mbar_init(&oc.empty[i], p.row_warps);
+    }
+    sm100::fence_barrier_init();
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       sm100::mbar_init(&full[i], 1);
@@ -208,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::tma_prefetch_desc(&tm_q);
     sm100::tma_prefetch_desc(&tm_k);
     sm100::tma_prefetch_desc(&tm_v);
+    sm100::tma_prefetch_desc(&tm_own_k);
+    sm100::tma_prefetch_desc(&tm_own_v);
   }
   if (warp == 1) {
     sm100::tmem_alloc(tmem_slot, 512);
@@ -221,6 +244,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // reads what it writes.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
+  const int prefix_ctas = __ldcg(&p.view.head->ctas);
+  if ((int)blockIdx.x >= prefix_ctas) {
+    // ----------------------------------------------------------- own pages
+    // (56 + 2 x 224 = 3 x 168 registers a thread)
+    const int cta = blockIdx.x - prefix_ctas;
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == 0) own::producer<D>(tm_own_k, tm_own_v, p, smem, oc, cta);
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+      own::consumer<D>(p, smem, oc, cta, warp - 4);
+    }
+    __syncthreads();
+    if (warp == 1) sm100::tmem_dealloc(tmem, 512);
+    return;
+  }
   Walk walk(p);
   Seg seg;
   bool ok = true;
@@ -502,23 +541,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s) {
   const PrefixShape& shape = p.view.shape;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, ok, ov;
   const cuuint64_t group = (cuuint64_t)p.group, Hkv = (cuuint64_t)a.Hkv;
   const cuuint64_t qdims[4] = {(cuuint64_t)D, group, Hkv, (cuuint64_t)a.B * p.R};
   const cuuint64_t qstrides[3] = {D * 2, group * D * 2, (cuuint64_t)a.Hq * D * 2};
   const cuuint32_t qbox[4] = {64, (cuuint32_t)std::min(p.group, kRows), 1, (cuuint32_t)shape.tokens};
   const cuuint64_t dims[4] = {(cuuint64_t)D, Hkv, (cuuint64_t)kBlock, (cuuint64_t)a.num_blocks};
   const cuuint64_t strides[3] = {D * 2, Hkv * D * 2, kBlock * Hkv * D * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1}, own_box[4] = {64, 1, (cuuint32_t)own::kKeys, 1};
   if (!make_bf16_map(&tq, a.q, 4, qdims, qstrides, qbox) || !make_bf16_map(&tk, a.k_cache, 4, dims, strides, box) ||
-      !make_bf16_map(&tv, a.v_cache, 4, dims, strides, box))
+      !make_bf16_map(&tv, a.v_cache, 4, dims, strides, box) || !make_bf16_map(&ok, a.k_cache, 4, dims, strides, own_box) ||
+      !make_bf16_map(&ov, a.v_cache, 4, dims, strides, own_box))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_behind_append(prefix_tc_kernel<D>, (unsigned)ctas, kThreads, Smem<D>::kBytes, s, tq, tk, tv, p);
+  return launch_behind_append(prefix_kernel<D>, (unsigned)ctas, kThreads, Smem<D>::kBytes, s, tq, tk, tv, ok, ov, p);
+}
+
+template <int D>
+void lay_out(const mtp_prefix_attn_args& a, OwnPlan* pl) {
+  const int blocks = (a.Hq / a.Hkv * (a.D + 1) + 15) / 16;     // of 16 rows
+  pl->row_tiles = (blocks + own::kWarps - 1) / own::kWarps;
+  pl->row_warps = (blocks + pl->row_tiles - 1) / pl->row_tiles;
+  // As many teams as there are warps for, with two stages each at least.
+  pl->teams = std::min(own::kWarps / pl->row_warps, Smem<D>::kOwnStages / 2);
+  pl->stages = std::min(own::kMaxStages, Smem<D>::kOwnStages / pl->teams);
 }
 
 }  // namespace
+
+OwnPlan plan_prefix_own(const mtp_prefix_attn_args& a) {
+  OwnPlan pl{};
+  a.d == 128 ? lay_out<128>(a, &pl) : lay_out<64>(a, &pl);
+  return pl;
+}
 
 cudaError_t launch_prefix_tc(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s) {
   return a.d == 128 ? launch<128>(a, p, ctas, s) : launch<64>(a, p, ctas, s);
