@@ -32,19 +32,22 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------- append
-// One CTA per (request, verify token), as window_append_kernel; a request that
-// its group's prefix rules out is left alone.
-__global__ void __launch_bounds__(128) prefix_append_kernel(const uint4* __restrict__ k_new,
-                                                            const uint4* __restrict__ v_new, uint4* __restrict__ k_cache,
-                                                            uint4* __restrict__ v_cache,
-                                                            const int32_t* __restrict__ block_table, int vecs, int num_blocks,
-                                                            const PrefixSchedule prefix) {
+// One CTA per (request, verify token): its K and V rows go to slot ctx+j of the
+// cache, 16 bytes a thread; a request that its group's prefix rules out is left
+// alone. The last CTA works out the shares.
+constexpr int kAppendThreads = 256;
+
+__global__ void __launch_bounds__(kAppendThreads) prefix_append_kernel(const uint4* __restrict__ k_new,
+                                                                       const uint4* __restrict__ v_new,
+                                                                       uint4* __restrict__ k_cache, uint4* __restrict__ v_cache,
+                                                                       const int32_t* __restrict__ block_table, int vecs,
+                                                                       int num_blocks, const PrefixSchedule prefix) {
   asm volatile("griddepcontrol.launch_dependents;");   // (the kernels behind it may set up)
-  if (blockIdx.x == gridDim.x - 1) {
-    prefix_schedule<128>(prefix);
+  if (blockIdx.x == 0) {                       // first, since the others wait for it
+    prefix_schedule<kAppendThreads>(prefix);
     return;
   }
-  const int R = prefix.R, b = blockIdx.x / R, j = blockIdx.x % R;
+  const int R = prefix.R, bj = blockIdx.x - 1, b = bj / R, j = bj % R;
   const int ctx = prefix.ctx_lens[b];
   bool bad;
   const int g = find_group(prefix.group_starts, prefix.G, prefix.B, b, &bad);
@@ -58,10 +61,10 @@ __global__ void __launch_bounds__(128) prefix_append_kernel(const uint4* __restr
     if (threadIdx.x == 0) raise_error(prefix.err, MTP_ERR_BLOCK_ID);
     return;
   }
-  const int64_t from = (int64_t)blockIdx.x * vecs, to = ((int64_t)blk * kBlock + (ctx + j) % kBlock) * vecs;
-  for (int i = threadIdx.x; i < vecs; i += 128) {
-    k_cache[to + i] = k_new[from + i];
-    v_cache[to + i] = v_new[from + i];
+  const int64_t from = (int64_t)bj * vecs, to = ((int64_t)blk * kBlock + (ctx + j) % kBlock) * vecs;
+  for (int i = threadIdx.x; i < 2 * vecs; i += kAppendThreads) {
+    if (i < vecs) k_cache[to + i] = k_new[from + i];
+    else v_cache[to + i - vecs] = v_new[from + i - vecs];
   }
 }
 
@@ -89,10 +92,10 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const PrefixPa
   const PrefixView& v = p.view;
   const PrefixHead head = load_head(v.head);
   if ((int)blockIdx.x >= head.ctas) return;
-  int pos = prefix_cut(head, blockIdx.x);
-  const int end = prefix_cut(head, blockIdx.x + 1);
-  int gi = v.cta_group[blockIdx.x];
-  PrefixGroup g = load_group(v.groups + gi);
+  const PrefixStart start = v.starts[blockIdx.x];
+  int pos = start.pos, gi = start.gi;
+  const int end = start.end;
+  PrefixGroup g = start.group;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const float f = p.sm_scale * kLog2e;
   const float *q = static_cast<const float*>(p.q), *kc = static_cast<const float*>(p.k_cache), *vc = static_cast<const float*>(p.v_cache);
@@ -278,7 +281,7 @@ struct PrefixPlan {
   OwnPlan own;                         // bf16
   int n_splits;                        // fp32
   // byte offsets in the workspace
-  size_t head, groups, group_of, first, cta_group, parts, stats, own_head, pages, own_parts, own_stats, bytes;
+  size_t head, groups, group_of, first, starts, own_starts, parts, stats, own_head, pages, own_parts, own_stats, bytes;
 };
 
 // False: more items or units than 31 bits count.
@@ -286,7 +289,7 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   const int group = a.Hq / a.Hkv, R = a.D + 1, G = std::min(a.G, a.B);   // (empty groups have no items)
   const bool fp32 = fp32_rows(a);
   pl->shape = fp32 ? prefix_shape(kRows, 1, 1, group) : prefix_shape(kPrefixTcRows, 2, 2, group);
-  pl->ctas = fp32 ? 2 * sm_count : sm_count;
+  pl->ctas = fp32 ? 2 * sm_count : std::max(4, sm_count / 2 * 2);   // bf16: pairs
   const long long limit = 0x7fffffffll - 0x10000;
   // Items of all groups: the tiles of all rows, and the ones that each group leaves part of empty.
   const long long tiles = ((long long)a.B * R / pl->shape.tokens + G) * pl->shape.chunks;
@@ -303,7 +306,7 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   pl->groups = take((size_t)a.G * sizeof(PrefixGroup));
   pl->group_of = take((size_t)a.B * sizeof(int32_t));
   pl->first = take((size_t)a.B * sizeof(int32_t));
-  pl->cta_group = take((size_t)pl->ctas * sizeof(int32_t));
+  pl->starts = take((size_t)pl->ctas * sizeof(PrefixStart));
   pl->stats = take(results * sizeof(float2));
   pl->parts = take(results * a.d * sizeof(float));
   if (fp32) {
@@ -318,6 +321,7 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
     const size_t n = ((size_t)own_items + (size_t)pl->ctas * pl->own.teams) * pl->own.row_warps * 16;
     pl->own_head = take(sizeof(PrefixHead));
     pl->pages = take(((size_t)a.B + 1) * sizeof(int32_t));
+    pl->own_starts = take((size_t)pl->ctas * pl->own.teams * sizeof(OwnStart));
     pl->own_stats = take(n * sizeof(float2));
     pl->own_parts = take(n * a.d * sizeof(float));
   }
@@ -378,7 +382,7 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   ps.groups = reinterpret_cast<PrefixGroup*>(ws + pl.groups);
   ps.group_of = i32(pl.group_of);
   ps.first = i32(pl.first);
-  ps.cta_group = i32(pl.cta_group);
+  ps.starts = reinterpret_cast<PrefixStart*>(ws + pl.starts);
   ps.group_starts = a->group_starts;
   ps.prefix_blocks = a->prefix_blocks;
   ps.ctx_lens = a->ctx_lens;
@@ -411,7 +415,7 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   p.view.groups = ps.groups;
   p.view.group_of = ps.group_of;
   p.view.first = ps.first;
-  p.view.cta_group = ps.cta_group;
+  p.view.starts = ps.starts;
   p.view.parts = reinterpret_cast<float*>(ws + pl.parts);
   p.view.stats = reinterpret_cast<float2*>(ws + pl.stats);
   p.view.parents = a->parents;
@@ -443,23 +447,26 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   } else {
     ps.own = reinterpret_cast<PrefixHead*>(ws + pl.own_head);
     ps.pages = i32(pl.pages);
+    ps.own_starts = reinterpret_cast<OwnStart*>(ws + pl.own_starts);
     ps.own_heads = p.Hkv * pl.own.row_tiles;
     ps.teams = pl.own.teams;
     ps.unit_cost = a->d == 128 ? 1800 : 1400;
-    ps.page_cost = 3300 / pl.own.teams;
+    ps.page_cost = 2600 / pl.own.teams;
+    ps.item_cost = 1800 / pl.own.teams;
     p.row_tiles = pl.own.row_tiles;
     p.row_warps = pl.own.row_warps;
     p.teams = pl.own.teams;
     p.stages = pl.own.stages;
     p.view.own = ps.own;
     p.view.pages = ps.pages;
+    p.view.own_starts = ps.own_starts;
     p.view.own_parts = reinterpret_cast<float*>(ws + pl.own_parts);
     p.view.own_stats = reinterpret_cast<float2*>(ws + pl.own_stats);
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto record = [&](void* ev) { return ev ? cudaEventRecord(static_cast<cudaEvent_t>(ev), s) : cudaSuccess; };
   const int vecs = a->Hkv * a->d * (fp32 ? 4 : 2) / 16;
-  prefix_append_kernel<<<a->B * p.R + 1, 128, 0, s>>>((const uint4*)a->k_new, (const uint4*)a->v_new, (uint4*)a->k_cache,
+  prefix_append_kernel<<<a->B * p.R + 1, kAppendThreads, 0, s>>>((const uint4*)a->k_new, (const uint4*)a->v_new, (uint4*)a->k_cache,
                                                      (uint4*)a->v_cache, a->block_table, vecs, a->num_blocks, ps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return set_cuda_error(e, "kv append launch");

@@ -33,6 +33,18 @@ struct alignas(16) PrefixHead {
   int32_t total, ctas;              // units of the line, shares
   int32_t size, more;               // units of a share; the first `more` have one more
 };
+// Where a share begins.
+struct alignas(16) PrefixStart {
+  PrefixGroup group;
+  int32_t gi;                       // which group that is
+  int32_t pos, end;                 // units of the line
+  int32_t pad;
+};
+struct alignas(16) OwnStart {
+  int32_t pos, end;                 // pages of the line
+  int32_t b, before, pages;         // the request, own pages of those before it (of one head), its own
+  int32_t pad[3];
+};
 
 constexpr int kPrefixTcRows = 128;  // of a tile on the tensor cores: two tiles an item, two pages a unit
 
@@ -53,7 +65,7 @@ struct PrefixView {
   const PrefixGroup* groups;
   const int32_t* group_of;          // [B] group of a request that has a prefix, else -1
   const int32_t* first;             // [B] first page of a request's own; -1: the request is skipped
-  const int32_t* cta_group;         // [ctas] group in which a CTA's share begins
+  const PrefixStart* starts;        // [ctas]
   float* parts;                     // [partial result][sub][d/4][rows][4]: sums of p v, not divided
   float2* stats;                    // [partial result][sub][rows]: maximum (log2 units), sum of p
   const int32_t* parents;           // [B, R] or NULL
@@ -61,6 +73,7 @@ struct PrefixView {
   // bf16 rows: the own pages
   const PrefixHead* own;
   const int32_t* pages;             // [B+1] own pages of the requests before each
+  const OwnStart* own_starts;       // [teams]
   float* own_parts;                 // [partial result][rows of a tile][d]
   float2* own_stats;                // [partial result][rows of a tile]
 };
@@ -93,14 +106,16 @@ cudaError_t launch_prefix_join(const mtp_prefix_attn_args& a, const PrefixParams
 struct PrefixSchedule {
   PrefixHead* head;                 // nullptr: nothing to prepare
   PrefixGroup* groups;
-  int32_t *group_of, *first, *cta_group;
+  int32_t *group_of, *first;
+  PrefixStart* starts;
   const int32_t *group_starts, *prefix_blocks, *ctx_lens;
   int G, B, R, Hkv, max_blocks, ctas;
   PrefixShape shape;
   PrefixHead* own;                  // nullptr: no line of own pages
   int32_t* pages;
+  OwnStart* own_starts;
   int own_heads, teams;             // items of a request; teams of a CTA that does own pages
-  int unit_cost, page_cost;         // of a CTA, for a unit of the prefix and a page of a request's own (ns)
+  int unit_cost, page_cost, item_cost;   // of a CTA, for a unit of the prefix, a page and an item of the requests' own (ns)
   unsigned* err;
 };
 
@@ -164,24 +179,78 @@ __device__ __forceinline__ int own_first(int blocks, int ctx, int max_blocks, in
   return blocks < 0 || blocks > max_blocks || ctx < blocks * kBlock ? -1 : blocks;
 }
 
+// The last of n entries (n >= 1, not decreasing) that is at most x, else 0.
+__device__ __forceinline__ int last_at_most(const int32_t* v, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    (v[mid] <= x ? lo : hi) = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ PrefixHead make_shares(int total, int ctas) {
+  PrefixHead h{total, min(ctas, total), 1, 0};
+  if (h.ctas > 0) h.size = total / h.ctas, h.more = total - h.ctas * h.size;
+  return h;
+}
+
+// The work of one CTA of THREADS threads. It stands between the lengths and
+// the attention: each input is read once, in parallel, and searches go through
+// copies in shared memory (of up to kCopy groups and requests).
 template <int THREADS>
 __device__ void prefix_schedule(const PrefixSchedule& w) {
-  constexpr int kWarps = THREADS / kWarp;
+  constexpr int kWarps = THREADS / kWarp, kCopy = 1024;
   __shared__ int2 s_sum[kWarps];
-  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-  bool bad;
-  find_group(w.group_starts, w.G, w.B, -1, &bad);
-  if (bad && threadIdx.x == 0) raise_error(w.err, MTP_ERR_LENGTH);
+  __shared__ int32_t s_start[kCopy + 1], s_blocks[kCopy], s_line[kCopy], s_pages[kCopy + 1];
+  const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+  // Sums of v over the threads before this one, and over all of them.
+  auto scan = [&](int2 v, int2* total) {
+    int2 incl = v;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) incl.x += x, incl.y += y;
+    }
+    __syncthreads();                           // the last totals have been read
+    if (lane == kWarp - 1) s_sum[warp] = incl;
+    __syncthreads();
+    incl.x -= v.x, incl.y -= v.y;
+    *total = make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int2 t = s_sum[i];
+      if (i < warp) incl.x += t.x, incl.y += t.y;
+      total->x += t.x, total->y += t.y;
+    }
+    return incl;
+  };
+
+  const int ctx0 = tid < w.B ? w.ctx_lens[tid] : 0;   // (on its way while the groups are looked at)
+  int wrong = 0;
+  for (int g = tid; g < w.G; g += THREADS) {
+    const int s0 = w.group_starts[g], s1 = w.group_starts[g + 1], blocks = w.prefix_blocks[g];
+    wrong |= s0 < 0 || s1 < s0 || s1 > w.B;
+    if (w.G <= kCopy) {
+      s_start[g] = s0;
+      s_start[g + 1] = s1;                     // (its neighbour writes the same)
+      s_blocks[g] = blocks;
+    }
+  }
+  const bool bad = __syncthreads_or(wrong) != 0;
+  if (bad && tid == 0) raise_error(w.err, MTP_ERR_LENGTH);
   const int G = bad ? 0 : w.G;                 // every request by itself
+  const int32_t *starts = w.G <= kCopy ? s_start : w.group_starts, *blocks_of = w.G <= kCopy ? s_blocks : w.prefix_blocks;
+
   int2 base = make_int2(0, 0);                 // units of the line, items
   for (int g0 = 0; g0 < G; g0 += THREADS) {
-    const int g = g0 + threadIdx.x;
+    const int g = g0 + tid;
     PrefixGroup e{0, 0, 0, 0, 0, 0, 0, 0};
     int2 mine = make_int2(0, 0);
     if (g < G) {
-      e.first = w.group_starts[g];
-      const int n = w.group_starts[g + 1] - e.first;
-      e.blocks = w.prefix_blocks[g];
+      e.first = starts[g];
+      const int n = starts[g + 1] - e.first;
+      e.blocks = blocks_of[g];
       if (n > 0 && e.blocks > 0 && e.blocks <= w.max_blocks) {
         e.units = (e.blocks + w.shape.pages - 1) / w.shape.pages;
         e.sub_tiles = (n * w.R + w.shape.tokens - 1) / w.shape.tokens * w.shape.chunks;
@@ -191,87 +260,85 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
         raise_error(w.err, MTP_ERR_LENGTH);
       }
     }
-    int2 incl = mine;
-#pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-      if (lane >= o) incl.x += x, incl.y += y;
+    int2 total;
+    const int2 before = scan(mine, &total);
+    e.line = base.x + before.x;
+    e.item = base.y + before.y;
+    base.x += total.x, base.y += total.y;
+    if (g < G) {
+      w.groups[g] = e;
+      if (G <= kCopy) s_line[g] = e.line;
     }
-    __syncthreads();                           // the last chunk's totals have been read
-    if (lane == kWarp - 1) s_sum[warp] = incl;
-    __syncthreads();
-    e.line = base.x + incl.x - mine.x;
-    e.item = base.y + incl.y - mine.y;
-    for (int i = 0; i < kWarps; ++i) {
-      const int2 t = s_sum[i];
-      if (i < warp) e.line += t.x, e.item += t.y;
-      base.x += t.x, base.y += t.y;
-    }
-    if (g < G) w.groups[g] = e;
   }
-  for (int b = threadIdx.x; b < w.B; b += THREADS) {
-    int lo = 0, hi = G, g = -1;                // the last group that begins at or before b, if b is in it
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      (w.group_starts[mid] <= b ? lo : hi) = mid;
-    }
-    if (G > 0 && w.group_starts[lo] <= b && b < w.group_starts[lo + 1]) g = lo;
-    const int blocks = g < 0 ? 0 : w.prefix_blocks[g];
-    const int first = own_first(blocks, w.ctx_lens[b], w.max_blocks, w.R);
-    w.first[b] = first;
-    w.group_of[b] = first > 0 ? g : -1;
-  }
+
   int own = 0;                                 // own pages of the requests so far
-  if (w.own != nullptr) {
-    __syncthreads();
-    for (int b0 = 0; b0 < w.B; b0 += THREADS) {
-      const int b = b0 + threadIdx.x;
-      int n = 0;
-      if (b < w.B && w.first[b] >= 0) n = (w.ctx_lens[b] + w.R + kBlock - 1) / kBlock - w.first[b];
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < kWarp; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+  for (int b0 = 0; b0 < w.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < w.B) {
+      const int ctx = b0 == 0 ? ctx0 : w.ctx_lens[b];
+      int g = -1;                              // the last group that begins at or before b, if b is in it
+      if (G > 0) {
+        const int lo = last_at_most(starts, G, b);
+        if (starts[lo] <= b && b < starts[lo + 1]) g = lo;
       }
-      __syncthreads();                         // the last chunk's totals have been read
-      if (lane == kWarp - 1) s_sum[warp].x = incl;
-      __syncthreads();
-      incl += own;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) incl += s_sum[i].x;
-        own += s_sum[i].x;
-      }
-      if (b < w.B) w.pages[b + 1] = incl;
+      const int first = own_first(g < 0 ? 0 : blocks_of[g], ctx, w.max_blocks, w.R);
+      w.first[b] = first;
+      w.group_of[b] = first > 0 ? g : -1;
+      if (first >= 0) n = (ctx + w.R + kBlock - 1) / kBlock - first;
     }
-    if (threadIdx.x == 0) w.pages[0] = 0;
+    if (w.own != nullptr) {
+      int2 total;
+      const int end = own + scan(make_int2(n, 0), &total).x + n;
+      own += total.x;
+      if (b < w.B) {
+        w.pages[b + 1] = end;
+        if (w.B <= kCopy) s_pages[b + 1] = end;
+      }
+    }
   }
-  // CTAs for the prefix and for the own pages: so that both should end at once.
+  if (tid == 0 && w.own != nullptr) w.pages[0] = s_pages[0] = 0;
   own *= w.own_heads;
+  // CTAs for the prefix and for the own pages: so that both should end at once.
   int ctas = w.ctas;
   if (own > 0 && base.x > 0) {
-    const float a = (float)base.x * w.unit_cost, z = (float)own * w.page_cost;
-    ctas = max(1, min(w.ctas - 1, (int)(w.ctas * a / (a + z) + 0.5f)));
+    const float a = (float)base.x * w.unit_cost, z = (float)own * w.page_cost + (float)w.B * w.own_heads * w.item_cost;
+    ctas = max(2, min(w.ctas - 2, 2 * (int)(w.ctas * a / (a + z) * 0.5f + 0.5f)));   // (pairs of CTAs do the same)
   }
-  auto shares = [](int total, int ctas) {
-    PrefixHead h{total, min(ctas, total), 1, 0};
-    if (h.ctas > 0) h.size = total / h.ctas, h.more = total - h.ctas * h.size;
-    return h;
-  };
-  const PrefixHead h = shares(base.x, ctas);
-  if (threadIdx.x == 0) {
-    *w.head = h;
-    if (w.own != nullptr) *w.own = shares(own, (w.ctas - h.ctas) * w.teams);
-  }
+  const PrefixHead h = make_shares(base.x, ctas);
+  if (tid == 0) *w.head = h;
   __syncthreads();                             // (writes to global memory too, for this CTA)
-  for (int c = threadIdx.x; c < h.ctas; c += THREADS) {
-    const int cut = prefix_cut(h, c);
-    int lo = 0, hi = G;                        // the last group whose line begins at or before the cut
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      (w.groups[mid].line <= cut ? lo : hi) = mid;
+  for (int c = tid; c < h.ctas; c += THREADS) {
+    PrefixStart s;
+    s.pos = prefix_cut(h, c);
+    s.end = prefix_cut(h, c + 1);
+    if (G <= kCopy) {
+      s.gi = last_at_most(s_line, G, s.pos);   // (the last group whose line begins there or before has items)
+    } else {
+      int lo = 0, hi = G;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (w.groups[mid].line <= s.pos ? lo : hi) = mid;
+      }
+      s.gi = lo;
     }
-    w.cta_group[c] = lo;
+    s.group = w.groups[s.gi];
+    s.pad = 0;
+    w.starts[c] = s;
+  }
+  if (w.own == nullptr) return;
+  const PrefixHead o = make_shares(own, (w.ctas - (h.ctas + 1) / 2 * 2) * w.teams);
+  if (tid == 0) *w.own = o;
+  const int32_t* pages = w.B <= kCopy ? s_pages : w.pages;
+  for (int c = tid; c < o.ctas; c += THREADS) {
+    OwnStart s;
+    s.pos = prefix_cut(o, c);
+    s.end = prefix_cut(o, c + 1);
+    s.b = last_at_most(pages, w.B, s.pos / w.own_heads);   // (the last request whose line begins there or before has pages)
+    s.before = pages[s.b];
+    s.pages = pages[s.b + 1] - s.before;
+    s.pad[0] = s.pad[1] = s.pad[2] = 0;
+    w.own_starts[c] = s;
   }
 }
 

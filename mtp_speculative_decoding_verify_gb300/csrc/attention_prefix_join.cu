@@ -22,8 +22,8 @@ __device__ __forceinline__ float ex2(float x) {
 // as they lie in the results, and SLICES x 16 dims, 4 of each a lane: all dims
 // where there are rows enough to fill the device, so that the finding of the
 // results is paid once a row; else a slice, for which more warps share the work.
-// Up to eight results are read as one batch. Bound by what it reads, out of L2
-// mostly, and by four dependent reads where that is little.
+// Several results are read as one batch. Bound by what it reads, out of L2
+// mostly, and by dependent reads where that is little.
 template <typename T>
 __device__ __forceinline__ void store4(T* to, float4 v);
 template <>
@@ -37,10 +37,9 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* to, float4 
 
 template <typename T, int D, int SLICES>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p, unsigned n_rows) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr bool kFp32 = sizeof(T) == 4;
   constexpr unsigned kUnits = D / 16 / SLICES;   // warps that share a row
-  constexpr int kMost = 8;
+  constexpr int kMost = SLICES == 1 ? 8 : 4;     // results read as one batch
   const unsigned lane = threadIdx.x % kWarp, unit = blockIdx.x * (kJoinThreads / kWarp) + threadIdx.x / kWarp;
   const unsigned idx = unit / kUnits * 8 + lane / 4;
   const int dim4 = unit % kUnits * SLICES * 4 + lane % 4;   // 4 dims from 4 dim4 + 16 x on
@@ -76,6 +75,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
   PrefixRow pre{nullptr, nullptr, 0, 0};
   if (gi >= 0) pre = prefix_row(v, head, load_group(v.groups + gi), p.R, p.group, b, kvh, r, D);
   const int n = pre.n + n1, rows0 = v.shape.rows;
+  // So far only what the append's launch left has been read, which was complete before the kernel ahead let this one
+  // begin (if it did before its own end). What follows reads that kernel's results.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   float m = -INFINITY, l = 0.0f;
   float4 o[SLICES];
@@ -119,18 +121,25 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
       ml[k].x = ml[k].x == -INFINITY ? 0.0f : ex2(ml[k].x - top);
       l += ml[k].y * ml[k].x;
     }
-#pragma unroll
-    for (int x = 0; x < SLICES; ++x) {
-      float4 w[kMost];
+    // (the next slice is on its way while one is added up)
+    float4 w[2][kMost];
+    auto read = [&](int x) {
 #pragma unroll
       for (int k = 0; k < kMost; ++k)
-        w[k] = from[k] != nullptr ? __ldcg(reinterpret_cast<const float4*>(from[k] + x * step[k])) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (from[k] != nullptr) w[x & 1][k] = __ldcg(reinterpret_cast<const float4*>(from[k] + x * step[k]));
+    };
+    read(0);
+#pragma unroll
+    for (int x = 0; x < SLICES; ++x) {
+      if (x + 1 < SLICES) read(x + 1);
       o[x].x *= a, o[x].y *= a, o[x].z *= a, o[x].w *= a;
 #pragma unroll
       for (int k = 0; k < kMost; ++k) {
-        if (k0 + k >= n) break;              // (0 x NaN of a part that is none)
-        const float c = ml[k].x;
-        o[x].x += w[k].x * c, o[x].y += w[k].y * c, o[x].z += w[k].z * c, o[x].w += w[k].w * c;
+        if (k0 + k < n) {                    // (0 x NaN of a part that is none)
+          const float c = ml[k].x;
+          const float4 y = w[x & 1][k];
+          o[x].x += y.x * c, o[x].y += y.y * c, o[x].z += y.z * c, o[x].w += y.w * c;
+        }
       }
     }
   }

@@ -12,8 +12,8 @@
 // parts is joined with the prefix's results, which have to be joined in any
 // case. Products are mma.sync m16n8k16: 16 rows need no more.
 //
-// One warp loads for all teams, a lane for each: it looks whether the team's next
-// stage is free, loads it, and has the block id after that on its way.
+// Four warps load, a lane for each team: it looks whether the team's next slot is
+// free, loads it, and has the block id after that on its way.
 //
 // Hidden slots (behind a row's own token, or off its path in a tree) occur in the
 // last stages only; those take the masked path of attention_window_mma.cu:
@@ -35,7 +35,7 @@ namespace own {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = 32;                 // of a stage
-constexpr int kWarps = 8;                 // consumers
+constexpr int kWarps = 8, kLoaders = 4;   // consumers, warps that load
 constexpr int kMaxStages = 8;             // of a team
 
 template <int D>
@@ -63,30 +63,37 @@ __device__ __forceinline__ bool take_out(uint32_t& w) {
 
 // A team's place in the line: pages pos .. end - 1, of which the next belong to
 // item (request b, head and row tile hr) with `pages` pages from unit u0 on.
+// What it needs of the request after b is on its way before it is asked for.
 struct OwnWalk {
   const PrefixParams& p;
-  int pos, end, b, hr, pages, u0, team, heads;   // (team: of all CTAs')
+  int pos, end, b, hr, pages, u0, heads, ctx, first;
+  int sum1, sum2, ctx1, first1;           // own pages of the requests up to b and b + 1; of request b + 1
   struct Seg {
     int b, hr, i0, i1;                    // pages i0 .. i1 - 1 of the request's own
+    int ctx, first;                       // its context, the first page of its own
   };
-  // The whole warp, or a lane by itself.
-  __device__ __forceinline__ OwnWalk(const PrefixParams& params, int t) : p(params), team(t) {
-    const PrefixHead head = load_head(p.view.own);
+  __device__ __forceinline__ void look_ahead() {
+    const int n = min(b + 1, p.B - 1);
+    sum2 = __ldcg(p.view.pages + n + 1);
+    ctx1 = __ldg(p.ctx_lens + n);
+    first1 = __ldcg(p.view.first + n);
+  }
+  __device__ __forceinline__ OwnWalk(const PrefixParams& params, int team) : p(params) {   // (team: of all CTAs')
     heads = p.Hkv * p.row_tiles;
-    pos = end = 0;
-    if (team >= head.ctas) return;
-    pos = prefix_cut(head, team);
-    end = prefix_cut(head, team + 1);
-    int lo = 0, hi = p.B;                 // the last request whose line begins at or before pos
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      (__ldcg(p.view.pages + mid) * heads <= pos ? lo : hi) = mid;
-    }
-    b = lo;
-    const int at = __ldcg(p.view.pages + b);
-    pages = __ldcg(p.view.pages + b + 1) - at;
-    hr = (pos - at * heads) / pages;
-    u0 = at * heads + hr * pages;
+    pos = end = b = hr = pages = u0 = ctx = first = sum1 = 0;
+    if (team >= __ldcg(&p.view.own->ctas)) return;
+    const OwnStart* at = p.view.own_starts + team;
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(at));
+    pages = __ldcg(&at->pages);
+    pos = v.x;
+    end = v.y;
+    b = v.z;
+    look_ahead();
+    ctx = __ldg(p.ctx_lens + b);
+    first = __ldcg(p.view.first + b);
+    sum1 = v.w + pages;
+    hr = (pos - v.w * heads) / pages;
+    u0 = v.w * heads + hr * pages;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (pos >= end) return false;
@@ -95,13 +102,19 @@ struct OwnWalk {
       if (++hr == heads) {
         hr = 0;
         ++b;
-        pages = __ldcg(p.view.pages + b + 1) - __ldcg(p.view.pages + b);
+        pages = sum2 - sum1;
+        sum1 = sum2;
+        ctx = ctx1;
+        first = first1;
+        look_ahead();
       }
     }
     s.b = b;
     s.hr = hr;
     s.i0 = pos - u0;
     s.i1 = min(pages, s.i0 + end - pos);
+    s.ctx = ctx;
+    s.first = first;
     pos += s.i1 - s.i0;
     return true;
   }
@@ -110,83 +123,86 @@ struct OwnWalk {
 // Stages of a page: 1 when the last verify token is in its first half.
 __device__ __forceinline__ int stages_of(int page, int ctx, int R) { return ctx + R - page * kBlock > kKeys ? 2 : 1; }
 
-// Barriers and flags of the teams' stages, behind the stages.
+// Barriers and flags of the teams' stages, behind the stages. K and V of a stage
+// are slots of their own (2 x and 2 x + 1), so that a K is replaced as soon as the
+// scores are there: of a team's 32 KB, 24 are on their way at any time.
 struct Control {
-  uint64_t *full, *empty;                 // [team][stage]
+  uint64_t *full, *empty;                 // [team][stage][2]
   volatile int* valid;                    // [team][stage] 0: the table named no block
   volatile int* abort;
 };
 
-// The warp that loads; cta: among those that do own pages.
+// The warps that load: a lane of warp w for each of the teams w, w + 4, .. (one warp
+// for all is the slowest part of the CTA); cta: among those that do own pages. A
+// lane must not wait for global memory, since the others wait with it: the next
+// segment and the next block id are read ahead.
 template <int D>
 __device__ __forceinline__ void producer(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PrefixParams& p, uint8_t* smem,
                                          const Control& c, int cta) {
   using T = Stage<D>;
-  const int lane = threadIdx.x % kWarp;
+  const int team = threadIdx.x % kWarp * kLoaders + threadIdx.x / kWarp;
   volatile int* abort = c.abort;
-  if (lane < p.teams) {
+  if (team < p.teams) {
     const uint64_t pol = sm100::l2_policy_evict_first();
-    OwnWalk walk(p, cta * p.teams + lane);
-    OwnWalk::Seg seg;
-    uint8_t* ring = smem + (size_t)lane * p.stages * T::kBytes;
-    uint64_t *my_full = c.full + lane * p.stages, *my_empty = c.empty + lane * p.stages;
-    volatile int* my_valid = c.valid + lane * p.stages;
-    int n = 0, slot = 0;
-    uint32_t phase = 1;                 // of `empty`: the first round needs no wait
-    bool more = walk.next(seg);
-    int i = 0, half = 0, halves = 0, id = 0, next_id = 0, page = 0, ctx = 0, first = 0, kvh = 0;
-    auto read_id = [&](int x) { return __ldg(p.block_table + (int64_t)seg.b * p.max_blocks + first + x); };
-    auto begin = [&]() {                // of a segment
-      ctx = __ldg(p.ctx_lens + seg.b);
-      first = __ldcg(p.view.first + seg.b);
+    OwnWalk walk(p, cta * p.teams + team);
+    OwnWalk::Seg seg, after;
+    const int slots = 2 * p.stages;
+    uint8_t* ring = smem + (size_t)team * p.stages * T::kBytes;
+    uint64_t *my_full = c.full + team * slots, *my_empty = c.empty + team * slots;
+    volatile int* my_valid = c.valid + team * p.stages;
+    int n = 0, slot = 0, i = 0, half = 0, halves = 0, id = 0, next_id = 0, kvh = 0;
+    uint32_t phase = 1;                   // of `empty`: the first round needs no wait
+    bool more = walk.next(seg), more_after = false;
+    auto read_id = [&](const OwnWalk::Seg& s, int x) { return __ldg(p.block_table + (int64_t)s.b * p.max_blocks + s.first + x); };
+    auto begin = [&]() {                  // of a segment, whose first id has been asked for
       kvh = seg.hr / p.row_tiles;
       i = seg.i0;
-      next_id = read_id(i);
+      more_after = walk.next(after);
     };
     auto begin_page = [&]() {
       id = next_id;
-      page = first + i;
       half = 0;
-      halves = stages_of(page, ctx, p.R);
-      if (i + 1 < seg.i1) next_id = read_id(i + 1);
+      halves = stages_of(seg.first + i, seg.ctx, p.R);
+      if (i + 1 < seg.i1) next_id = read_id(seg, i + 1);
+      else if (more_after) next_id = read_id(after, after.i0);
     };
     if (more) {
+      next_id = read_id(seg, seg.i0);
       begin();
       begin_page();
     }
     uint64_t t0 = sm100::globaltimer();
     for (uint32_t spin = 1; more; ++spin) {
       if (sm100::mbar_test_wait(&my_empty[slot], phase)) {
-        const bool good = id >= 0 && id < p.num_blocks;
-        my_valid[slot] = good;
+        const bool good = id >= 0 && id < p.num_blocks, is_v = slot & 1;
+        if (!is_v) my_valid[slot / 2] = good;
         if (good) {
-          uint8_t* to = ring + slot * T::kBytes;
-          sm100::mbar_arrive_expect_tx(&my_full[slot], T::kBytes);
+          uint8_t* to = ring + slot * T::kHalf;
+          sm100::mbar_arrive_expect_tx(&my_full[slot], T::kHalf);
+          const CUtensorMap* map = is_v ? &tm_v : &tm_k;
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) {
-            sm100::tma_load_4d(to + x * kKeys * 128, &tm_k, &my_full[slot], x * 64, kvh, half * kKeys, id, pol);
-            sm100::tma_load_4d(to + T::kHalf + x * kKeys * 128, &tm_v, &my_full[slot], x * 64, kvh, half * kKeys, id, pol);
-          }
+          for (int x = 0; x < D / 64; ++x)
+            sm100::tma_load_4d(to + x * kKeys * 128, map, &my_full[slot], x * 64, kvh, half * kKeys, id, pol);
         } else {
           raise_error(p.err, MTP_ERR_BLOCK_ID);
           sm100::mbar_arrive(&my_full[slot]);
         }
         ++n;
-        if (++slot == p.stages) {
+        if (++slot == slots) {
           slot = 0;
           phase ^= 1u;
         }
-        if (++half == halves) {
-          if (++i < seg.i1) {
-            begin_page();
-          } else if ((more = walk.next(seg))) {
-            begin();
-            begin_page();
+        if (is_v && ++half == halves) {
+          if (++i == seg.i1) {
+            more = more_after;
+            seg = after;
+            if (more) begin();
           }
+          if (more) begin_page();
         }
-        t0 = sm100::globaltimer();
-        spin = 1;
+        spin = 0;
       } else if ((spin & 255u) == 0) {
+        if (spin == 256) t0 = sm100::globaltimer();
         if (*abort) break;
         if (sm100::globaltimer() - t0 > sm100::kWaitTimeoutNs) {
           *abort = 1;
@@ -196,8 +212,8 @@ __device__ __forceinline__ void producer(const CUtensorMap& tm_k, const CUtensor
       }
     }
     // Every copy issued lands before the CTA may exit.
-    for (int x = max(0, n - p.stages); x < n; ++x)
-      sm100::mbar_wait_timeout(&my_full[x % p.stages], (uint32_t)((x / p.stages) & 1), sm100::kWaitTimeoutNs);
+    for (int x = max(0, n - slots); x < n; ++x)
+      sm100::mbar_wait_timeout(&my_full[x % slots], (uint32_t)((x / slots) & 1), sm100::kWaitTimeoutNs);
   }
   __syncwarp();
 }
@@ -212,7 +228,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
   const int team = cw / p.row_warps, rw = cw % p.row_warps;
   const int g = lane >> 2, t = lane & 3, mi = lane >> 3;
   uint8_t* ring = smem + (size_t)team * p.stages * T::kBytes;
-  uint64_t *my_full = c.full + team * p.stages, *my_empty = c.empty + team * p.stages;
+  uint64_t *my_full = c.full + team * 2 * p.stages, *my_empty = c.empty + team * 2 * p.stages;
   volatile int* my_valid = c.valid + team * p.stages;
   const float f = p.sm_scale * kLog2e;
   const int tile_rows = p.row_warps * 16;
@@ -222,9 +238,19 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
   uint32_t phase = 0;
   bool ok = true;
 
+  // Q of the item after this one, on its way into L1: a line of it a lane.
+  auto ask_for_q = [&]() {
+    if (walk.pos >= walk.end) return;
+    const bool same = walk.hr + 1 < walk.heads;
+    const int b = same ? walk.b : min(walk.b + 1, p.B - 1), hr = same ? walk.hr + 1 : 0, row = rw * 16 + lane / (D / 64);
+    const int r = min(hr % p.row_tiles * tile_rows + row, p.rows - 1);
+    const char* at = static_cast<const char*>(p.q) +
+                     (((int64_t)b * p.R + r / p.group) * p.Hq + hr / p.row_tiles * p.group + r % p.group) * (D * 2) + lane % (D / 64) * 128;
+    if (lane < 16 * (D / 64)) asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+  };
+
   while (ok && walk.next(seg)) {
-    const int b = seg.b, kvh = seg.hr / p.row_tiles;
-    const int ctx = __ldg(p.ctx_lens + b), first = __ldcg(p.view.first + b);
+    const int b = seg.b, kvh = seg.hr / p.row_tiles, ctx = seg.ctx, first = seg.first;
     const int r_lo = seg.hr % p.row_tiles * tile_rows + rw * 16 + g, r_hi = r_lo + 8;
     const int c_lo = min(r_lo, p.rows - 1), c_hi = min(r_hi, p.rows - 1);     // padding rows repeat the last row
     const int j_lo = c_lo / p.group, j_hi = c_hi / p.group;
@@ -242,6 +268,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
         qa[kk][3] = __ldg(hi + kk * 8 + 4 + t);
       }
     }
+    ask_for_q();
     const uint32_t path_lo = tree_path_mask(p.view.parents, b, p.R, j_lo, p.err);
     const uint32_t path_hi = tree_path_mask(p.view.parents, b, p.R, j_hi, p.err);
     float o[D / 8][4];
@@ -249,6 +276,11 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.0f, l_hi = 0.0f;   // maxima (log2 units), this lane's part of the sums
 
+    auto wait = [&](int slot) { return __all_sync(0xffffffffu, sm100::mbar_wait(&my_full[slot], phase, abort) ? 1 : 0) != 0; };
+    auto release = [&](int slot) {
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&my_empty[slot]);
+    };
     auto consume = [&](int slot0, auto masked_c) {   // keys at slots slot0 .. slot0 + 31
       constexpr bool kMasked = decltype(masked_c)::value;
       const uint32_t kbase = sm100::smem_u32(ring + stage * T::kBytes), vbase = kbase + T::kHalf;
@@ -265,6 +297,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
           mma::mma_bf16_16816(s[2 * np + 1], qa[kk], b2, b3);
         }
       }
+      release(2 * stage);
       bool some_lo = true, some_hi = true;           // the row sees a slot of the stage
       if constexpr (kMasked) {
         const int rel = slot0 - ctx;                 // (node 0, at slot ctx, is on every path)
@@ -325,6 +358,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
           o[i][3] *= k_hi;
         }
       }
+      if (!(ok = wait(2 * stage + 1))) return;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -372,15 +406,17 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
     for (int i = seg.i0; i < seg.i1 && ok; ++i) {
       const int page = first + i, halves = stages_of(page, ctx, p.R);
       for (int half = 0; half < halves; ++half) {
-        ok = __all_sync(0xffffffffu, sm100::mbar_wait(&my_full[stage], phase, abort) ? 1 : 0) != 0;
-        if (!ok) break;
+        if (!(ok = wait(2 * stage))) break;
         if (my_valid[stage]) {
           const int slot0 = page * kBlock + half * kKeys;
           if (slot0 + kKeys - 1 <= ctx) consume(slot0, std::false_type());
           else consume(slot0, std::true_type());
+          if (!ok) break;
+        } else {
+          if (!(ok = wait(2 * stage + 1))) break;
+          release(2 * stage);
         }
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&my_empty[stage]);
+        release(2 * stage + 1);
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
@@ -392,7 +428,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
     l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
     l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
     l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
-    const int64_t part = (int64_t)b * walk.heads + seg.hr + walk.team;
+    const int64_t part = (int64_t)b * walk.heads + seg.hr + cta * p.teams + team;
     const int at = rw * 16 + g;
     if (t == 0) {
       p.view.own_stats[part * tile_rows + at] = make_float2(m_lo, l_lo);

@@ -57,11 +57,11 @@ struct Smem {
   static constexpr int kQ = 0, kRing = 2 * kTile;
   static constexpr int kSlots = D == 128 ? 5 : 12;              // K and V tiles in turn
   static constexpr int kBar = kRing + kSlots * kTile;           // behind the stages of the own pages, too
-  static constexpr int kBars = 2 * kSlots + 2 + 6 + kInfo + 1;
+  static constexpr int kBars = 2 * kSlots + 2 + 8 + kInfo + 1;
   static constexpr int kMisc = kBar + kBars * 8;                // marks [kInfo], abort, TMEM base
   static constexpr int kOwnStages = kBar / own::Stage<D>::kBytes;
   static constexpr int kOwn = kMisc + kInfo * 4 + 8;            // own::Control
-  static constexpr int kBytes = kOwn + kOwnStages * 20 + 1024;
+  static constexpr int kBytes = kOwn + kOwnStages * 36 + 1024;
   static_assert(kBytes <= 232448, "227 KB of shared memory");
   static_assert(kOwn % 8 == 0, "barriers are 8 bytes");
 };
@@ -134,6 +134,19 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// sm100::mbar_wait that polls.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  if (sm100::mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = sm100::globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (sm100::mbar_test_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (sm100::globaltimer() - t0 > sm100::kWaitTimeoutNs) return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------- walk
 // This CTA's part of an item: tiles u0 .. u1 - 1 of keys.
 struct Seg {
@@ -145,16 +158,17 @@ struct Seg {
 
 struct Walk {
   const PrefixParams& p;
-  PrefixHead head;
   PrefixGroup g;
   int pos, end, gi, cta;
-  __device__ __forceinline__ explicit Walk(const PrefixParams& params) : p(params), cta(blockIdx.x) {
-    head = load_head(p.view.head);
-    pos = end = 0;
-    pos = prefix_cut(head, cta);
-    end = prefix_cut(head, cta + 1);
-    gi = __ldcg(p.view.cta_group + cta);
-    g = load_group(p.view.groups + gi);
+  __device__ __forceinline__ Walk(const PrefixParams& params, int prefix_cta) : p(params), cta(prefix_cta) {
+    pos = end = gi = 0;
+    if (cta >= __ldcg(&p.view.head->ctas)) return;
+    const PrefixStart* at = p.view.starts + cta;
+    g = load_group(&at->group);
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(&at->gi));
+    gi = v.x;
+    pos = v.y;
+    end = v.z;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (pos >= end) return false;
@@ -174,7 +188,7 @@ struct Walk {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_own_k,
                   const __grid_constant__ CUtensorMap tm_own_v, const PrefixParams p) {
@@ -187,15 +201,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = empty + kSlots;
   uint64_t* q_empty = q_full + 1;                                 // the last S of a segment is done
   uint64_t* s_full = q_empty + 1;                                 // [2] S, and the P V before it
-  uint64_t* p_full = s_full + 2;                                  // [2] P has replaced S (and O was read, if it was the last)
-  uint64_t* o_full = p_full + 2;                                  // [2] the segment's O
+  uint64_t* p_full = s_full + 2;                                  // [2][2] a half of P has replaced S (and the last segment's O was read)
+  uint64_t* o_full = p_full + 4;                                  // [2] the segment's O
   uint64_t* info_full = o_full + 2;                               // [kInfo]
   uint64_t* final_bar = info_full + kInfo;
   volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(smem + S::kMisc);   // bit h: page h of the tile is there
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMisc + kInfo * 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc + kInfo * 4 + 4);
 
-  const int n_own = p.teams * p.stages;
+  const int n_own = 2 * p.teams * p.stages;
   own::Control oc;
   oc.full = reinterpret_cast<uint64_t*>(smem + S::kOwn);
   oc.empty = oc.full + n_own;
@@ -219,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&s_full[i], 1);
-      sm100::mbar_init(&p_full[i], 4);
+      sm100::mbar_init(&p_full[2 * i], 4);
+      sm100::mbar_init(&p_full[2 * i + 1], 4);
       sm100::mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&info_full[i], 1);
@@ -244,14 +259,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   // reads what it writes.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int prefix_ctas = __ldcg(&p.view.head->ctas);
-  if ((int)blockIdx.x >= prefix_ctas) {
+  // Prefix or own pages: pairs of CTAs do the same, spread evenly over the grid.
+  // (A cluster of two has the two SMs of a TPC, which share a way to L2: a
+  // prefix CTA beside one that reads own pages took 177 us instead of 147, 256
+  // requests behind 8192 shared tokens.)
+  const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int own_pairs = pairs - (__ldcg(&p.view.head->ctas) + 1) / 2;
+  const int own_before = pair * own_pairs / pairs;
+  if ((pair + 1) * own_pairs / pairs > own_before) {
     // ----------------------------------------------------------- own pages
     // (56 + 2 x 224 = 3 x 168 registers a thread)
-    const int cta = blockIdx.x - prefix_ctas;
+    const int cta = own_before * 2 + blockIdx.x % 2;
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-      if (warp == 0) own::producer<D>(tm_own_k, tm_own_v, p, smem, oc, cta);
+      own::producer<D>(tm_own_k, tm_own_v, p, smem, oc, cta);
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
       own::consumer<D>(p, smem, oc, cta, warp - 4);
@@ -260,11 +281,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) sm100::tmem_dealloc(tmem, 512);
     return;
   }
-  Walk walk(p);
+  Walk walk(p, blockIdx.x - own_before * 2);
   Seg seg;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {   // the whole warp
     return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort) ? 1 : 0) != 0;
+  };
+  // The same without being suspended, for the hand-overs between MMA and softmax.
+  auto poll = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort) ? 1 : 0) != 0;
   };
 
   // Registers: 168 a thread at launch; the softmax warps take what the others
@@ -379,19 +404,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = i + 1 < tiles;
           ok = wait(&full[v_slot], (uint32_t)((n / kSlots) & 1));
           for (int x = 0; x < seg.nsub && ok; ++x) {
-            ok = wait(&p_full[x], p_phase[x]);
+            for (int h = 0; h < 2; ++h) {
+              ok = poll(&p_full[2 * x + h], p_phase[x]);
+              if (!ok) break;
+              sm100::tc_fence_after();
+              if (sm100::elect_one()) {
+#pragma unroll
+                for (int kk = h * 4; kk < h * 4 + 4; ++kk)
+                  mma_ts(tmem + kColO + x * 128, tmem + x * 128 + kk * 8, vd + (uint64_t)(v_slot * (S::kTile >> 4) + kk * 128),
+                         idesc_o, i > 0 || kk > 0 ? 1u : 0u);
+                if (h == 1) {
+                  if (x == last_x) sm100::tc_commit(&empty[v_slot]);
+                  if (!more) sm100::tc_commit(&o_full[x]);
+                }
+              }
+              __syncwarp();
+            }
             if (!ok) break;
             p_phase[x] ^= 1u;
-            sm100::tc_fence_after();
-            if (sm100::elect_one()) {
-  #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ts(tmem + kColO + x * 128, tmem + x * 128 + kk * 8, vd + (uint64_t)(v_slot * (S::kTile >> 4) + kk * 128), idesc_o,
-                       i > 0 || kk > 0 ? 1u : 0u);
-              if (x == last_x) sm100::tc_commit(&empty[v_slot]);
-              if (!more) sm100::tc_commit(&o_full[x]);
-            }
-            __syncwarp();
             if (more) {
               if (x == 0) {
                 ok = wait(&full[k_slot], (uint32_t)(((n + 1) / kSlots) & 1));
@@ -491,19 +521,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float a = s[c * 32 + 2 * i], b = s[c * 32 + 2 * i + 1];
+            float &a = s[c * 32 + 2 * i], &b = s[c * 32 + 2 * i + 1];
             fma2(a, b, f, base);
             a = ex2(a);
             b = ex2(b);
-            add2(l0, l1, a, b);
             w[i] = pack_bf16(a, b);
           }
           tmem_st_x16(ts + c * 16, w);
+          if (c % 2 == 1) {                    // a half of the keys: its P V may begin
+            tmem_st_wait();
+            sm100::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&p_full[2 * x + c / 2]);
+          }
         }
-        tmem_st_wait();
-        sm100::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&p_full[x]);
+        // (the sums while the products run)
+        float l2 = 0.0f, l3 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 128; i += 4) {
+          add2(l0, l1, s[i], s[i + 1]);
+          add2(l2, l3, s[i + 2], s[i + 3]);
+        }
+        l0 += l2;
+        l1 += l3;
       }
       if (!ok) break;
       ok = wait(&o_full[x], o_phase);
