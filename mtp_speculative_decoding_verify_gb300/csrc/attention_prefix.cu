@@ -12,13 +12,15 @@
 // is as tall as the group is large.
 //
 // Launches: the append, which also works out the shares of work in one more
-// CTA; the prefix; the own pages; the join of the two.
+// CTA; prefix and own pages (fp32 rows: one after the other); the join.
 #include <math.h>
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_prefix.h"
+#include "attention_prefix_own.cuh"
 #include "attention_window.h"
 
 namespace mtp {
@@ -68,159 +70,237 @@ __global__ void __launch_bounds__(kAppendThreads) prefix_append_kernel(const uin
   }
 }
 
-// --------------------------------------------------------------- fp32 prefix
-// A CTA walks its share of the line (attention_prefix.h): for each item 64 rows
-// of one KV head, page after page. A thread holds 4 rows x 4 keys of the
-// scores and 4 rows x D/16 dims of the output, so that a value from shared
-// memory serves four or more products; P takes K's place once the scores are
-// there, which lets two CTAs share an SM, one loading while the other computes.
-constexpr int kRows = 64, kThreads = 256;
-
-template <int D>
-struct SimtSmem {
-  static constexpr int kQ = 0, kK = kQ + kRows * (D + 4), kV = kK + kBlock * (D + 4), kFloats = kV + kBlock * D;
+// ---------------------------------------------------------------- fp32 rows
+// Prefix and own pages on FFMA, by the same kernel: a CTA walks its share of the
+// line (attention_prefix.h): for each item ROWS rows of one KV head, page after
+// page. A thread holds RPT rows x 4 keys of the scores and RPT rows x D/16 dims of
+// the output, so that a value from shared memory serves several products; P takes
+// K's place once the scores are there, and two (64 rows) or three (16 rows) CTAs
+// share an SM, one loading while the others compute. 64 rows where a KV head has
+// more than 32 over all requests, else 16 (2 rows of 8 KV heads behind 6400
+// tokens: 56 us with 64, a third of that with 16); own pages, of few rows, 16.
+// Own pages: a hidden slot's P is held as -1 and takes no part in the products (0
+// x NaN), and slots behind the last token are read as 0.
+template <int D, int ROWS>
+struct SimtCfg {
+  static constexpr int kThreads = ROWS == 64 ? 256 : 128, kRpt = ROWS * 16 / kThreads, kCtas = ROWS == 64 ? 2 : 3;
+  static constexpr int kQ = 0, kK = kQ + ROWS * (D + 4), kV = kK + kBlock * (D + 4), kFloats = kV + kBlock * D;
   static constexpr int kBytes = kFloats * (int)sizeof(float);
-  static_assert(kRows * (kBlock + 4) <= kBlock * (D + 4), "P fits in K's place");
+  static_assert(ROWS * (kBlock + 4) <= kBlock * (D + 4), "P fits in K's place");
+  static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "the CTAs fit an SM");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) prefix_simt_kernel(const PrefixParams p) {
-  using S = SimtSmem<D>;
+// An item of either line.
+struct SimtItem {
+  int table;                                   // the request whose table row names the pages
+  int page0, page1;                            // pages of it
+  int kvh, tile;                               // KV head; tile of rows of the group, or of the request
+  int ctx;                                     // own pages: the request's
+  int64_t part;
+};
+
+template <int D, int ROWS, bool kOwn>
+__global__ void __launch_bounds__((SimtCfg<D, ROWS>::kThreads), (SimtCfg<D, ROWS>::kCtas))
+    prefix_simt_kernel(const PrefixParams p, int behind_prefix) {
+  using S = SimtCfg<D, ROWS>;
+  constexpr int kThreads = S::kThreads, RPT = S::kRpt;
   constexpr int QS = D + 4, PS = kBlock + 4, E = D / 16;   // row strides; output dims of a thread
   extern __shared__ float smem[];
   float *qs = smem + S::kQ, *ks = smem + S::kK, *vs = smem + S::kV, *ps = ks;
   const PrefixView& v = p.view;
-  const PrefixHead head = load_head(v.head);
-  if ((int)blockIdx.x >= head.ctas) return;
-  const PrefixStart start = v.starts[blockIdx.x];
-  int pos = start.pos, gi = start.gi;
-  const int end = start.end;
-  PrefixGroup g = start.group;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const float f = p.sm_scale * kLog2e;
   const float *q = static_cast<const float*>(p.q), *kc = static_cast<const float*>(p.k_cache), *vc = static_cast<const float*>(p.v_cache);
   auto load4 = [](const float* at) { return __ldg(reinterpret_cast<const float4*>(at)); };
 
-  while (pos < end) {
-    while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(v.groups + ++gi);
-    const int k = (pos - g.line) / g.units, u0 = pos - g.line - k * g.units, u1 = min(g.units, u0 + end - pos);
-    const int kvh = k / g.tiles, tile = k % g.tiles;
-    const int item = g.item + k;
-    pos += u1 - u0;
+  // (Own pages: the append is complete when the prefix's kernel, which waited for it, lets this grid begin. What that
+  // kernel writes is not read here.)
+  if (!kOwn || !behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");   // (the next one reads what the append left before it waits)
+
+  // What the two lines have apart: the next item.
+  PrefixStart start{};
+  int pos = 0, end = 0;
+  if constexpr (!kOwn) {
+    if ((int)blockIdx.x < __ldcg(&v.head->ctas)) {
+      start.group = load_group(&v.starts[blockIdx.x].group);
+      start.gi = __ldcg(&v.starts[blockIdx.x].gi);
+      pos = __ldcg(&v.starts[blockIdx.x].pos);
+      end = __ldcg(&v.starts[blockIdx.x].end);
+    }
+  }
+  own::OwnWalk walk(p, kOwn ? (int)blockIdx.x : 0x7fffffff);
+  auto next = [&](SimtItem& it) -> bool {
+    if constexpr (kOwn) {
+      own::OwnWalk::Seg s;
+      if (!walk.next(s)) return false;
+      it = SimtItem{s.b, s.first + s.i0, s.first + s.i1, s.hr / p.row_tiles, s.hr % p.row_tiles, s.ctx,
+                    (int64_t)s.b * walk.heads + s.hr + blockIdx.x};
+    } else {
+      if (pos >= end) return false;
+      PrefixGroup& g = start.group;
+      while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(v.groups + ++start.gi);
+      const int k = (pos - g.line) / g.units, u0 = pos - g.line - k * g.units, u1 = min(g.units, u0 + end - pos);
+      it = SimtItem{g.first, u0, u1, k / g.tiles, k % g.tiles, 0, (int64_t)g.item + k + blockIdx.x};
+      pos += u1 - u0;
+    }
+    return true;
+  };
+
+  SimtItem it;
+  while (next(it)) {
     __syncthreads();                           // the last item's Q has been read
-    for (int x = tid; x < kRows * (D / 4); x += kThreads) {
+    for (int x = tid; x < ROWS * (D / 4); x += kThreads) {
       const int r = x / (D / 4), c = x % (D / 4) * 4;
-      const int token = v.shape.chunks > 1 ? tile / v.shape.chunks : tile * v.shape.tokens + r / p.group;
-      const int hh = v.shape.chunks > 1 ? tile % v.shape.chunks * kRows + r : r % p.group;
-      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // rows behind the group's compute on 0
-      if ((int64_t)g.first * p.R + token < (int64_t)p.B * p.R && hh < p.group && (v.shape.chunks > 1 || r < v.shape.tokens * p.group))
-        w = load4(q + (((int64_t)g.first * p.R + token) * p.Hq + kvh * p.group + hh) * D + c);
+      int64_t token;                           // (request, verify token)
+      int hh;
+      bool in;
+      if constexpr (kOwn) {
+        const int row = it.tile * ROWS + r;
+        token = (int64_t)it.table * p.R + row / p.group;
+        hh = row % p.group;
+        in = row < p.rows;
+      } else {
+        token = (int64_t)it.table * p.R + (v.shape.chunks > 1 ? it.tile / v.shape.chunks : it.tile * v.shape.tokens + r / p.group);
+        hh = v.shape.chunks > 1 ? it.tile % v.shape.chunks * ROWS + r : r % p.group;
+        in = token < (int64_t)p.B * p.R && hh < p.group && (v.shape.chunks > 1 || r < v.shape.tokens * p.group);
+      }
+      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // other rows compute on 0
+      if (in) w = load4(q + (token * p.Hq + it.kvh * p.group + hh) * D + c);
       *reinterpret_cast<float4*>(qs + r * QS + c) = w;
     }
-    float m[4], l[4], o[4][E];
+    uint32_t path[RPT];                        // own pages: the verify keys that the row sees
+    float m[RPT], l[RPT], o[RPT][E];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
+      path[i] = 0;
+      if constexpr (kOwn)
+        path[i] = tree_path_mask(v.parents, it.table, p.R, min(it.tile * ROWS + RPT * ty + i, p.rows - 1) / p.group, p.err);
       m[i] = -INFINITY;
       l[i] = 0.0f;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
     }
-    for (int u = u0; u < u1; ++u) {
-      const int blk = p.block_table[(int64_t)g.first * p.max_blocks + u];
+    for (int page = it.page0; page < it.page1; ++page) {
+      const int blk = __ldg(p.block_table + (int64_t)it.table * p.max_blocks + page);
       if (blk < 0 || blk >= p.num_blocks) {    // the same for every thread
         if (tid == 0) raise_error(p.err, MTP_ERR_BLOCK_ID);
         continue;
       }
+      const int keys = kOwn ? min(kBlock, it.ctx + p.R - page * kBlock) : kBlock;
+      const bool masked = kOwn && page * kBlock + kBlock - 1 > it.ctx;
       __syncthreads();                         // the last page's P and V have been read
+#pragma unroll 4
       for (int x = tid; x < kBlock * (D / 4); x += kThreads) {
         const int key = x / (D / 4), c = x % (D / 4) * 4;
-        const int64_t at = (((int64_t)blk * kBlock + key) * p.Hkv + kvh) * D + c;
-        *reinterpret_cast<float4*>(ks + key * QS + c) = load4(kc + at);
-        *reinterpret_cast<float4*>(vs + key * D + c) = load4(vc + at);
+        const int64_t at = (((int64_t)blk * kBlock + key) * p.Hkv + it.kvh) * D + c;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+        if (key < keys) a = __ldcg(reinterpret_cast<const float4*>(kc + at)), b = __ldcg(reinterpret_cast<const float4*>(vc + at));
+        *reinterpret_cast<float4*>(ks + key * QS + c) = a;
+        *reinterpret_cast<float4*>(vs + key * D + c) = b;
       }
       __syncthreads();
-      float s[4][4];                           // rows 4 ty + i, keys tx + 16 x
+      float s[RPT][4];                         // rows RPT ty + i, keys tx + 16 x
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+      for (int i = 0; i < RPT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
-        float4 a[4], b[4];
+        float4 a[RPT], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * QS + c);
+        for (int i = 0; i < RPT; ++i) a[i] = *reinterpret_cast<const float4*>(qs + (RPT * ty + i) * QS + c);
 #pragma unroll
         for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float4*>(ks + (tx + 16 * x) * QS + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RPT; ++i) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) s[i][x] += a[i].x * b[x].x + a[i].y * b[x].y + a[i].z * b[x].z + a[i].w * b[x].w;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RPT; ++i) {
+        unsigned hidden = 0;                   // of this thread's keys
+        if (kOwn && masked) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) hidden |= (tree_hidden(page * kBlock + tx + 16 * x, it.ctx, path[i]) ? 1u : 0u) << x;
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          s[i][x] *= f;
+          s[i][x] = (hidden >> x) & 1 ? -INFINITY : s[i][x] * f;
           top = fmaxf(top, s[i][x]);
         }
+        bool seen = hidden != 15u;             // the row sees a slot of the page
 #pragma unroll
-        for (int z = 8; z > 0; z >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-        const float n = fmaxf(fmaxf(m[i], top), kNoWeight);
-        const float a = m[i] == -INFINITY ? 0.0f : exp2f(m[i] - n);
+        for (int z = 8; z > 0; z >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+          if (kOwn) seen |= __shfl_xor_sync(0xffffffffu, (int)seen, z) != 0;
+        }
+        const float n = fmaxf(fmaxf(m[i], top), seen ? kNoWeight : -INFINITY);
+        const float base = n == -INFINITY ? 0.0f : n;
+        const float a = m[i] == -INFINITY ? 0.0f : exp2f(m[i] - base);
         m[i] = n;
         l[i] *= a;                             // (of this thread's keys; joined at the end)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          s[i][x] = exp2f(s[i][x] - n);
-          l[i] += s[i][x];
+          const float w = exp2f(s[i][x] - base);
+          s[i][x] = (hidden >> x) & 1 ? -1.0f : w;
+          if (!((hidden >> x) & 1)) l[i] += w;
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) o[i][e] *= a;
       }
       __syncthreads();                         // K has been read
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RPT; ++i) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ps[(4 * ty + i) * PS + tx + 16 * x] = s[i][x];
+        for (int x = 0; x < 4; ++x) ps[(RPT * ty + i) * PS + tx + 16 * x] = s[i][x];
       }
       __syncwarp();                            // (a row's P is written and read by one warp)
+      auto products = [&](auto masked_c) {
+        constexpr bool kMasked = decltype(masked_c)::value;
 #pragma unroll 2
-      for (int key = 0; key < kBlock; key += 4) {
-        float a[4][4];
+        for (int key = 0; key < kBlock; key += 4) {
+          float a[RPT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 w = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * PS + key);
-          a[i][0] = w.x, a[i][1] = w.y, a[i][2] = w.z, a[i][3] = w.w;
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          float b[E];                          // dims 4 tx + 64 (e / 4) + e % 4
-#pragma unroll
-          for (int e = 0; e < E; e += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(vs + (key + y) * D + 4 * tx + e * 16);
-            b[e] = w.x, b[e + 1] = w.y, b[e + 2] = w.z, b[e + 3] = w.w;
+          for (int i = 0; i < RPT; ++i) {
+            const float4 w = *reinterpret_cast<const float4*>(ps + (RPT * ty + i) * PS + key);
+            a[i][0] = w.x, a[i][1] = w.y, a[i][2] = w.z, a[i][3] = w.w;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int y = 0; y < 4; ++y) {
+            float b[E];                        // dims 4 tx + 64 (e / 4) + e % 4
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[i][e] += a[i][y] * b[e];
+            for (int e = 0; e < E; e += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(vs + (key + y) * D + 4 * tx + e * 16);
+              b[e] = w.x, b[e + 1] = w.y, b[e + 2] = w.z, b[e + 3] = w.w;
+            }
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+              if (kMasked && a[i][y] < 0.0f) continue;
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[i][e] += a[i][y] * b[e];
+            }
           }
         }
-      }
+      };
+      if (kOwn && masked) products(std::true_type());
+      else products(std::false_type());
     }
-    const int64_t part = (int64_t)item + blockIdx.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
 #pragma unroll
       for (int z = 8; z > 0; z >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], z);
-      const int r = 4 * ty + i;
-      if (tx == 0) v.stats[part * kRows + r] = make_float2(m[i], l[i]);
+      const int r = RPT * ty + i;
+      if (tx == 0) (kOwn ? v.own_stats : v.stats)[it.part * ROWS + r] = make_float2(m[i], l[i]);
 #pragma unroll
-      for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<float4*>(v.parts + part * kRows * D + ((tx + e * 4) * kRows + r) * 4) =
-            make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
+      for (int e = 0; e < E; e += 4) {
+        float* to = kOwn ? v.own_parts + (it.part * ROWS + r) * D + (tx + e * 4) * 4
+                         : v.parts + it.part * ROWS * D + ((tx + e * 4) * ROWS + r) * 4;
+        *reinterpret_cast<float4*>(to) = make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
+      }
     }
   }
+  if (kOwn && behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");   // whoever waits for this grid waits for that one too
 }
 
 // ----------------------------------------------------------- checks and plan
@@ -262,24 +342,11 @@ int check_prefix(const mtp_prefix_attn_args* a) {
 
 bool fp32_rows(const mtp_prefix_attn_args& a) { return a.dtype == MTP_F32; }
 
-// What window_simt_kernel (fp32 rows) has to know.
-mtp_window_attn_args own_args(const mtp_prefix_attn_args& a) {
-  mtp_window_attn_args w{};
-  w.B = a.B;
-  w.D = a.D;
-  w.Hq = a.Hq;
-  w.Hkv = a.Hkv;
-  w.d = a.d;
-  w.max_blocks = a.max_blocks;
-  w.dtype = a.dtype;
-  return w;
-}
-
 struct PrefixPlan {
   PrefixShape shape;
-  int ctas;                            // shares of the prefix
-  OwnPlan own;                         // bf16
-  int n_splits;                        // fp32
+  int ctas;                            // of the prefix (bf16: and the own pages)
+  int own_ctas;                        // fp32
+  OwnPlan own;
   // byte offsets in the workspace
   size_t head, groups, group_of, first, starts, own_starts, parts, stats, own_head, pages, own_parts, own_stats, bytes;
 };
@@ -288,8 +355,18 @@ struct PrefixPlan {
 bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   const int group = a.Hq / a.Hkv, R = a.D + 1, G = std::min(a.G, a.B);   // (empty groups have no items)
   const bool fp32 = fp32_rows(a);
-  pl->shape = fp32 ? prefix_shape(kRows, 1, 1, group) : prefix_shape(kPrefixTcRows, 2, 2, group);
-  pl->ctas = fp32 ? 2 * sm_count : std::max(4, sm_count / 2 * 2);   // bf16: pairs
+  if (fp32) {
+    const int rows = a.B * R * group > 32 ? 64 : 16;
+    pl->shape = prefix_shape(rows, 1, 1, group);
+    pl->ctas = (rows == 64 ? 2 : 3) * sm_count;
+    pl->own_ctas = 3 * sm_count;
+    pl->own = OwnPlan{(R * group + 15) / 16, 1, 1, 0};
+  } else {
+    pl->shape = prefix_shape(kPrefixTcRows, 2, 2, group);
+    pl->ctas = std::max(4, sm_count / 2 * 2);   // pairs
+    pl->own_ctas = 0;
+    pl->own = plan_prefix_own(a);
+  }
   const long long limit = 0x7fffffffll - 0x10000;
   // Items of all groups: the tiles of all rows, and the ones that each group leaves part of empty.
   const long long tiles = ((long long)a.B * R / pl->shape.tokens + G) * pl->shape.chunks;
@@ -309,33 +386,35 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   pl->starts = take((size_t)pl->ctas * sizeof(PrefixStart));
   pl->stats = take(results * sizeof(float2));
   pl->parts = take(results * a.d * sizeof(float));
-  if (fp32) {
-    pl->n_splits = window_simt_splits(own_args(a), sm_count);
-    const size_t n = (size_t)a.B * R * a.Hq * pl->n_splits;
-    pl->own_stats = take(n * sizeof(float));
-    pl->own_parts = take(n * a.d * sizeof(float));
-  } else {
-    pl->own = plan_prefix_own(a);
-    const long long own_items = (long long)a.B * a.Hkv * pl->own.row_tiles;
-    if (own_items * a.max_blocks > limit) return false;
-    const size_t n = ((size_t)own_items + (size_t)pl->ctas * pl->own.teams) * pl->own.row_warps * 16;
-    pl->own_head = take(sizeof(PrefixHead));
-    pl->pages = take(((size_t)a.B + 1) * sizeof(int32_t));
-    pl->own_starts = take((size_t)pl->ctas * pl->own.teams * sizeof(OwnStart));
-    pl->own_stats = take(n * sizeof(float2));
-    pl->own_parts = take(n * a.d * sizeof(float));
-  }
+  const long long own_items = (long long)a.B * a.Hkv * pl->own.row_tiles;
+  if (own_items * a.max_blocks > limit) return false;
+  const size_t own_shares = fp32 ? (size_t)pl->own_ctas : (size_t)pl->ctas * pl->own.teams;
+  const size_t n = ((size_t)own_items + own_shares) * pl->own.row_warps * 16;
+  pl->own_head = take(sizeof(PrefixHead));
+  pl->pages = take(((size_t)a.B + 1) * sizeof(int32_t));
+  pl->own_starts = take(own_shares * sizeof(OwnStart));
+  pl->own_stats = take(n * sizeof(float2));
+  pl->own_parts = take(n * a.d * sizeof(float));
   pl->bytes = at;
   return true;
 }
 
-template <int D>
-cudaError_t launch_prefix_simt(const PrefixParams& p, int ctas, cudaStream_t s) {
-  const int smem = SimtSmem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int D, int ROWS, bool kOwn>
+cudaError_t launch_simt(const PrefixParams& p, int ctas, int behind_prefix, cudaStream_t s) {
+  using S = SimtCfg<D, ROWS>;
+  const auto kernel = prefix_simt_kernel<D, ROWS, kOwn>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  prefix_simt_kernel<D><<<ctas, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind_append(kernel, (unsigned)ctas, S::kThreads, S::kBytes, s, p, behind_prefix);
+}
+
+template <int D>
+cudaError_t launch_fp32(const PrefixParams& p, const PrefixPlan& pl, bool groups, cudaStream_t s) {
+  if (groups) {
+    const cudaError_t e = pl.shape.rows == 64 ? launch_simt<D, 64, false>(p, pl.ctas, 0, s) : launch_simt<D, 16, false>(p, pl.ctas, 0, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_simt<D, 16, true>(p, pl.own_ctas, groups, s);
 }
 
 }  // namespace
@@ -420,49 +499,26 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   p.view.stats = reinterpret_cast<float2*>(ws + pl.stats);
   p.view.parents = a->parents;
   p.view.shape = pl.shape;
-  WindowParams w{};
-  if (fp32) {
-    w.q = a->q;
-    w.k_cache = a->k_cache;
-    w.v_cache = a->v_cache;
-    w.block_table = a->block_table;
-    w.ctx_lens = a->ctx_lens;
-    w.err = err;
-    w.B = p.B;
-    w.R = p.R;
-    w.Hq = p.Hq;
-    w.Hkv = p.Hkv;
-    w.group = p.group;
-    w.rows = p.rows;
-    w.max_blocks = p.max_blocks;
-    w.num_blocks = p.num_blocks;
-    w.sm_scale = p.sm_scale;
-    w.n_splits = p.n_splits = pl.n_splits;
-    w.part_o = reinterpret_cast<float*>(ws + pl.own_parts);
-    w.part_lse = reinterpret_cast<float*>(ws + pl.own_stats);
-    p.part_o = w.part_o;
-    p.part_lse = w.part_lse;
-    w.own_first = ps.first;
-    w.parents = a->parents;
-  } else {
-    ps.own = reinterpret_cast<PrefixHead*>(ws + pl.own_head);
-    ps.pages = i32(pl.pages);
-    ps.own_starts = reinterpret_cast<OwnStart*>(ws + pl.own_starts);
-    ps.own_heads = p.Hkv * pl.own.row_tiles;
-    ps.teams = pl.own.teams;
+  ps.own = reinterpret_cast<PrefixHead*>(ws + pl.own_head);
+  ps.pages = i32(pl.pages);
+  ps.own_starts = reinterpret_cast<OwnStart*>(ws + pl.own_starts);
+  ps.own_heads = p.Hkv * pl.own.row_tiles;
+  ps.own_ctas = pl.own_ctas;
+  ps.teams = pl.own.teams;
+  if (!fp32) {
     ps.unit_cost = a->d == 128 ? 1800 : 1400;
     ps.page_cost = 2600 / pl.own.teams;
     ps.item_cost = 1800 / pl.own.teams;
-    p.row_tiles = pl.own.row_tiles;
-    p.row_warps = pl.own.row_warps;
-    p.teams = pl.own.teams;
-    p.stages = pl.own.stages;
-    p.view.own = ps.own;
-    p.view.pages = ps.pages;
-    p.view.own_starts = ps.own_starts;
-    p.view.own_parts = reinterpret_cast<float*>(ws + pl.own_parts);
-    p.view.own_stats = reinterpret_cast<float2*>(ws + pl.own_stats);
   }
+  p.row_tiles = pl.own.row_tiles;
+  p.row_warps = pl.own.row_warps;
+  p.teams = pl.own.teams;
+  p.stages = pl.own.stages;
+  p.view.own = ps.own;
+  p.view.pages = ps.pages;
+  p.view.own_starts = ps.own_starts;
+  p.view.own_parts = reinterpret_cast<float*>(ws + pl.own_parts);
+  p.view.own_stats = reinterpret_cast<float2*>(ws + pl.own_stats);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto record = [&](void* ev) { return ev ? cudaEventRecord(static_cast<cudaEvent_t>(ev), s) : cudaSuccess; };
   const int vecs = a->Hkv * a->d * (fp32 ? 4 : 2) / 16;
@@ -471,13 +527,8 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return set_cuda_error(e, "kv append launch");
   if ((e = record(a->timing_events[0])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
-  if (fp32) {
-    if (a->G > 0 && (e = a->d == 128 ? launch_prefix_simt<128>(p, pl.ctas, s) : launch_prefix_simt<64>(p, pl.ctas, s)) != cudaSuccess)
-      return set_cuda_error(e, "prefix attention launch");
-    e = launch_window_simt_own(w, a->d, s);
-  } else {
-    e = launch_prefix_tc(*a, p, pl.ctas, s);
-  }
+  if (fp32) e = a->d == 128 ? launch_fp32<128>(p, pl, a->G > 0, s) : launch_fp32<64>(p, pl, a->G > 0, s);
+  else e = launch_prefix_tc(*a, p, pl.ctas, s);
   if (e != cudaSuccess) return set_cuda_error(e, "attention launch");
   e = launch_prefix_join(*a, p, s);
   if (e != cudaSuccess) return set_cuda_error(e, "attention join launch");

@@ -70,8 +70,7 @@ struct PrefixView {
   float2* stats;                    // [partial result][sub][rows]: maximum (log2 units), sum of p
   const int32_t* parents;           // [B, R] or NULL
   PrefixShape shape;
-  // bf16 rows: the own pages
-  const PrefixHead* own;
+  const PrefixHead* own;            // the own pages
   const int32_t* pages;             // [B+1] own pages of the requests before each
   const OwnStart* own_starts;       // [teams]
   float* own_parts;                 // [partial result][rows of a tile][d]
@@ -87,10 +86,8 @@ struct PrefixParams {
   int B, R, Hq, Hkv, group, rows;   // rows = query rows per (request, KV head)
   int max_blocks, num_blocks;
   float sm_scale;
-  int n_splits;                     // fp32: own partial results of a row, as window_simt_kernel leaves them
-  const float *part_o, *part_lse;
-  // bf16: the kernel of the own pages
-  int row_tiles, row_warps, teams, stages;   // tiles of 16 row_warps rows; teams of a CTA, stages of a team
+  int row_tiles, row_warps;         // own pages: tiles of 16 row_warps rows of a request
+  int teams, stages;                // .. bf16: teams of a CTA, stages of a team
   PrefixView view;
 };
 
@@ -111,10 +108,11 @@ struct PrefixSchedule {
   const int32_t *group_starts, *prefix_blocks, *ctx_lens;
   int G, B, R, Hkv, max_blocks, ctas;
   PrefixShape shape;
-  PrefixHead* own;                  // nullptr: no line of own pages
+  PrefixHead* own;
   int32_t* pages;
   OwnStart* own_starts;
-  int own_heads, teams;             // items of a request; teams of a CTA that does own pages
+  int own_heads, own_ctas;          // items of a request; CTAs that do own pages, 0: some of `ctas`
+  int teams;                        // of such a CTA
   int unit_cost, page_cost, item_cost;   // of a CTA, for a unit of the prefix, a page and an item of the requests' own (ns)
   unsigned* err;
 };
@@ -287,21 +285,19 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
       w.group_of[b] = first > 0 ? g : -1;
       if (first >= 0) n = (ctx + w.R + kBlock - 1) / kBlock - first;
     }
-    if (w.own != nullptr) {
-      int2 total;
-      const int end = own + scan(make_int2(n, 0), &total).x + n;
-      own += total.x;
-      if (b < w.B) {
-        w.pages[b + 1] = end;
-        if (w.B <= kCopy) s_pages[b + 1] = end;
-      }
+    int2 total;
+    const int end = own + scan(make_int2(n, 0), &total).x + n;
+    own += total.x;
+    if (b < w.B) {
+      w.pages[b + 1] = end;
+      if (w.B <= kCopy) s_pages[b + 1] = end;
     }
   }
-  if (tid == 0 && w.own != nullptr) w.pages[0] = s_pages[0] = 0;
+  if (tid == 0) w.pages[0] = s_pages[0] = 0;
   own *= w.own_heads;
   // CTAs for the prefix and for the own pages: so that both should end at once.
   int ctas = w.ctas;
-  if (own > 0 && base.x > 0) {
+  if (w.own_ctas == 0 && own > 0 && base.x > 0) {
     const float a = (float)base.x * w.unit_cost, z = (float)own * w.page_cost + (float)w.B * w.own_heads * w.item_cost;
     ctas = max(2, min(w.ctas - 2, 2 * (int)(w.ctas * a / (a + z) * 0.5f + 0.5f)));   // (pairs of CTAs do the same)
   }
@@ -326,8 +322,7 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
     s.pad = 0;
     w.starts[c] = s;
   }
-  if (w.own == nullptr) return;
-  const PrefixHead o = make_shares(own, (w.ctas - (h.ctas + 1) / 2 * 2) * w.teams);
+  const PrefixHead o = make_shares(own, (w.own_ctas > 0 ? w.own_ctas : w.ctas - (h.ctas + 1) / 2 * 2) * w.teams);
   if (tid == 0) *w.own = o;
   const int32_t* pages = w.B <= kCopy ? s_pages : w.pages;
   for (int c = tid; c < o.ctas; c += THREADS) {

@@ -37,7 +37,6 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* to, float4 
 
 template <typename T, int D, int SLICES>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p, unsigned n_rows) {
-  constexpr bool kFp32 = sizeof(T) == 4;
   constexpr unsigned kUnits = D / 16 / SLICES;   // warps that share a row
   constexpr int kMost = SLICES == 1 ? 8 : 4;     // results read as one batch
   const unsigned lane = threadIdx.x % kWarp, unit = blockIdx.x * (kJoinThreads / kWarp) + threadIdx.x / kWarp;
@@ -50,27 +49,15 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
   const PrefixHead head = load_head(v.head);
   const unsigned j = r / (unsigned)p.group, h = kvh * p.group + (r - j * p.group);
   const int64_t row = ((int64_t)b * p.R + j) * p.Hq + h;
-  // The own results: n1 of them.
-  const float *o1, *m1;                      // (fp32 rows: o / l and log2 of the weight)
-  int n1;
-  int64_t step1;                             // rows from one to the next
-  if constexpr (kFp32) {
-    n1 = p.n_splits;
-    step1 = 1;
-    o1 = p.part_o + row * n1 * D;
-    m1 = p.part_lse + row * n1;
-  } else {
-    const PrefixHead own = load_head(v.own);
-    const int before = __ldcg(v.pages + b), pages = __ldcg(v.pages + b + 1) - before;
-    const unsigned tile_rows = p.row_warps * 16, tile = r / tile_rows;
-    const int heads = p.Hkv * p.row_tiles, hr = kvh * p.row_tiles + tile, u0 = before * heads + hr * pages;
-    const int c0 = prefix_cta_of(own, u0), c1 = prefix_cta_of(own, u0 + pages - 1);
-    const int64_t at = ((int64_t)b * heads + hr + c0) * tile_rows + (r - tile * tile_rows);
-    n1 = c1 - c0 + 1;
-    step1 = tile_rows;
-    o1 = v.own_parts + at * D;
-    m1 = reinterpret_cast<const float*>(v.own_stats + at);
-  }
+  // The own results: n1 of them, step1 rows from one to the next.
+  const unsigned step1 = p.row_warps * 16, tile = r / step1;
+  const PrefixHead own = load_head(v.own);
+  const int before = __ldcg(v.pages + b), pages = __ldcg(v.pages + b + 1) - before;
+  const int heads = p.Hkv * p.row_tiles, hr = kvh * p.row_tiles + tile, u0 = before * heads + hr * pages;
+  const int c0 = prefix_cta_of(own, u0), n1 = prefix_cta_of(own, u0 + pages - 1) - c0 + 1;
+  const int64_t at1 = ((int64_t)b * heads + hr + c0) * step1 + (r - tile * step1);
+  const float* o1 = v.own_parts + at1 * D;
+  const float2* m1 = v.own_stats + at1;
   if (first < 0) return;                     // flagged; its rows stay as they were
   PrefixRow pre{nullptr, nullptr, 0, 0};
   if (gi >= 0) pre = prefix_row(v, head, load_group(v.groups + gi), p.R, p.group, b, kvh, r, D);
@@ -99,13 +86,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
         from[k] = pre.o + at * D + dim4 * rows0 * 4;
         step[k] = rows0 * 16;                // from 4 dims to those 16 on
       } else if (i < n) {
-        const int64_t at = (i - pre.n) * step1;
-        if constexpr (kFp32) {
-          const float w = __ldcg(m1 + at);
-          ml[k] = make_float2(w, w == -INFINITY || w == kNoWeight ? 0.0f : 1.0f);
-        } else {
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(m1) + at);
-        }
+        const int64_t at = (int64_t)(i - pre.n) * step1;
+        ml[k] = __ldcg(m1 + at);
         from[k] = o1 + at * D + dim4 * 4;
         step[k] = 16;
       }

@@ -89,9 +89,7 @@ constexpr int simt_smem_bytes() {
   return (kBlock * (D + 4) + kBlock * D + kSimtRows * D) * (int)sizeof(float);
 }
 
-// kOwn: the pages behind a group's prefix (mtp_verify_attention_prefix), a
-// partial result each split.
-template <typename T, typename KV, int D, bool kOwn>
+template <typename T, typename KV, int D>
 __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const WindowParams p) {
   constexpr int E = D / kWarp;
   extern __shared__ float smem[];
@@ -107,17 +105,11 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
     if (threadIdx.x == 0 && split == 0) raise_error(p.err, MTP_ERR_LENGTH);
     return;
   }
-  PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
-  if constexpr (kOwn) {
-    const int first = p.own_first[b];
-    if (first < 0) return;                     // flagged by the append
-    span = own_span(ctx, p.R, first);
-  }
+  const PageSpan span = page_span(ctx, p.R, p.window, p.sinks);
   const int i0 = (int)((int64_t)span.n * split / p.n_splits), i1 = (int)((int64_t)span.n * (split + 1) / p.n_splits);
 
   int64_t orow[2];
   int pos[2];
-  uint32_t path[2];                            // kOwn: the verify keys that the row sees
   bool live[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
@@ -125,7 +117,6 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
     live[x] = r < p.rows;
     const int rc = min(r, p.rows - 1);
     pos[x] = ctx + rc / p.group;
-    path[x] = kOwn ? tree_path_mask(p.parents, b, p.R, rc / p.group, p.err) : 0;
     orow[x] = ((int64_t)b * p.R + rc / p.group) * p.Hq + kvh * p.group + rc % p.group;
     for (int e = lane; e < D; e += kWarp)
       qs[(warp + x * kSimtWarps) * D + e] = Num<T>::to_f(static_cast<const T*>(p.q)[orow[x] * D + e]);
@@ -189,8 +180,7 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
       unsigned see[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int slot = page * kBlock + lane + y * kWarp;
-        const bool vis = kOwn ? !tree_hidden(slot, ctx, path[x]) : slot_visible(slot, pos[x], p.window, p.sinks);
+        const bool vis = slot_visible(page * kBlock + lane + y * kWarp, pos[x], p.window, p.sinks);
         see[y] = __ballot_sync(0xffffffffu, vis);
         s[y] = vis ? s[y] * p.sm_scale : -INFINITY;
       }
@@ -227,8 +217,8 @@ __global__ void __launch_bounds__(kSimtWarps* kWarp) window_simt_kernel(const Wi
   for (int x = 0; x < 2; ++x) {
     if (!live[x]) continue;
     // no weight: nothing seen (bad blocks only), or -inf only
-    const float inv = l[x] != 0.0f ? 1.0f / l[x] : m[x] == -INFINITY || kOwn || p.n_splits > 1 ? 0.0f : NAN;
-    if (!kOwn && p.n_splits == 1) {
+    const float inv = l[x] != 0.0f ? 1.0f / l[x] : m[x] == -INFINITY || p.n_splits > 1 ? 0.0f : NAN;
+    if (p.n_splits == 1) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         static_cast<T*>(p.out)[orow[x] * D + lane * E + e] = Num<T>::from_f(o[x][e] * inv);
@@ -273,13 +263,13 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowParams p,
   for (int e = 0; e < E; ++e) static_cast<T*>(p.out)[row * D + lane * E + e] = Num<T>::from_f(o[e] * inv);
 }
 
-template <typename T, typename KV, int D, bool kOwn = false>
+template <typename T, typename KV, int D>
 cudaError_t run_simt(const WindowParams& p, cudaStream_t s, int* launches) {
   const int smem = simt_smem_bytes<D>();
-  cudaError_t e = cudaFuncSetAttribute(window_simt_kernel<T, KV, D, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(window_simt_kernel<T, KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.B * p.Hkv, p.n_splits, (p.rows + kSimtRows - 1) / kSimtRows);
-  window_simt_kernel<T, KV, D, kOwn><<<grid, kSimtWarps * kWarp, smem, s>>>(p);
+  window_simt_kernel<T, KV, D><<<grid, kSimtWarps * kWarp, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches = 1;
   return cudaSuccess;
@@ -352,8 +342,9 @@ int check_window(const mtp_window_attn_args* a, bool kv8) {
 // The tensor cores take bf16 rows, the SIMT kernel fp32 ones.
 bool uses_mma(const mtp_window_attn_args& a) { return a.dtype == MTP_BF16; }
 
-// Ranges that the SIMT kernel cuts a request's pages into.
-int simt_splits(const mtp_window_attn_args& a, int sm_count) {
+WindowPlan plan_window(const mtp_window_attn_args& a, bool kv8, int sm_count) {
+  if (uses_mma(a)) return kv8 ? plan_kv8_tc(a, sm_count) : plan_window_mma(a, sm_count);
+  WindowPlan p{};
   const int rows = a.Hq / a.Hkv * (a.D + 1);
   const long long ctas = (long long)a.B * a.Hkv * ((rows + kSimtRows - 1) / kSimtRows);
   // Two CTAs an SM where the batch alone has fewer, and at least four pages a
@@ -361,13 +352,7 @@ int simt_splits(const mtp_window_attn_args& a, int sm_count) {
   const long long pages = a.window == 0 ? a.max_blocks
                                         : std::min<long long>(a.max_blocks, ((long long)a.window + a.sinks) / kBlock + 3);
   const long long want = std::max<long long>(1, (2ll * sm_count + ctas - 1) / std::max(ctas, 1ll));
-  return (int)std::max<long long>(1, std::min({want, pages / 4, 64ll}));
-}
-
-WindowPlan plan_window(const mtp_window_attn_args& a, bool kv8, int sm_count) {
-  if (uses_mma(a)) return kv8 ? plan_kv8_tc(a, sm_count) : plan_window_mma(a, sm_count);
-  WindowPlan p{};
-  p.n_splits = simt_splits(a, sm_count);
+  p.n_splits = (int)std::max<long long>(1, std::min({want, pages / 4, 64ll}));
   p.ws_bytes = 256;
   if (p.n_splits > 1) {
     const size_t n = (size_t)a.B * (a.D + 1) * a.Hq * p.n_splits;
@@ -496,13 +481,6 @@ int attend(const mtp_window_attn_args* a, bool kv8, void* stream) {
 }
 
 }  // namespace
-
-int window_simt_splits(const mtp_window_attn_args& a, int sm_count) { return simt_splits(a, sm_count); }
-
-cudaError_t launch_window_simt_own(const WindowParams& p, int d, cudaStream_t s) {
-  int launches = 0;
-  return d == 128 ? run_simt<float, float, 128, true>(p, s, &launches) : run_simt<float, float, 64, true>(p, s, &launches);
-}
 }  // namespace mtp
 
 extern "C" {

@@ -64,7 +64,6 @@ struct WindowParams {
   int max_blocks, num_blocks, window, sinks, n_splits;
   int row_tiles, row_warps, key_parts, stages;
   float sm_scale;
-  const int32_t *own_first, *parents;   // mtp_verify_attention_prefix: [B] first page of a request's own, -1: none; trees
 };
 
 struct WindowSchedule {
@@ -102,9 +101,6 @@ inline size_t plan_schedule(WindowPlan* pl, int B, int Hkv) {
 
 WindowPlan plan_window_mma(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_window_mma(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
-int window_simt_splits(const mtp_window_attn_args& a, int sm_count);
-// mtp_verify_attention_prefix, fp32 rows: partial results over the own pages, n_splits of a row.
-cudaError_t launch_window_simt_own(const WindowParams& p, int d, cudaStream_t s);
 WindowPlan plan_kv8_tc(const mtp_window_attn_args& a, int sm_count);
 cudaError_t launch_kv8_tc(const mtp_window_attn_args& a, const WindowPlan& pl, const WindowParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(const mtp_kv8_append_args& a, int uniform, const WindowSchedule& sch, unsigned* err,

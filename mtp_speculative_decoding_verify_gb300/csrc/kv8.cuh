@@ -90,11 +90,6 @@ __host__ __device__ __forceinline__ PageSpan page_span(int ctx, int R, int windo
   return s;
 }
 
-// A request's own pages behind a prefix of `first` pages.
-__host__ __device__ __forceinline__ PageSpan own_span(int ctx, int R, int first) {
-  return PageSpan{0, first, (ctx + R + kBlock - 1) / kBlock - first};
-}
-
 // ----------------------------------------------------------- shares of work
 struct Cuts {
   int total;       // pages of the line
