@@ -630,11 +630,15 @@ def kv_block_assign(block_table, seq_lens, starts, free_list, free_count, slot_m
     _on(index, stream, lambda s: _scratch(a, workspace, index, n, s, lambda: L.kv_block_assign(ctypes.byref(a), s)))
 
 
-def _refuse_rows(t, name, index, dtype, shape):
-    """Say what is wrong with a [T, Hkv, d] tensor whose tokens may lie apart."""
-    if t.is_cuda and t.get_device() == index and t.dtype is dtype and t.shape == shape:
+def _token_rows(t, name, index, dtype, shape):
+    """Elements from a token to the next of a [T, Hkv, d] tensor whose tokens may lie apart."""
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, index, dtype, shape)
+    apart, head, one = t.stride()
+    T, Hkv, d = shape
+    if (one != 1 and d > 1) or (head != d and Hkv > 1):
         raise ValueError("%s: a token's values must be contiguous" % name)
-    _refuse(t, name, index, dtype, shape)
+    return apart if T > 1 else Hkv * d
 
 
 def mtp_kv_append(k_new, v_new, slot_map, k_cache, v_cache, *, stream=None):
@@ -643,26 +647,25 @@ def mtp_kv_append(k_new, v_new, slot_map, k_cache, v_cache, *, stream=None):
     k_new, v_new [T, Hkv, d] (float32 or bfloat16; views with tokens apart will do, a token's values contiguous), caches
     [blocks, 64, Hkv, d] of the same type. Absorbed MLA: k_new [T, 576] or [T, 1, 576], v_new = v_cache = None.
     """
-    if k_new.dim() == 2 and v_new is None:
+    if v_new is None and k_new.dim() == 2:
         k_new = k_new.unsqueeze(1)
-    T, Hkv, d = k_new.shape
+    T, Hkv, d = shape = k_new.shape
     nb, dt, index = k_cache.shape[0], k_new.dtype, _cuda_index(k_new, "k_new")
-    rows = [(k_new, "k_new", d)]
     _check_all(index, ((slot_map, "slot_map", torch.int64, (T,)), (k_cache, "k_cache", dt, (nb, BLOCK_SIZE, Hkv, d))))
-    d_v, v_stride = 0, 0
-    if v_new is not None or v_cache is not None:
-        if v_new is None or v_cache is None:
+    k_stride = _token_rows(k_new, "k_new", index, dt, shape)
+    v = v_at = None
+    d_v = v_stride = 0
+    if v_new is not None:
+        if v_cache is None:
             raise ValueError("v_new and v_cache go together")
-        d_v, v_stride = v_new.shape[-1], v_new.stride(0) if T > 1 else Hkv * v_new.shape[-1]
-        rows.append((v_new, "v_new", d_v))
+        d_v = v_new.shape[-1]
+        v_stride = _token_rows(v_new, "v_new", index, dt, (T, Hkv, d_v))
         _check_all(index, ((v_cache, "v_cache", dt, (nb, BLOCK_SIZE, Hkv, d_v)),))
-    for t, name, n in rows:
-        if t.get_device() != index or t.dtype is not dt or t.shape != (T, Hkv, n) or \
-                (t.numel() and ((t.stride(2) != 1 and n > 1) or (t.stride(1) != n and Hkv > 1))):
-            _refuse_rows(t, name, index, dt, (T, Hkv, n))
-    a = KvAppendArgs(k_new.data_ptr(), None if v_new is None else v_new.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
-                     None if v_cache is None else v_cache.data_ptr(), k_new.stride(0) if T > 1 else Hkv * d, v_stride, T,
-                     Hkv, d, d_v, BLOCK_SIZE, nb, int(v_new is None), _dtype_code(k_new))
+        v, v_at = v_new.data_ptr(), v_cache.data_ptr()
+    elif v_cache is not None:
+        raise ValueError("v_new and v_cache go together")
+    a = KvAppendArgs(k_new.data_ptr(), v, slot_map.data_ptr(), k_cache.data_ptr(), v_at, k_stride, v_stride, T, Hkv, d, d_v,
+                     BLOCK_SIZE, nb, v is None, _dtype_code(k_new))
     _on(index, stream, lambda s: lib().mtp_kv_append(ctypes.byref(a), s))
 
 

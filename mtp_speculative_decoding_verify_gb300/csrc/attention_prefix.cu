@@ -507,8 +507,8 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   ps.teams = pl.own.teams;
   if (!fp32) {
     ps.unit_cost = a->d == 128 ? 1800 : 1400;
-    ps.page_cost = 2600 / pl.own.teams;
-    ps.item_cost = 1800 / pl.own.teams;
+    ps.page_cost = 2700 / pl.own.teams;
+    ps.item_cost = 1900 / pl.own.teams;
   }
   p.row_tiles = pl.own.row_tiles;
   p.row_warps = pl.own.row_warps;
