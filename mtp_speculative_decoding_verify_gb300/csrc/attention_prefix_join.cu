@@ -10,6 +10,11 @@ namespace mtp {
 namespace {
 
 constexpr int kJoinThreads = 128;
+// 32 dims of a row a warp from 1024 rows on (2496 rows of trees: 21.0 us with 16,
+// 19.5 us so; 256 rows with 17 results: 15.0 us with 16, and 17.2 with those in
+// batches of 8), all from 8192 on (12288 rows: 54.9 with 32, 52.4 so; 7808 rows:
+// 105.5 with all, 102.1 with 32); calls in a graph.
+constexpr unsigned kSomeRows = 1024, kManyRows = 8192;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -21,9 +26,9 @@ __device__ __forceinline__ float ex2(float x) {
 // results, the prefix's and then its own. A warp takes 8 rows of one KV head,
 // as they lie in the results, and SLICES x 16 dims, 4 of each a lane: all dims
 // where there are rows enough to fill the device, so that the finding of the
-// results is paid once a row; else a slice, for which more warps share the work.
-// Several results are read as one batch. Bound by what it reads, out of L2
-// mostly, and by dependent reads where that is little.
+// results is paid once a row; else fewer, for which more warps share the work and
+// more results are read as one batch. Bound by what it reads, out of L2 mostly
+// (32768 rows, 59 MB: 16 us), and by one round of reads where that is little.
 template <typename T>
 __device__ __forceinline__ void store4(T* to, float4 v);
 template <>
@@ -38,7 +43,7 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* to, float4 
 template <typename T, int D, int SLICES>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p, unsigned n_rows) {
   constexpr unsigned kUnits = D / 16 / SLICES;   // warps that share a row
-  constexpr int kMost = SLICES == 1 ? 8 : 4;     // results read as one batch
+  constexpr int kMost = SLICES == 1 ? 20 : SLICES == 2 ? 8 : 4;   // results read as one batch
   const unsigned lane = threadIdx.x % kWarp, unit = blockIdx.x * (kJoinThreads / kWarp) + threadIdx.x / kWarp;
   const unsigned idx = unit / kUnits * 8 + lane / 4;
   const int dim4 = unit % kUnits * SLICES * 4 + lane % 4;   // 4 dims from 4 dim4 + 16 x on
@@ -92,6 +97,14 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
         step[k] = 16;
       }
     }
+    // (the first slice with the maxima, each next one while one is added up)
+    float4 w[2][kMost];
+    auto read = [&](int x) {
+#pragma unroll
+      for (int k = 0; k < kMost; ++k)
+        if (from[k] != nullptr) w[x & 1][k] = __ldcg(reinterpret_cast<const float4*>(from[k] + x * step[k]));
+    };
+    read(0);
     float top = m;
 #pragma unroll
     for (int k = 0; k < kMost; ++k) top = fmaxf(top, ml[k].x);
@@ -103,14 +116,6 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
       ml[k].x = ml[k].x == -INFINITY ? 0.0f : ex2(ml[k].x - top);
       l += ml[k].y * ml[k].x;
     }
-    // (the next slice is on its way while one is added up)
-    float4 w[2][kMost];
-    auto read = [&](int x) {
-#pragma unroll
-      for (int k = 0; k < kMost; ++k)
-        if (from[k] != nullptr) w[x & 1][k] = __ldcg(reinterpret_cast<const float4*>(from[k] + x * step[k]));
-    };
-    read(0);
 #pragma unroll
     for (int x = 0; x < SLICES; ++x) {
       if (x + 1 < SLICES) read(x + 1);
@@ -135,8 +140,12 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
 template <typename T, int D>
 cudaError_t launch_join(const PrefixParams& p, cudaStream_t s) {
   const unsigned rows = (unsigned)p.B * p.Hkv * p.rows, groups = (rows + 7) / 8, warps = kJoinThreads / kWarp;
-  if (rows >= 8192) return launch_behind_append(prefix_join_kernel<T, D, D / 16>, (groups + warps - 1) / warps, kJoinThreads, 0, s, p, rows);
-  return launch_behind_append(prefix_join_kernel<T, D, 1>, (groups * (D / 16) + warps - 1) / warps, kJoinThreads, 0, s, p, rows);
+  auto launch = [&](auto kernel, unsigned slices) {
+    return launch_behind_append(kernel, (groups * (D / 16 / slices) + warps - 1) / warps, kJoinThreads, 0, s, p, rows);
+  };
+  if (rows >= kManyRows) return launch(prefix_join_kernel<T, D, D / 16>, D / 16);
+  if (rows >= kSomeRows) return launch(prefix_join_kernel<T, D, 2>, 2);
+  return launch(prefix_join_kernel<T, D, 1>, 1);
 }
 
 }  // namespace

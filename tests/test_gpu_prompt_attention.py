@@ -167,6 +167,22 @@ def test_many_rows_and_long_prefixes(t, P, n):
     c.check(g)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("n_groups", [0, 3, 1300])
+def test_many_requests_and_many_groups(t, n_groups):
+    """More of both than the schedule keeps in shared memory."""
+    rng = np.random.default_rng(n_groups)
+    if n_groups == 1300:
+        groups = [(int(rng.integers(0, 3)), [int(x) for x in rng.integers(0, 40, int(rng.integers(0, 3)))]) for _ in range(1300)]
+    else:
+        groups = [(2 + i, [int(x) for x in rng.integers(0, 150, 400)]) for i in range(n_groups)]
+    c = Case(t, 1, 2, 1, 64, groups=groups, before=[5, 70], after=[int(x) for x in rng.integers(0, 150, 30 if n_groups else 1400)])
+    g = c.to_gpu()
+    c.call(g)
+    mv.sync_status()
+    c.check(g)
+
+
 def test_the_same_as_verify_attention():
     """Over the same tables, up to the order of the sums; and the others' entries of the prefix are not looked at. (In
     slots behind the last token mtp_verify_attention wants finite values.)"""
