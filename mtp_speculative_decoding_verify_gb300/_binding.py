@@ -6,6 +6,7 @@ of the verify path runs in the library's CUDA kernels. There is no CPU
 fallback: if the library is missing, loading it raises.
 """
 import ctypes
+import operator
 import os
 
 import torch
@@ -607,6 +608,51 @@ def kv_window_release(block_table, seq_lens, free_list, free_count, *, window, s
     _on(index, stream, lambda s: _scratch(a, workspace, index, n, s, lambda: L.kv_window_release(ctypes.byref(a), s)))
 
 
+_SHAPE, _DTYPE, _DATA = operator.attrgetter("shape"), operator.attrgetter("dtype"), torch.Tensor.data_ptr
+_DEVICE, _DENSE = torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
+def _pointers(index, names, tensors, dtypes, shapes):
+    """The tensors' addresses, if all are on that device, of those types and shapes, and contiguous. (In a few passes that
+    run in C: such a call's checks are a third of its time on the host.)"""
+    if tuple(map(_SHAPE, tensors)) != shapes or tuple(map(_DTYPE, tensors)) != dtypes or not all(map(_DENSE, tensors)) or \
+            tuple(map(_DEVICE, tensors)) != (index,) * len(tensors):
+        _check_all(index, zip(tensors, names, dtypes, shapes))
+    return map(_DATA, tensors)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _run(index, stream, workspace, a, size, call):
+    """call(a, stream handle) on device `index`, with the caller's workspace or size(a) bytes that torch holds for the
+    stream (as _on and _scratch, without the steps that the usual call does not need)."""
+    ref = ctypes.byref(a)
+
+    def bytes_needed():
+        n = size(ref)
+        if n == 0:
+            _check(MTP_INVALID_ARG)
+        return n
+
+    if workspace is not None or stream is not None or _current_device() != index:
+        _on(index, stream, lambda s: _scratch(a, workspace, index, bytes_needed() if workspace is None else 0, s, lambda: call(ref, s)))
+        return
+    s, n = _raw_stream(index), bytes_needed()
+    a.workspace_bytes = n
+    a.workspace = p = _raw_alloc(n, s)
+    try:
+        rc = call(ref, s)
+    finally:
+        _raw_free(p)
+    if rc != MTP_OK:
+        _check(rc)
+
+
+_ASSIGN_NAMES = ("block_table", "seq_lens", "starts", "free_list", "free_count", "slot_map", "taken")
+_ASSIGN_TYPES = (torch.int32, torch.int32, torch.int32, torch.int32, torch.int32, torch.int64, torch.int32)
+
+
 def kv_block_assign(block_table, seq_lens, starts, free_list, free_count, slot_map, taken, *, workspace=None, stream=None):
     """Take blocks for the tokens about to be appended from the free list, and map those tokens to cache slots.
 
@@ -617,17 +663,12 @@ def kv_block_assign(block_table, seq_lens, starts, free_list, free_count, slot_m
     was, and later requests do not overtake it).
     """
     B, max_blocks = block_table.shape
-    index, i32 = _cuda_index(block_table, "block_table"), torch.int32
-    n_free, T = free_list.numel(), slot_map.numel()
-    _check_all(index, ((block_table, "block_table", i32, (B, max_blocks)), (seq_lens, "seq_lens", i32, (B,)),
-                       (starts, "starts", i32, (B + 1,)), (free_list, "free_list", i32, (n_free,)),
-                       (free_count, "free_count", i32, (1,)), (slot_map, "slot_map", torch.int64, (T,)),
-                       (taken, "taken", i32, (B,))))
+    n_free, T, index = free_list.numel(), slot_map.numel(), _cuda_index(block_table, "block_table")
+    ptrs = _pointers(index, _ASSIGN_NAMES, (block_table, seq_lens, starts, free_list, free_count, slot_map, taken), _ASSIGN_TYPES,
+                     ((B, max_blocks), (B,), (B + 1,), (n_free,), (1,), (T,), (B,)))
     L = lib()
-    a = BlockAssignArgs(block_table.data_ptr(), seq_lens.data_ptr(), starts.data_ptr(), free_list.data_ptr(),
-                        free_count.data_ptr(), slot_map.data_ptr(), taken.data_ptr(), B, T, BLOCK_SIZE, max_blocks, n_free)
-    n = max(256, L.mtp_block_assign_workspace_size(B, T)) if workspace is None else 0
-    _on(index, stream, lambda s: _scratch(a, workspace, index, n, s, lambda: L.kv_block_assign(ctypes.byref(a), s)))
+    a = BlockAssignArgs(*ptrs, B, T, BLOCK_SIZE, max_blocks, n_free)
+    _run(index, stream, workspace, a, lambda _: max(256, L.mtp_block_assign_workspace_size(B, T)), L.kv_block_assign)
 
 
 def _token_rows(t, name, index, dtype, shape):
@@ -651,22 +692,28 @@ def mtp_kv_append(k_new, v_new, slot_map, k_cache, v_cache, *, stream=None):
         k_new = k_new.unsqueeze(1)
     T, Hkv, d = shape = k_new.shape
     nb, dt, index = k_cache.shape[0], k_new.dtype, _cuda_index(k_new, "k_new")
-    _check_all(index, ((slot_map, "slot_map", torch.int64, (T,)), (k_cache, "k_cache", dt, (nb, BLOCK_SIZE, Hkv, d))))
     k_stride = _token_rows(k_new, "k_new", index, dt, shape)
-    v = v_at = None
-    d_v = v_stride = 0
-    if v_new is not None:
-        if v_cache is None:
-            raise ValueError("v_new and v_cache go together")
+    if v_new is not None and v_cache is not None:
         d_v = v_new.shape[-1]
         v_stride = _token_rows(v_new, "v_new", index, dt, (T, Hkv, d_v))
-        _check_all(index, ((v_cache, "v_cache", dt, (nb, BLOCK_SIZE, Hkv, d_v)),))
-        v, v_at = v_new.data_ptr(), v_cache.data_ptr()
-    elif v_cache is not None:
+        slots, k_at, v_at = _pointers(index, ("slot_map", "k_cache", "v_cache"), (slot_map, k_cache, v_cache), (torch.int64, dt, dt),
+                                      ((T,), (nb, BLOCK_SIZE, Hkv, d), (nb, BLOCK_SIZE, Hkv, d_v)))
+        v = v_new.data_ptr()
+    elif v_new is None and v_cache is None:
+        v = v_at = None
+        d_v = v_stride = 0
+        slots, k_at = _pointers(index, ("slot_map", "k_cache"), (slot_map, k_cache), (torch.int64, dt), ((T,), (nb, BLOCK_SIZE, Hkv, d)))
+    else:
         raise ValueError("v_new and v_cache go together")
-    a = KvAppendArgs(k_new.data_ptr(), v, slot_map.data_ptr(), k_cache.data_ptr(), v_at, k_stride, v_stride, T, Hkv, d, d_v,
-                     BLOCK_SIZE, nb, v is None, _dtype_code(k_new))
-    _on(index, stream, lambda s: lib().mtp_kv_append(ctypes.byref(a), s))
+    a = KvAppendArgs(k_new.data_ptr(), v, slots, k_at, v_at, k_stride, v_stride, T, Hkv, d, d_v, BLOCK_SIZE, nb, v is None,
+                     _dtype_code(k_new))
+    if stream is None and _current_device() == index:
+        _check(lib().mtp_kv_append(ctypes.byref(a), _raw_stream(index)))
+    else:
+        _on(index, stream, lambda s: lib().mtp_kv_append(ctypes.byref(a), s))
+
+
+_PREFIX_NAMES = ("q", "k_new", "v_new", "k_cache", "v_cache", "block_table", "ctx_lens", "group_starts", "prefix_blocks", "out")
 
 
 def mtp_verify_attention_prefix(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, group_starts, prefix_blocks, out,
@@ -678,36 +725,21 @@ def mtp_verify_attention_prefix(q, k_new, v_new, k_cache, v_cache, block_table, 
     group_starts[g] .. group_starts[g+1]-1; prefix_blocks [G] int32: full blocks that they share, those of the row of the
     group's first request. parents [B, R] int32 (tree drafts) or None (chains).
     """
-    B, R, Hq, d = q.shape
+    B, R, Hq, d = rows = q.shape
     nb, _, Hkv, _ = k_cache.shape
     max_blocks, G = block_table.shape[-1], prefix_blocks.shape[0]
-    dt, i32 = q.dtype, torch.int32
-    index = _cuda_index(q, "q")
+    dt, i32, index = q.dtype, torch.int32, _cuda_index(q, "q")
     new, cache = (B, R, Hkv, d), (nb, BLOCK_SIZE, Hkv, d)
-    _check_all(index, ((q, "q", dt, (B, R, Hq, d)), (k_new, "k_new", dt, new), (v_new, "v_new", dt, new),
-                       (k_cache, "k_cache", dt, cache), (v_cache, "v_cache", dt, cache),
-                       (block_table, "block_table", i32, (B, max_blocks)), (ctx_lens, "ctx_lens", i32, (B,)),
-                       (group_starts, "group_starts", i32, (G + 1,)), (prefix_blocks, "prefix_blocks", i32, (G,)),
-                       (out, "out", dt, (B, R, Hq, d))))
+    ptrs = _pointers(index, _PREFIX_NAMES,
+                     (q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, group_starts, prefix_blocks, out),
+                     (dt, dt, dt, dt, dt, i32, i32, i32, i32, dt),
+                     (rows, new, new, cache, cache, (B, max_blocks), (B,), (G + 1,), (G,), rows))
     if parents is not None:
-        _check_all(index, ((parents, "parents", i32, (B, R)),))
+        parents, = _pointers(index, ("parents",), (parents,), (i32,), ((B, R),))
     L = lib()
-    a = PrefixAttnArgs(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                       block_table.data_ptr(), ctx_lens.data_ptr(), group_starts.data_ptr(), prefix_blocks.data_ptr(),
-                       out.data_ptr(), B, R - 1, G, Hq, Hkv, d, BLOCK_SIZE, max_blocks, nb,
-                       d ** -0.5 if sm_scale is None else float(sm_scale), _dtype_code(q),
-                       None if parents is None else parents.data_ptr())
-    ref = ctypes.byref(a)
-
-    def call(s):
-        n = 0
-        if workspace is None:
-            n = L.mtp_attention_prefix_workspace_size(ref)
-            if n == 0:
-                _check(MTP_INVALID_ARG)
-        return _scratch(a, workspace, index, n, s, lambda: L.mtp_verify_attention_prefix(ref, s))
-
-    _on(index, stream, call)
+    a = PrefixAttnArgs(*ptrs, B, R - 1, G, Hq, Hkv, d, BLOCK_SIZE, max_blocks, nb, d ** -0.5 if sm_scale is None else float(sm_scale),
+                       _dtype_code(q), parents)
+    _run(index, stream, workspace, a, L.mtp_attention_prefix_workspace_size, L.mtp_verify_attention_prefix)
 
 
 def sync_status(stream=None):

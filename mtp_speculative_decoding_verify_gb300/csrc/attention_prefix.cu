@@ -76,9 +76,13 @@ __global__ void __launch_bounds__(kAppendThreads) prefix_append_kernel(const uin
 // page. A thread holds RPT rows x 4 keys of the scores and RPT rows x D/16 dims of
 // the output, so that a value from shared memory serves several products; P takes
 // K's place once the scores are there, and two (64 rows) or three (16 rows) CTAs
-// share an SM, one loading while the others compute. 64 rows where a KV head has
-// more than 32 over all requests, else 16 (2 rows of 8 KV heads behind 6400
-// tokens: 56 us with 64, a third of that with 16); own pages, of few rows, 16.
+// share an SM, one loading while the others compute. Own pages, of few rows,
+// take 16 a tile; the prefix 64 where a KV head has more than 32 over all
+// requests, else 16, and then one launch does both lines (2 rows of 8 KV heads
+// behind 6400 tokens: 84 us with 64, 47 us with 16; 4 requests of 4 rows behind
+// 1024: 15.4 us in two launches, 13.6 in one). FFMA and shared memory bound it: 32
+// TFLOP/s (512 rows a KV head behind 2048 tokens), 1.5 TB/s over own pages of 16
+// rows.
 // Own pages: a hidden slot's P is held as -1 and takes no part in the products (0
 // x NaN), and slots behind the last token are read as 0.
 template <int D, int ROWS>
@@ -99,9 +103,9 @@ struct SimtItem {
   int64_t part;
 };
 
+// The CTAs of one line; cta: among them.
 template <int D, int ROWS, bool kOwn>
-__global__ void __launch_bounds__((SimtCfg<D, ROWS>::kThreads), (SimtCfg<D, ROWS>::kCtas))
-    prefix_simt_kernel(const PrefixParams p, int behind_prefix) {
+__device__ __forceinline__ void simt_line(const PrefixParams& p, int cta) {
   using S = SimtCfg<D, ROWS>;
   constexpr int kThreads = S::kThreads, RPT = S::kRpt;
   constexpr int QS = D + 4, PS = kBlock + 4, E = D / 16;   // row strides; output dims of a thread
@@ -113,35 +117,30 @@ __global__ void __launch_bounds__((SimtCfg<D, ROWS>::kThreads), (SimtCfg<D, ROWS
   const float *q = static_cast<const float*>(p.q), *kc = static_cast<const float*>(p.k_cache), *vc = static_cast<const float*>(p.v_cache);
   auto load4 = [](const float* at) { return __ldg(reinterpret_cast<const float4*>(at)); };
 
-  // (Own pages: the append is complete when the prefix's kernel, which waited for it, lets this grid begin. What that
-  // kernel writes is not read here.)
-  if (!kOwn || !behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");   // (the next one reads what the append left before it waits)
-
   // What the two lines have apart: the next item.
   PrefixStart start{};
   int pos = 0, end = 0;
   if constexpr (!kOwn) {
-    if ((int)blockIdx.x < __ldcg(&v.head->ctas)) {
-      start.group = load_group(&v.starts[blockIdx.x].group);
-      start.gi = __ldcg(&v.starts[blockIdx.x].gi);
-      pos = __ldcg(&v.starts[blockIdx.x].pos);
-      end = __ldcg(&v.starts[blockIdx.x].end);
+    if (cta < __ldcg(&v.head->ctas)) {
+      start.group = load_group(&v.starts[cta].group);
+      start.gi = __ldcg(&v.starts[cta].gi);
+      pos = __ldcg(&v.starts[cta].pos);
+      end = __ldcg(&v.starts[cta].end);
     }
   }
-  own::OwnWalk walk(p, kOwn ? (int)blockIdx.x : 0x7fffffff);
+  own::OwnWalk walk(p, kOwn ? cta : 0x7fffffff);
   auto next = [&](SimtItem& it) -> bool {
     if constexpr (kOwn) {
       own::OwnWalk::Seg s;
       if (!walk.next(s)) return false;
       it = SimtItem{s.b, s.first + s.i0, s.first + s.i1, s.hr / p.row_tiles, s.hr % p.row_tiles, s.ctx,
-                    (int64_t)s.b * walk.heads + s.hr + blockIdx.x};
+                    (int64_t)s.b * walk.heads + s.hr + cta};
     } else {
       if (pos >= end) return false;
       PrefixGroup& g = start.group;
       while (g.units == 0 || pos >= g.line + g.tiles * p.Hkv * g.units) g = load_group(v.groups + ++start.gi);
       const int k = (pos - g.line) / g.units, u0 = pos - g.line - k * g.units, u1 = min(g.units, u0 + end - pos);
-      it = SimtItem{g.first, u0, u1, k / g.tiles, k % g.tiles, 0, (int64_t)g.item + k + blockIdx.x};
+      it = SimtItem{g.first, u0, u1, k / g.tiles, k % g.tiles, 0, (int64_t)g.item + k + cta};
       pos += u1 - u0;
     }
     return true;
@@ -300,7 +299,28 @@ __global__ void __launch_bounds__((SimtCfg<D, ROWS>::kThreads), (SimtCfg<D, ROWS
       }
     }
   }
-  if (kOwn && behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");   // whoever waits for this grid waits for that one too
+}
+
+// kPrefix, kOwn or kBoth, some CTAs each (as many as the schedule gives the prefix).
+enum SimtLines { kPrefix, kOwn, kBoth };
+
+template <int D, int ROWS, SimtLines kLines>
+__global__ void __launch_bounds__((SimtCfg<D, ROWS>::kThreads), (SimtCfg<D, ROWS>::kCtas))
+    prefix_simt_kernel(const PrefixParams p, int behind_prefix) {
+  // (Own pages: the append is complete when the prefix's kernel, which waited for it, lets this grid begin. What that
+  // kernel writes is not read here.)
+  if (!behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");   // (the next one reads what the append left before it waits)
+  if constexpr (kLines == kPrefix) {
+    simt_line<D, ROWS, false>(p, blockIdx.x);
+  } else if constexpr (kLines == kOwn) {
+    simt_line<D, ROWS, true>(p, blockIdx.x);
+  } else {
+    const int ctas = (__ldcg(&p.view.head->ctas) + 1) / 2 * 2;
+    if ((int)blockIdx.x < ctas) simt_line<D, ROWS, false>(p, blockIdx.x);
+    else simt_line<D, ROWS, true>(p, blockIdx.x - ctas);
+  }
+  if (behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");   // whoever waits for this grid waits for that one too
 }
 
 // ----------------------------------------------------------- checks and plan
@@ -358,8 +378,8 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   if (fp32) {
     const int rows = a.B * R * group > 32 ? 64 : 16;
     pl->shape = prefix_shape(rows, 1, 1, group);
-    pl->ctas = (rows == 64 ? 2 : 3) * sm_count;
-    pl->own_ctas = 3 * sm_count;
+    pl->ctas = rows == 64 ? 2 * sm_count : std::max(4, 3 * sm_count / 2 * 2);
+    pl->own_ctas = rows == 64 ? 3 * sm_count : 0;
     pl->own = OwnPlan{(R * group + 15) / 16, 1, 1, 0};
   } else {
     pl->shape = prefix_shape(kPrefixTcRows, 2, 2, group);
@@ -388,7 +408,7 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   pl->parts = take(results * a.d * sizeof(float));
   const long long own_items = (long long)a.B * a.Hkv * pl->own.row_tiles;
   if (own_items * a.max_blocks > limit) return false;
-  const size_t own_shares = fp32 ? (size_t)pl->own_ctas : (size_t)pl->ctas * pl->own.teams;
+  const size_t own_shares = (size_t)(pl->own_ctas > 0 ? pl->own_ctas : pl->ctas) * pl->own.teams;
   const size_t n = ((size_t)own_items + own_shares) * pl->own.row_warps * 16;
   pl->own_head = take(sizeof(PrefixHead));
   pl->pages = take(((size_t)a.B + 1) * sizeof(int32_t));
@@ -399,10 +419,10 @@ bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   return true;
 }
 
-template <int D, int ROWS, bool kOwn>
+template <int D, int ROWS, SimtLines kLines>
 cudaError_t launch_simt(const PrefixParams& p, int ctas, int behind_prefix, cudaStream_t s) {
   using S = SimtCfg<D, ROWS>;
-  const auto kernel = prefix_simt_kernel<D, ROWS, kOwn>;
+  const auto kernel = prefix_simt_kernel<D, ROWS, kLines>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
   return launch_behind_append(kernel, (unsigned)ctas, S::kThreads, S::kBytes, s, p, behind_prefix);
@@ -410,11 +430,12 @@ cudaError_t launch_simt(const PrefixParams& p, int ctas, int behind_prefix, cuda
 
 template <int D>
 cudaError_t launch_fp32(const PrefixParams& p, const PrefixPlan& pl, bool groups, cudaStream_t s) {
+  if (pl.own_ctas == 0) return launch_simt<D, 16, kBoth>(p, pl.ctas, 0, s);
   if (groups) {
-    const cudaError_t e = pl.shape.rows == 64 ? launch_simt<D, 64, false>(p, pl.ctas, 0, s) : launch_simt<D, 16, false>(p, pl.ctas, 0, s);
+    const cudaError_t e = launch_simt<D, 64, kPrefix>(p, pl.ctas, 0, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_simt<D, 16, true>(p, pl.own_ctas, groups, s);
+  return launch_simt<D, 16, kOwn>(p, pl.own_ctas, groups, s);
 }
 
 }  // namespace
@@ -505,7 +526,10 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   ps.own_heads = p.Hkv * pl.own.row_tiles;
   ps.own_ctas = pl.own_ctas;
   ps.teams = pl.own.teams;
-  if (!fp32) {
+  if (fp32) {                          // (a page of 16 rows either way)
+    ps.unit_cost = ps.page_cost = 2;
+    ps.item_cost = 1;
+  } else {
     ps.unit_cost = a->d == 128 ? 1800 : 1400;
     ps.page_cost = 2700 / pl.own.teams;
     ps.item_cost = 1900 / pl.own.teams;
@@ -533,7 +557,7 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   e = launch_prefix_join(*a, p, s);
   if (e != cudaSuccess) return set_cuda_error(e, "attention join launch");
   if ((e = record(a->timing_events[1])) != cudaSuccess) return set_cuda_error(e, "cudaEventRecord");
-  set_launch_count(fp32 && a->G > 0 ? 4 : 3);
+  set_launch_count(pl.own_ctas > 0 && a->G > 0 ? 4 : 3);
   return MTP_OK;
 }
 

@@ -134,19 +134,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// sm100::mbar_wait that polls.
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-  if (sm100::mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = sm100::globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (sm100::mbar_test_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*abort) return false;
-      if (sm100::globaltimer() - t0 > sm100::kWaitTimeoutNs) return false;
-    }
-  }
-}
-
 // ---------------------------------------------------------------------- walk
 // This CTA's part of an item: tiles u0 .. u1 - 1 of keys.
 struct Seg {
@@ -190,8 +177,7 @@ struct Walk {
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_own_k,
-                  const __grid_constant__ CUtensorMap tm_own_v, const PrefixParams p) {
+                  const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
   using S = Smem<D>;
   constexpr int kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -244,8 +230,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     sm100::tma_prefetch_desc(&tm_q);
     sm100::tma_prefetch_desc(&tm_k);
     sm100::tma_prefetch_desc(&tm_v);
-    sm100::tma_prefetch_desc(&tm_own_k);
-    sm100::tma_prefetch_desc(&tm_own_v);
   }
   if (warp == 1) {
     sm100::tmem_alloc(tmem_slot, 512);
@@ -268,28 +252,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int own_before = pair * own_pairs / pairs;
   if ((pair + 1) * own_pairs / pairs > own_before) {
     // ----------------------------------------------------------- own pages
-    // (56 + 2 x 224 = 3 x 168 registers a thread)
+    // (72 + 2 x 216 = 3 x 168 registers a thread)
     const int cta = own_before * 2 + blockIdx.x % 2;
     if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-      own::producer<D>(tm_own_k, tm_own_v, p, smem, oc, cta);
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      own::producer<D>(tm_k, tm_v, p, smem, oc, cta);
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       own::consumer<D>(p, smem, oc, cta, warp - 4);
     }
     __syncthreads();
     if (warp == 1) sm100::tmem_dealloc(tmem, 512);
     return;
   }
-  Walk walk(p, blockIdx.x - own_before * 2);
-  Seg seg;
+  const int prefix_cta = blockIdx.x - own_before * 2;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {   // the whole warp
     return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort) ? 1 : 0) != 0;
-  };
-  // The same without being suspended, for the hand-overs between MMA and softmax.
-  auto poll = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort) ? 1 : 0) != 0;
   };
 
   // Registers: 168 a thread at launch; the softmax warps take what the others
@@ -298,6 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA
+      Walk walk(p, prefix_cta);
+      Seg seg;
       const uint64_t keep = sm100::l2_policy_evict_last();
       const PrefixShape& shape = p.view.shape;
       const int heads = min(p.group, kRows);
@@ -340,12 +321,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 sm100::mbar_arrive_expect_tx(&full[slot], S::kTile);
                 uint8_t* to = smem + S::kRing + slot * S::kTile;
-  #pragma unroll
+                const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;   // boxes of 32 keys x 64 dims
+#pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                  const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
-                  sm100::tma_load_4d(to + c * S::kChunk, map, &full[slot], c * 64, seg.kvh, 0, id0 < 0 ? p.num_blocks : id0, keep);
-                  sm100::tma_load_4d(to + c * S::kChunk + S::kChunk / 2, map, &full[slot], c * 64, seg.kvh, 0,
-                                     id1 < 0 ? p.num_blocks : id1, keep);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const int id = x < 2 ? id0 : id1;
+                    sm100::tma_load_4d(to + c * S::kChunk + x * (S::kChunk / 4), map, &full[slot], c * 64, seg.kvh, x % 2 * own::kKeys,
+                                       id < 0 ? p.num_blocks : id, keep);
+                  }
                 }
               }
               __syncwarp();
@@ -368,13 +352,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- MMA
       // (The whole warp walks, so that descriptors stay uniform; one elected
       // lane issues.)
+      Walk walk(p, prefix_cta);
+      Seg seg;
       constexpr uint32_t idesc_s = sm100::idesc_bf16_f32(128, kKeys);
       constexpr uint32_t idesc_o = sm100::idesc_bf16_f32(128, D) | (1u << 16);   // V MN-major
       const uint64_t qd = sm100::smem_desc_sw128_kmajor(sbase + S::kQ);
       const uint64_t kd = sm100::smem_desc_sw128_kmajor(sbase + S::kRing);
       const uint64_t vd = desc_mnmajor(sbase + S::kRing, S::kChunk);
       auto issue_s = [&](int x, int slot) {
-  #pragma unroll
+#pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t at = (uint64_t)((kk >> 2) * (S::kChunk >> 4) + (kk & 3) * 2);
           sm100::tc_mma_bf16(tmem + x * 128, qd + (uint64_t)(x * (S::kTile >> 4)) + at, kd + (uint64_t)(slot * (S::kTile >> 4)) + at,
@@ -405,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = wait(&full[v_slot], (uint32_t)((n / kSlots) & 1));
           for (int x = 0; x < seg.nsub && ok; ++x) {
             for (int h = 0; h < 2; ++h) {
-              ok = poll(&p_full[2 * x + h], p_phase[x]);
+              ok = wait(&p_full[2 * x + h], p_phase[x]);
               if (!ok) break;
               sm100::tc_fence_after();
               if (sm100::elect_one()) {
@@ -454,6 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------- softmax
+    Walk walk(p, prefix_cta);
+    Seg seg;
     const int x = (warp - 4) / 4, row = threadIdx.x % 128;       // TMEM lanes of warp w: 32 (w % 4) and up
     const uint32_t lane0 = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + x * 128 + lane0, to = tmem + kColO + x * 128 + lane0;
@@ -581,21 +569,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const mtp_prefix_attn_args& a, const PrefixParams& p, int ctas, cudaStream_t s) {
   const PrefixShape& shape = p.view.shape;
-  CUtensorMap tq, tk, tv, ok, ov;
+  CUtensorMap tq, tk, tv;
   const cuuint64_t group = (cuuint64_t)p.group, Hkv = (cuuint64_t)a.Hkv;
   const cuuint64_t qdims[4] = {(cuuint64_t)D, group, Hkv, (cuuint64_t)a.B * p.R};
   const cuuint64_t qstrides[3] = {D * 2, group * D * 2, (cuuint64_t)a.Hq * D * 2};
   const cuuint32_t qbox[4] = {64, (cuuint32_t)std::min(p.group, kRows), 1, (cuuint32_t)shape.tokens};
   const cuuint64_t dims[4] = {(cuuint64_t)D, Hkv, (cuuint64_t)kBlock, (cuuint64_t)a.num_blocks};
   const cuuint64_t strides[3] = {D * 2, Hkv * D * 2, kBlock * Hkv * D * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1}, own_box[4] = {64, 1, (cuuint32_t)own::kKeys, 1};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)own::kKeys, 1};
   if (!make_bf16_map(&tq, a.q, 4, qdims, qstrides, qbox) || !make_bf16_map(&tk, a.k_cache, 4, dims, strides, box) ||
-      !make_bf16_map(&tv, a.v_cache, 4, dims, strides, box) || !make_bf16_map(&ok, a.k_cache, 4, dims, strides, own_box) ||
-      !make_bf16_map(&ov, a.v_cache, 4, dims, strides, own_box))
+      !make_bf16_map(&tv, a.v_cache, 4, dims, strides, box))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_behind_append(prefix_kernel<D>, (unsigned)ctas, kThreads, Smem<D>::kBytes, s, tq, tk, tv, ok, ov, p);
+  return launch_behind_append(prefix_kernel<D>, (unsigned)ctas, kThreads, Smem<D>::kBytes, s, tq, tk, tv, p);
 }
 
 template <int D>
