@@ -1,11 +1,11 @@
 // Launch parameters and the shares of work of mtp_verify_attention_prefix,
-// between attention_prefix.cu, attention_prefix_tc.cu and the kernels that do
-// the requests' own pages (attention_window.cu, attention_window_mma.cu).
+// between attention_prefix.cu (entry, append, fp32 rows), attention_prefix_tc.cu
+// and attention_prefix_own.cuh (bf16 rows) and attention_prefix_join.cu.
 //
 // The query rows of a group that share a KV head are numbered token after
 // token (request, verify token), the heads of a token side by side, and cut
-// into tiles of kRows rows that hold whole tokens (kRows / group of them; of
-// a token with more heads than that, kRows heads at a time). An item is
+// into tiles of `rows` rows that hold whole tokens (rows / group of them; of
+// a token with more heads than that, `rows` heads at a time). An item is
 // `subs` such tiles of one group and KV head against all of the group's
 // prefix. The items form a line in units of `pages` pages of keys, cut into
 // an even share for each CTA. Item i's part from CTA c is partial result i + c:
@@ -31,7 +31,7 @@ struct alignas(16) PrefixGroup {
 };
 struct alignas(16) PrefixHead {
   int32_t total, ctas;              // units of the line, shares
-  int32_t size, more;               // units of a share; the first `more` have one more
+  int32_t narrow, pad;              // total x ctas fits 32 bits (a division of 64 costs what the join's other steps do together)
 };
 // Where a share begins.
 struct alignas(16) PrefixStart {
@@ -117,10 +117,17 @@ struct PrefixSchedule {
   unsigned* err;
 };
 
-__device__ __forceinline__ int prefix_cut(const PrefixHead& h, int c) { return c * h.size + min(c, h.more); }
+// Shares are cut as evenly as can be, so that where there are as many for each KV
+// head they are the same stretches of each: the heads' interleaved rows of a page
+// are then read at about the same time, which DRAM likes (a prefix of 32768
+// tokens, 16 rows, 8 KV heads: 46.7 us with uneven cuts, 41.9 us so).
+__device__ __forceinline__ int prefix_cut(const PrefixHead& h, int c) {
+  if (h.narrow) return (int)((uint32_t)c * (uint32_t)h.total / (uint32_t)max(h.ctas, 1));
+  return (int)((long long)c * h.total / max(h.ctas, 1));
+}
 __device__ __forceinline__ int prefix_cta_of(const PrefixHead& h, int unit) {
-  const int split = h.more * (h.size + 1);
-  return unit < split ? unit / (h.size + 1) : h.more + (unit - split) / h.size;
+  if (h.narrow) return (int)((((uint32_t)unit + 1u) * (uint32_t)h.ctas - 1u) / (uint32_t)max(h.total, 1));
+  return (int)((((long long)unit + 1) * h.ctas - 1) / max(h.total, 1));
 }
 
 __device__ __forceinline__ PrefixHead load_head(const PrefixHead* at) {
@@ -188,9 +195,8 @@ __device__ __forceinline__ int last_at_most(const int32_t* v, int n, int x) {
 }
 
 __device__ __forceinline__ PrefixHead make_shares(int total, int ctas) {
-  PrefixHead h{total, min(ctas, total), 1, 0};
-  if (h.ctas > 0) h.size = total / h.ctas, h.more = total - h.ctas * h.size;
-  return h;
+  const int n = min(ctas, total);
+  return PrefixHead{total, n, (long long)total * n < 0x7fffffffll, 0};
 }
 
 // The work of one CTA of THREADS threads. It stands between the lengths and
@@ -301,7 +307,10 @@ __device__ void prefix_schedule(const PrefixSchedule& w) {
     const float a = (float)base.x * w.unit_cost, z = (float)own * w.page_cost + (float)w.B * w.own_heads * w.item_cost;
     ctas = max(2, min(w.ctas - 2, 2 * (int)(w.ctas * a / (a + z) * 0.5f + 0.5f)));   // (pairs of CTAs do the same)
   }
-  const PrefixHead h = make_shares(base.x, ctas);
+  // (of one group as many for each KV head, where that leaves few CTAs out)
+  int n = min(ctas, base.x);
+  if (G == 1 && n % w.Hkv * 10 <= n) n -= n % w.Hkv;
+  const PrefixHead h = make_shares(base.x, n);
   if (tid == 0) *w.head = h;
   __syncthreads();                             // (writes to global memory too, for this CTA)
   for (int c = tid; c < h.ctas; c += THREADS) {
