@@ -625,14 +625,17 @@ int mtp_kv_append(const mtp_kv_append_args* args, void* stream);
  *   layouts as in mtp_verify_attention; group_starts [G+1] int32,
  *   prefix_blocks [G] int32
  * R = D+1 <= 16, d 64 or 128, Hq % Hkv == 0, Hkv <= 2^16, Hq / Hkv <= 2^15,
- * max_blocks <= 2^24, B max_blocks < 2^31, B R Hq <= 2^29, (B R Hq / 64 + 2 G
- * Hkv) max_blocks < 2^31. q, out, k_new, v_new and the caches must be 16-byte
- * aligned; a workspace is always needed, and one call at a time may use it.
+ * max_blocks <= 2^24, B max_blocks < 2^31, B R Hq <= 2^29, G <= 2^20; (B R Hq
+ * / 8 + (B + 2 G) Hkv) max_blocks <= 2^31 - 2^17 is always taken, more than that
+ * refused where the work cannot be counted in 31 bits. q, out, k_new, v_new and
+ * the caches must be 16-byte aligned; a workspace is always needed, and one call
+ * at a time may use it.
  * Errors: MTP_ERR_LENGTH for a bad length (as in mtp_verify_attention), a
  * prefix outside [0, max_blocks] and a context shorter than the prefix: that
  * request is skipped (nothing is appended, its rows of out stay as they were);
  * and for group_starts that decrease or leave [0, B]: every request then
- * attends all blocks of its own row by itself. A block with a bad id sets
+ * attends all blocks of its own row by itself. MTP_ERR_TREE as in
+ * mtp_verify_attention. A block with a bad id sets
  * MTP_ERR_BLOCK_ID and takes no part; a row that sees nothing else is 0. MLA
  * is not provided: its 128 query heads share one latent row a token, so
  * products bound it, not the read. */

@@ -371,7 +371,9 @@ struct PrefixPlan {
   size_t head, groups, group_of, first, starts, own_starts, parts, stats, own_head, pages, own_parts, own_stats, bytes;
 };
 
-// False: more items or units than 31 bits count.
+// False: more units of work than 31 bits count. (A KV head has at most B R group / 8 tiles of rows, B + 2 G more of which
+// are only part full, and a tile at most max_blocks units.)
+constexpr const char* kTooMany = "(B R Hq / 8 + (B + 2 G) Hkv) max_blocks is too large: more units of work than 31 bits count";
 bool plan_prefix(const mtp_prefix_attn_args& a, int sm_count, PrefixPlan* pl) {
   const int group = a.Hq / a.Hkv, R = a.D + 1, G = std::min(a.G, a.B);   // (empty groups have no items)
   const bool fp32 = fp32_rows(a);
@@ -451,7 +453,7 @@ size_t mtp_attention_prefix_workspace_size(const mtp_prefix_attn_args* a) {
   if (device_context(&err, &sm_count) != MTP_OK) return 0;
   PrefixPlan pl;
   if (!plan_prefix(*a, sm_count, &pl)) {
-    unsupported("(B R Hq / 64 + 2 G Hkv) max_blocks >= 2^31");
+    unsupported(kTooMany);
     return 0;
   }
   return pl.bytes;
@@ -467,7 +469,7 @@ int mtp_verify_attention_prefix(const mtp_prefix_attn_args* a, void* stream) {
   int sm_count = 0;
   if ((rc = device_context(&err, &sm_count)) != MTP_OK) return rc;
   PrefixPlan pl;
-  if (!plan_prefix(*a, sm_count, &pl)) return unsupported("(B R Hq / 64 + 2 G Hkv) max_blocks >= 2^31");
+  if (!plan_prefix(*a, sm_count, &pl)) return unsupported(kTooMany);
   if (!a->workspace || a->workspace_bytes < pl.bytes) {
     char buf[160];
     snprintf(buf, sizeof buf, "workspace of %zu bytes needed, %zu given", pl.bytes, a->workspace ? a->workspace_bytes : (size_t)0);

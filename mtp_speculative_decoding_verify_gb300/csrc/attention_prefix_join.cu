@@ -45,9 +45,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
   constexpr unsigned kUnits = D / 16 / SLICES;   // warps that share a row
   constexpr int kMost = SLICES == 1 ? 20 : SLICES == 2 ? 8 : 4;   // results read as one batch
   const unsigned lane = threadIdx.x % kWarp, unit = blockIdx.x * (kJoinThreads / kWarp) + threadIdx.x / kWarp;
-  const unsigned idx = unit / kUnits * 8 + lane / 4;
+  const unsigned place = unit / kUnits * 8 + lane / 4, idx = min(place, n_rows - 1);
   const int dim4 = unit % kUnits * SLICES * 4 + lane % 4;   // 4 dims from 4 dim4 + 16 x on
-  if (idx >= n_rows) return;
   const unsigned rows = p.rows, bh = idx / rows, r = idx - bh * rows, b = bh / (unsigned)p.Hkv, kvh = bh - b * p.Hkv;
   const PrefixView& v = p.view;
   const int first = __ldcg(v.first + b), gi = __ldcg(v.group_of + b);
@@ -63,13 +62,14 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
   const int64_t at1 = ((int64_t)b * heads + hr + c0) * step1 + (r - tile * step1);
   const float* o1 = v.own_parts + at1 * D;
   const float2* m1 = v.own_stats + at1;
-  if (first < 0) return;                     // flagged; its rows stay as they were
   PrefixRow pre{nullptr, nullptr, 0, 0};
   if (gi >= 0) pre = prefix_row(v, head, load_group(v.groups + gi), p.R, p.group, b, kvh, r, D);
   const int n = pre.n + n1, rows0 = v.shape.rows;
   // So far only what the append's launch left has been read, which was complete before the kernel ahead let this one
   // begin (if it did before its own end). What follows reads that kernel's results.
+  // A warp without rows waits too: the launch behind this one may only begin once the kernel ahead is done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (place >= n_rows || first < 0) return;  // (a flagged request's rows stay as they were)
 
   float m = -INFINITY, l = 0.0f;
   float4 o[SLICES];

@@ -315,6 +315,80 @@ def test_a_bad_block_takes_no_part(t, bad):
         assert (np.abs(got[b] - ref) <= bound(t, 64, len(at), ref, absolute, score)).all(), b
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_a_call_that_serves_nobody_and_one_right_behind_it(t):
+    """With the same workspace: the second begins only when the first is done."""
+    c = Case(t, 2, 8, 2, 64, groups=[(40, [0, 70, 9] * 9), (0, [6, 7, 70])])
+    g, ws = c.to_gpu(), torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    none = dict(g, ctx=torch.full_like(g["ctx"], -1))
+    for _ in range(3):
+        c.call(none, workspace=ws)
+        assert (g["out"] == 7.0).all()
+    for _ in range(3):
+        c.call(none, workspace=ws)
+        c.call(g, workspace=ws)
+    with pytest.raises(mv.MtpError, match="length"):
+        mv.sync_status()
+    c.check(g)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_a_malformed_tree_is_taken_as_a_chain_and_reported(t):
+    c = Case(t, 4, 8, 2, 64, groups=[(2, [0, 70, 9]), (1, [62])], tree=True)
+    g = c.to_gpu()
+    for b, k, par in ((0, 0, 0), (1, 2, 2), (3, 3, -1)):
+        g["parents"][b, k] = par
+        c.parents[b] = np.arange(-1, 3)
+    c.call(g)
+    with pytest.raises(mv.MtpError, match="tree"):
+        mv.sync_status()
+    c.check(g)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_blocks_beyond_32_bits(t):
+    """Blocks at both ends of a cache of more than 2^32 values."""
+    c = Case(t, 3, 16, 8, 128, groups=[(6, [0, 70, 9])], after=[100])
+    g = c.to_gpu()
+    nb = (1 << 32) // (64 * 8 * 128) + c.nb + 1
+    far = torch.arange(c.nb, device=DEV)
+    far[c.nb // 2:] += nb - c.nb
+    for n in "kv":
+        cache = torch.zeros(nb, 64, 8, 128, dtype=g[n].dtype, device=DEV)
+        cache[far] = g[n]
+        g[n] = cache
+    g["table"] = torch.where(g["table"] >= 0, far[g["table"].long().clamp(min=0)].int(), -1)
+    c.call(g)
+    mv.sync_status()
+    for n in "kv":
+        g[n] = g[n][far]
+    c.check(g)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_two_graphs_with_one_workspace(t):
+    """One after the other, with other sizes and from other streams."""
+    cases = [Case(t, 3, 16, 4, 64, groups=[(9, [5 * i for i in range(n)])], before=[40], seed=n) for n in (2, 31)]
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for c in cases:
+        g = c.to_gpu()
+        c.call(g, workspace=ws)
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            c.call(g, workspace=ws)
+        graphs.append((graph, g))
+    for _ in range(3):
+        for graph, g in graphs:
+            g["out"].fill_(7.0)
+            graph.replay()
+    torch.cuda.synchronize()
+    mv.sync_status()
+    for c, (_, g) in zip(cases, graphs):
+        c.check(g)
+
+
 def test_in_a_graph_on_its_own_stream():
     c = Case("bf16", 4, 32, 8, 128, groups=[(20, [10 * i for i in range(9)]), (3, [900, 3])])
     g = c.to_gpu()
