@@ -12,9 +12,9 @@ namespace {
 constexpr int kJoinThreads = 128;
 // 32 dims of a row a warp from 1024 rows on (2496 rows of trees: 21.0 us with 16,
 // 19.5 us so; 256 rows with 17 results: 15.0 us with 16, and 17.2 with those in
-// batches of 8), all from 8192 on (12288 rows: 54.9 with 32, 52.4 so; 7808 rows:
-// 105.5 with all, 102.1 with 32); calls in a graph.
-constexpr unsigned kSomeRows = 1024, kManyRows = 8192;
+// batches of 8), 64 from 4096 on (7808 rows: 101.5 us with 32, 105.0 with 128, 99.7
+// so; 24576 rows: 50.2 with 128, 48.7 so); calls in a graph.
+constexpr unsigned kSomeRows = 1024, kManyRows = 4096;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -24,10 +24,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 // out = (sum of o 2^(m - top)) / (sum of l 2^(m - top)) over a row's partial
 // results, the prefix's and then its own. A warp takes 8 rows of one KV head,
-// as they lie in the results, and SLICES x 16 dims, 4 of each a lane: all dims
-// where there are rows enough to fill the device, so that the finding of the
-// results is paid once a row; else fewer, for which more warps share the work and
-// more results are read as one batch. Bound by what it reads, out of L2 mostly
+// as they lie in the results, and SLICES x 16 dims, 4 of each a lane: the more
+// rows there are to fill the device, the more dims, so that the finding of the
+// results is paid less often; with fewer, more warps share the work and more
+// results are read as one batch. Bound by what it reads, out of L2 mostly
 // (32768 rows, 59 MB: 16 us), and by one round of reads where that is little.
 template <typename T>
 __device__ __forceinline__ void store4(T* to, float4 v);
@@ -143,7 +143,7 @@ cudaError_t launch_join(const PrefixParams& p, cudaStream_t s) {
   auto launch = [&](auto kernel, unsigned slices) {
     return launch_behind_append(kernel, (groups * (D / 16 / slices) + warps - 1) / warps, kJoinThreads, 0, s, p, rows);
   };
-  if (rows >= kManyRows) return launch(prefix_join_kernel<T, D, D / 16>, D / 16);
+  if (rows >= kManyRows) return launch(prefix_join_kernel<T, D, 4>, 4);
   if (rows >= kSomeRows) return launch(prefix_join_kernel<T, D, 2>, 2);
   return launch(prefix_join_kernel<T, D, 1>, 1);
 }
