@@ -87,12 +87,12 @@ struct PrefixParams {
   int max_blocks, num_blocks;
   float sm_scale;
   int row_tiles, row_warps;         // own pages: tiles of 16 row_warps rows of a request
-  int teams, stages;                // .. bf16: teams of a CTA, stages of a team
+  int teams, stages, own_keys;      // .. bf16: teams of a CTA, stages of a team, keys of a stage
   PrefixView view;
 };
 
 struct OwnPlan {
-  int row_tiles, row_warps, teams, stages;
+  int row_tiles, row_warps, teams, stages, keys;
 };
 OwnPlan plan_prefix_own(const mtp_prefix_attn_args& a);
 // bf16 rows: prefix and own pages.

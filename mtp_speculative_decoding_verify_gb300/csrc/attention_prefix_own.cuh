@@ -6,11 +6,17 @@
 // for another at the many beginnings and ends. So warps work in teams that have
 // nothing to do with each other: the row_warps warps of a team take 16 rows each
 // of one (request, KV head), page after page, out of a ring of shared-memory
-// stages of the team's own (32 keys of K and V each, by TMA), and leave a partial
-// result. The teams have an even share of the line of all pages (as the
-// prefix's CTAs of theirs, attention_prefix.h), cut wherever it falls; what a cut
-// parts is joined with the prefix's results, which have to be joined in any
-// case. Products are mma.sync m16n8k16: 16 rows need no more.
+// stages of the team's own (32 or 64 keys of K and V each, by TMA; which, lay_out
+// decides), and leave a partial result. The teams have an even share of the line
+// of all pages (as the prefix's CTAs of theirs, attention_prefix.h), cut wherever
+// it falls; what a cut parts is joined with the prefix's results, which have to be
+// joined in any case. Products are mma.sync m16n8k16: 16 rows need no more.
+//
+// Alone on the device: 16 rows of 128 dims 6.0 TB/s; 48 rows 4.5 TB/s, 64 dims 3.8,
+// bound by the chain from one stage's scores to its products (the tensor pipe is
+// busy 40 % of the time; the next scores ahead of a stage's softmax cost more
+// registers than they gave: 15 % slower). On 54 SMs, 16 rows get 90 GB/s an SM, of
+// the 121 that loads alone get.
 //
 // Four warps load, a lane for each team: it looks whether the team's next slot is
 // free, loads it, and has the block id after that on its way.
@@ -34,16 +40,16 @@ namespace mtp {
 namespace own {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKeys = 32;                 // of a stage
+constexpr int kBox = 32;                  // keys of a box
 constexpr int kWarps = 8, kLoaders = 4;   // consumers, warps that load
 constexpr int kMaxStages = 8;             // of a team
 
-template <int D>
+template <int D, int KEYS>
 struct Stage {
-  static constexpr int kHalf = kKeys * D * 2, kBytes = 2 * kHalf;   // K or V; both
+  static constexpr int kHalf = KEYS * D * 2, kBytes = 2 * kHalf;    // K or V; both
   // byte offset of the 16-byte chunk c of a key's row: boxes of 64 dims, 128-byte swizzle
   __device__ __forceinline__ static uint32_t at(int key, int c) {
-    return (c >> 3) * (kKeys * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+    return (c >> 3) * (KEYS * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
   }
 };
 
@@ -120,12 +126,17 @@ struct OwnWalk {
   }
 };
 
-// Stages of a page: 1 when the last verify token is in its first half.
-__device__ __forceinline__ int stages_of(int page, int ctx, int R) { return ctx + R - page * kBlock > kKeys ? 2 : 1; }
+// Boxes of a page: 1 when the last verify token is in its first half.
+__device__ __forceinline__ int boxes_of(int page, int ctx, int R) { return ctx + R - page * kBlock > kBox ? 2 : 1; }
+// .. and stages.
+template <int KEYS>
+__device__ __forceinline__ int stages_of(int page, int ctx, int R) {
+  return KEYS == kBlock ? 1 : boxes_of(page, ctx, R);
+}
 
 // Barriers and flags of the teams' stages, behind the stages. K and V of a stage
 // are slots of their own (2 x and 2 x + 1), so that a K is replaced as soon as the
-// scores are there: of a team's 32 KB, 24 are on their way at any time.
+// scores are there: of two stages' four slots, three are on their way at any time.
 struct Control {
   uint64_t *full, *empty;                 // [team][stage][2]
   volatile int* valid;                    // [team][stage] 0: the table named no block
@@ -136,10 +147,10 @@ struct Control {
 // for all is the slowest part of the CTA); cta: among those that do own pages. A
 // lane must not wait for global memory, since the others wait with it: the next
 // segment and the next block id are read ahead.
-template <int D>
+template <int D, int KEYS>
 __device__ __forceinline__ void producer(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PrefixParams& p, uint8_t* smem,
                                          const Control& c, int cta) {
-  using T = Stage<D>;
+  using T = Stage<D, KEYS>;
   const int team = threadIdx.x % kWarp * kLoaders + threadIdx.x / kWarp;
   volatile int* abort = c.abort;
   if (team < p.teams) {
@@ -162,7 +173,7 @@ __device__ __forceinline__ void producer(const CUtensorMap& tm_k, const CUtensor
     auto begin_page = [&]() {
       id = next_id;
       half = 0;
-      halves = stages_of(seg.first + i, seg.ctx, p.R);
+      halves = stages_of<KEYS>(seg.first + i, seg.ctx, p.R);
       if (i + 1 < seg.i1) next_id = read_id(seg, i + 1);
       else if (more_after) next_id = read_id(after, after.i0);
     };
@@ -178,11 +189,15 @@ __device__ __forceinline__ void producer(const CUtensorMap& tm_k, const CUtensor
         if (!is_v) my_valid[slot / 2] = good;
         if (good) {
           uint8_t* to = ring + slot * T::kHalf;
-          sm100::mbar_arrive_expect_tx(&my_full[slot], T::kHalf);
+          // (of a page that is one stage, the half that is needed: what lies in the other is masked)
+          const int boxes = KEYS == kBox ? 1 : boxes_of(seg.first + i, seg.ctx, p.R);
+          sm100::mbar_arrive_expect_tx(&my_full[slot], boxes * kBox * D * 2);
           const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+          for (int y = 0; y < boxes; ++y) {
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-            sm100::tma_load_4d(to + x * kKeys * 128, map, &my_full[slot], x * 64, kvh, half * kKeys, id, pol);
+            for (int x = 0; x < D / 64; ++x)
+              sm100::tma_load_4d(to + (x * KEYS + y * kBox) * 128, map, &my_full[slot], x * 64, kvh, (half + y) * kBox, id, pol);
+          }
         } else {
           raise_error(p.err, MTP_ERR_BLOCK_ID);
           sm100::mbar_arrive(&my_full[slot]);
@@ -219,9 +234,9 @@ __device__ __forceinline__ void producer(const CUtensorMap& tm_k, const CUtensor
 }
 
 // Consumer warp cw of the CTA's.
-template <int D>
+template <int D, int KEYS>
 __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, const Control& c, int cta, int cw) {
-  using T = Stage<D>;
+  using T = Stage<D, KEYS>;
   if (cw >= p.teams * p.row_warps) return;
   const int lane = threadIdx.x % kWarp;
   volatile int* abort = c.abort;
@@ -276,35 +291,40 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.0f, l_hi = 0.0f;   // maxima (log2 units), this lane's part of the sums
 
-    auto wait = [&](int slot) { return __all_sync(0xffffffffu, sm100::mbar_wait(&my_full[slot], phase, abort) ? 1 : 0) != 0; };
+    auto wait = [&](int slot) {                      // (most often there is nothing to wait for: a test takes less than a wait)
+      return __all_sync(0xffffffffu, sm100::mbar_test_wait(&my_full[slot], phase)) ||
+             __all_sync(0xffffffffu, sm100::mbar_wait(&my_full[slot], phase, abort) ? 1 : 0);
+    };
     auto release = [&](int slot) {
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&my_empty[slot]);
     };
-    auto consume = [&](int slot0, auto masked_c) {   // keys at slots slot0 .. slot0 + 31
+    // keys_c keys at slots slot0 and up, the stage's from key0 on; `begins` and `ends`: the stage's first, its last
+    auto consume = [&](int slot0, int key0, bool begins, bool ends, auto keys_c, auto masked_c) {
       constexpr bool kMasked = decltype(masked_c)::value;
-      const uint32_t kbase = sm100::smem_u32(ring + stage * T::kBytes), vbase = kbase + T::kHalf;
-      float s[4][4];
+      constexpr int kKeys = decltype(keys_c)::value;
+      const uint32_t kbase = sm100::smem_u32(ring + stage * T::kBytes) + key0 * 128, vbase = kbase + T::kHalf;
+      float s[kKeys / 8][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      for (int n = 0; n < kKeys / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
 #pragma unroll
-        for (int np = 0; np < 2; ++np) {
+        for (int np = 0; np < kKeys / 16; ++np) {
           uint32_t b0, b1, b2, b3;
           mma::ldsm_x4(kbase + T::at(np * 16 + (mi >> 1) * 8 + (lane & 7), kk * 2 + (mi & 1)), b0, b1, b2, b3);
           mma::mma_bf16_16816(s[2 * np], qa[kk], b0, b1);
           mma::mma_bf16_16816(s[2 * np + 1], qa[kk], b2, b3);
         }
       }
-      release(2 * stage);
+      if (ends) release(2 * stage);
       bool some_lo = true, some_hi = true;           // the row sees a slot of the stage
       if constexpr (kMasked) {
         const int rel = slot0 - ctx;                 // (node 0, at slot ctx, is on every path)
         some_lo = rel <= 0 || (rel < 32 && path_lo >> rel != 0);
         some_hi = rel <= 0 || (rel < 32 && path_hi >> rel != 0);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < kKeys / 8; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (tree_hidden(slot0 + n * 8 + 2 * t + (e & 1), ctx, e < 2 ? path_lo : path_hi)) s[n][e] = -INFINITY;
@@ -312,7 +332,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
       }
       float x_lo = -INFINITY, x_hi = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int n = 0; n < kKeys / 8; ++n) {
         x_lo = fmaxf(x_lo, fmaxf(s[n][0], s[n][1]));
         x_hi = fmaxf(x_hi, fmaxf(s[n][2], s[n][3]));
       }
@@ -328,9 +348,9 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
       m_lo = n_lo;
       m_hi = n_hi;
       float t_lo = 0.0f, t_hi = 0.0f;
-      uint32_t pa[2][4];
+      uint32_t pa[kKeys / 16][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int n = 0; n < kKeys / 8; ++n) {
         const float p0 = ex2(fmaf(s[n][0], f, -z_lo)), p1 = ex2(fmaf(s[n][1], f, -z_lo));
         const float p2 = ex2(fmaf(s[n][2], f, -z_hi)), p3 = ex2(fmaf(s[n][3], f, -z_hi));
         t_lo += p0 + p1;
@@ -344,7 +364,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
       uint32_t some = 0;        // probabilities that are not 0: of the i-th word of pa, bits 31 - i (upper half) and 15 - i
       if constexpr (kMasked) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < kKeys / 8; ++n) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) some |= ((pa[n >> 1][(n & 1) * 2 + e] + 0x7fff7fffu) & 0x80008000u) >> (2 * n + e);
         }
@@ -358,9 +378,9 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
           o[i][3] *= k_hi;
         }
       }
-      if (!(ok = wait(2 * stage + 1))) return;
+      if (begins && !(ok = wait(2 * stage + 1))) return;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kKeys / 16; ++k) {
 #pragma unroll
         for (int dp = 0; dp < D / 16; ++dp) {
           uint32_t b0, b1, b2, b3;
@@ -391,7 +411,7 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
               for (int e = 0; e < 2; ++e) {
                 // the dim of o[i][e] and o[i][e + 2]
                 const int dim = i * 8 + 2 * t + e;
-                const float v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt + T::at(key, dim / 8) + dim % 8 * 2));
+                const float v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt + T::at(key0 + key, dim / 8) + dim % 8 * 2));
                 if (!(fabsf(v) <= FLT_MAX)) {
                   if (see_lo) o[i][e] += v + none_lo;
                   if (see_hi) o[i][e + 2] += v + none_hi;
@@ -404,13 +424,23 @@ __device__ __forceinline__ void consumer(const PrefixParams& p, uint8_t* smem, c
     };
 
     for (int i = seg.i0; i < seg.i1 && ok; ++i) {
-      const int page = first + i, halves = stages_of(page, ctx, p.R);
+      const int page = first + i, halves = stages_of<KEYS>(page, ctx, p.R);
       for (int half = 0; half < halves; ++half) {
         if (!(ok = wait(2 * stage))) break;
         if (my_valid[stage]) {
-          const int slot0 = page * kBlock + half * kKeys;
-          if (slot0 + kKeys - 1 <= ctx) consume(slot0, std::false_type());
-          else consume(slot0, std::true_type());
+          const int slot0 = page * kBlock + half * KEYS;
+          // (where some keys are hidden, 32 at a time: there are few such stages, and twice the keys do not fit the registers)
+          using One = std::integral_constant<int, kBox>;
+          if (KEYS > kBox && slot0 + KEYS - 1 <= ctx) {
+            consume(slot0, 0, true, true, std::integral_constant<int, KEYS>(), std::false_type());
+          } else {
+            const int boxes = KEYS == kBox ? 1 : boxes_of(page, ctx, p.R);
+            for (int y = 0; y < boxes && ok; ++y) {
+              const int at = slot0 + y * kBox;
+              if (KEYS == kBox && at + kBox - 1 <= ctx) consume(at, y * kBox, y == 0, y + 1 == boxes, One(), std::false_type());
+              else consume(at, y * kBox, y == 0, y + 1 == boxes, One(), std::true_type());
+            }
+          }
           if (!ok) break;
         } else {
           if (!(ok = wait(2 * stage + 1))) break;

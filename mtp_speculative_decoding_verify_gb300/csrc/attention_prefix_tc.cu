@@ -59,7 +59,7 @@ struct Smem {
   static constexpr int kBar = kRing + kSlots * kTile;           // behind the stages of the own pages, too
   static constexpr int kBars = 2 * kSlots + 2 + 8 + kInfo + 1;
   static constexpr int kMisc = kBar + kBars * 8;                // marks [kInfo], abort, TMEM base
-  static constexpr int kOwnStages = kBar / own::Stage<D>::kBytes;
+  static constexpr int kOwnStages = kBar / own::Stage<D, own::kBox>::kBytes;   // of 32 keys
   static constexpr int kOwn = kMisc + kInfo * 4 + 8;            // own::Control
   static constexpr int kBytes = kOwn + kOwnStages * 36 + 1024;
   static_assert(kBytes <= 232448, "227 KB of shared memory");
@@ -174,7 +174,7 @@ struct Walk {
   }
 };
 
-template <int D>
+template <int D, int OWN_KEYS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
@@ -256,10 +256,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cta = own_before * 2 + blockIdx.x % 2;
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      own::producer<D>(tm_k, tm_v, p, smem, oc, cta);
+      own::producer<D, OWN_KEYS>(tm_k, tm_v, p, smem, oc, cta);
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      own::consumer<D>(p, smem, oc, cta, warp - 4);
+      own::consumer<D, OWN_KEYS>(p, smem, oc, cta, warp - 4);
     }
     __syncthreads();
     if (warp == 1) sm100::tmem_dealloc(tmem, 512);
@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int x = 0; x < 4; ++x) {
                     const int id = x < 2 ? id0 : id1;
-                    sm100::tma_load_4d(to + c * S::kChunk + x * (S::kChunk / 4), map, &full[slot], c * 64, seg.kvh, x % 2 * own::kKeys,
+                    sm100::tma_load_4d(to + c * S::kChunk + x * (S::kChunk / 4), map, &full[slot], c * 64, seg.kvh, x % 2 * own::kBox,
                                        id < 0 ? p.num_blocks : id, keep);
                   }
                 }
@@ -576,13 +576,14 @@ cudaError_t launch(const mtp_prefix_attn_args& a, const PrefixParams& p, int cta
   const cuuint32_t qbox[4] = {64, (cuuint32_t)std::min(p.group, kRows), 1, (cuuint32_t)shape.tokens};
   const cuuint64_t dims[4] = {(cuuint64_t)D, Hkv, (cuuint64_t)kBlock, (cuuint64_t)a.num_blocks};
   const cuuint64_t strides[3] = {D * 2, Hkv * D * 2, kBlock * Hkv * D * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)own::kKeys, 1};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)own::kBox, 1};
   if (!make_bf16_map(&tq, a.q, 4, qdims, qstrides, qbox) || !make_bf16_map(&tk, a.k_cache, 4, dims, strides, box) ||
       !make_bf16_map(&tv, a.v_cache, 4, dims, strides, box))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  const auto kernel = p.own_keys == kBlock ? prefix_kernel<D, kBlock> : prefix_kernel<D, own::kBox>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_behind_append(prefix_kernel<D>, (unsigned)ctas, kThreads, Smem<D>::kBytes, s, tq, tk, tv, p);
+  return launch_behind_append(kernel, (unsigned)ctas, kThreads, Smem<D>::kBytes, s, tq, tk, tv, p);
 }
 
 template <int D>
@@ -590,9 +591,17 @@ void lay_out(const mtp_prefix_attn_args& a, OwnPlan* pl) {
   const int blocks = (a.Hq / a.Hkv * (a.D + 1) + 15) / 16;     // of 16 rows
   pl->row_tiles = (blocks + own::kWarps - 1) / own::kWarps;
   pl->row_warps = (blocks + pl->row_tiles - 1) / pl->row_tiles;
-  // As many teams as there are warps for, with two stages each at least.
-  pl->teams = std::min(own::kWarps / pl->row_warps, Smem<D>::kOwnStages / 2);
-  pl->stages = std::min(own::kMaxStages, Smem<D>::kOwnStages / pl->teams);
+  // As many teams as there are warps for, with two stages each at least. Stages of 64 keys where that takes no team away: a
+  // warp then waits, and goes through a softmax, half as often, which is most of what it does (128 requests of 48 rows,
+  // 1000 own tokens: 147 us with 32, 128 so; 48 rows of 64 dims: 53 and 46; of 100 tokens: 42.9 and 43.2, 21.5 and 21.4).
+  // Or one team of eight where there is work for all (16 rows of 64 dims, 1024 items of 1000 tokens: 65.0 and 54.4 us; 64
+  // items of 8000: 33.4 and 36.5).
+  constexpr int kStages = Smem<D>::kOwnStages, kManyItems = 1024;
+  const int teams = std::min(own::kWarps / pl->row_warps, kStages / 2), fewer = std::min(teams, kStages / 4);
+  const bool many = (long long)a.B * a.Hkv * pl->row_tiles >= kManyItems;
+  pl->keys = fewer == teams || (many && fewer * 8 >= teams * 7) ? kBlock : own::kBox;
+  pl->teams = pl->keys == kBlock ? fewer : teams;
+  pl->stages = std::min(own::kMaxStages, kStages * own::kBox / pl->keys / pl->teams);
 }
 
 }  // namespace
