@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kAppendThreads) prefix_append_kernel(const uin
 // requests, else 16, and then one launch does both lines (2 rows of 8 KV heads
 // behind 6400 tokens: 84 us with 64, 47 us with 16; 4 requests of 4 rows behind
 // 1024: 15.4 us in two launches, 13.6 in one). FFMA and shared memory bound it: 32
-// TFLOP/s (512 rows a KV head behind 2048 tokens), 1.5 TB/s over own pages of 16
+// TFLOP/s (512 rows a KV head behind 2048 tokens), 1.4 TB/s over own pages of 16
 // rows.
 // Own pages: a hidden slot's P is held as -1 and takes no part in the products (0
 // x NaN), and slots behind the last token are read as 0.
