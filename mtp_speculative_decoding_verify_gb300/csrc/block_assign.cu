@@ -9,10 +9,14 @@
 // what is taken has no gaps.
 //
 // A step's call (a few tokens a request) is one CTA, a thread a request: a
-// chain of five dependent reads bounds it. Longer appends go by pieces of 32
-// blocks, one entry a lane: the first launch counts each piece's missing
-// entries, the second sums the counts before its own (they are few, and in
-// L2), takes its blocks and writes the slots, 8 bytes a token.
+// chain of five dependent reads bounds it (256 requests: 3.5 us). Longer appends
+// go by pieces of 32 blocks, one entry a lane: the first launch counts each
+// piece's missing entries, the second sums the counts before its own (they are
+// few, and in L2), takes its blocks and writes the slots, 8 bytes a token (64
+// requests of 500-1500 tokens: 5.8 us, 32 of 5000-65000: 8.5). Where there are
+// many pieces, so that each piece's sum would take as long as the rest, the first
+// launch also counts by groups of pieces, and a sum is of those and of a part of
+// one group (65536 requests: 1754 -> 508 us; with 3000 pieces it loses: 12 us, 33 so).
 #include <algorithm>
 
 #include "attention_window.h"
@@ -29,6 +33,8 @@ namespace {
 
 constexpr int kPieceBlocks = kWarp, kPieceTokens = kPieceBlocks * kBlock;
 constexpr int kStepThreads = 1024, kPieceThreads = 256;
+constexpr int kGroup = kPieceThreads;    // pieces of a group
+constexpr int kManyPieces = 16384;       // from which on there are groups
 
 struct AssignParams {
   int32_t* table;
@@ -37,6 +43,7 @@ struct AssignParams {
   int64_t* slots;
   int32_t* taken;
   int32_t* counts;             // [1 + pieces]: the free list's length, missing entries of each piece
+  int32_t* sums;               // [groups]: missing entries of the pieces of each group, if they are counted
   int B, T, max_blocks, capacity, pieces;
   unsigned* err;
 };
@@ -214,11 +221,14 @@ __device__ __forceinline__ int piece_block(const Req& r, int k, int lane) {
   return k >= 0 && r.n > 0 && i <= (r.L + r.n - 1) / kBlock ? i : -1;
 }
 
+// GROUPS: a CTA counts a group of kGroup pieces; else a piece a warp.
+template <bool GROUPS>
 __global__ void __launch_bounds__(kPieceThreads) assign_count_kernel(const AssignParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x % kWarp;
-  const int piece = blockIdx.x * (kPieceThreads / kWarp) + threadIdx.x / kWarp;
-  const int b_taken = blockIdx.x * kPieceThreads + threadIdx.x;
+  __shared__ int s_sum;
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, warps = kPieceThreads / kWarp;
+  const int b_taken = blockIdx.x * kPieceThreads + threadIdx.x;   // (as many CTAs have B threads: a request has two pieces)
+  if (GROUPS && threadIdx.x == 0) s_sum = 0;   // (starts_ok is a barrier)
   const bool ok = starts_ok(p);
   if (blockIdx.x == 0 && threadIdx.x == 0) {   // the second launch lowers it while others still need it
     const int listed = *p.free_count, free0 = free_blocks(p, listed);
@@ -232,16 +242,28 @@ __global__ void __launch_bounds__(kPieceThreads) assign_count_kernel(const Assig
     if (r.error) raise_error(p.err, r.error);
     p.taken[b_taken] = r.error || r.n > 0 ? -1 : 0;
   }
-  if (!ok || piece >= p.pieces) return;
-  int first;
-  const int b = piece_request(p, piece, &first);
-  const Req r = load_request(p, b);
-  const int i = piece_block(r, piece - first, lane);
-  const bool miss = r.error == 0 && i * (int64_t)kBlock >= r.L && i >= 0 && p.table[(int64_t)b * p.max_blocks + i] < 0;
-  const unsigned m = __ballot_sync(0xffffffffu, miss);
-  if (lane == 0) p.counts[1 + piece] = __popc(m);
+  if (!ok) return;
+  int sum = 0;
+  for (int x = warp; x < (GROUPS ? kGroup : warps); x += warps) {
+    const int piece = blockIdx.x * (GROUPS ? kGroup : warps) + x;
+    if (piece >= p.pieces) break;
+    int first;
+    const int b = piece_request(p, piece, &first);
+    const Req r = load_request(p, b);
+    const int i = piece_block(r, piece - first, lane);
+    const bool miss = r.error == 0 && i * (int64_t)kBlock >= r.L && i >= 0 && p.table[(int64_t)b * p.max_blocks + i] < 0;
+    const int c = __popc(__ballot_sync(0xffffffffu, miss));
+    if (lane == 0) p.counts[1 + piece] = c;
+    sum += c;
+  }
+  if constexpr (GROUPS) {
+    if (lane == 0 && sum != 0) atomicAdd(&s_sum, sum);
+    __syncthreads();
+    if (threadIdx.x == 0) p.sums[blockIdx.x] = s_sum;
+  }
 }
 
+template <bool GROUPS>
 __global__ void __launch_bounds__(kPieceThreads) assign_pieces_kernel(const AssignParams p) {
   __shared__ int s_id[kPieceBlocks];
   __shared__ long long s_sum[2][kPieceThreads / kWarp];
@@ -259,11 +281,22 @@ __global__ void __launch_bounds__(kPieceThreads) assign_pieces_kernel(const Assi
   const int stop = first + n_pieces;
   long long before = 0, end = 0;
   int own = 0;                 // of this request
-  for (int x = tid; x < stop; x += kPieceThreads) {
-    const int c = __ldcg(p.counts + 1 + x);
-    end += c;
-    if (x < piece) before += c;
-    if (x >= first) own += c;
+  if constexpr (GROUPS) {      // the groups before piece's and before the last, then the pieces of these two
+    for (int g = tid; g < stop / kGroup; g += kPieceThreads) {
+      const int c = __ldcg(p.sums + g);
+      end += c;
+      if (g < piece / kGroup) before += c;
+    }
+    for (int x = piece / kGroup * kGroup + tid; x < piece; x += kPieceThreads) before += __ldcg(p.counts + 1 + x);
+    for (int x = stop / kGroup * kGroup + tid; x < stop; x += kPieceThreads) end += __ldcg(p.counts + 1 + x);
+    for (int x = first + tid; x < stop; x += kPieceThreads) own += __ldcg(p.counts + 1 + x);
+  } else {
+    for (int x = tid; x < stop; x += kPieceThreads) {
+      const int c = __ldcg(p.counts + 1 + x);
+      end += c;
+      if (x < piece) before += c;
+      if (x >= first) own += c;
+    }
   }
   own = __syncthreads_or(own);
 #pragma unroll
@@ -310,6 +343,14 @@ __global__ void __launch_bounds__(kPieceThreads) assign_pieces_kernel(const Assi
 
 int pieces_of(int B, int T) { return T / kPieceTokens + 2 * B; }
 
+template <bool GROUPS>
+cudaError_t launch_pieces(const AssignParams& p, cudaStream_t s) {
+  const int of_cta = GROUPS ? kGroup : kPieceThreads / kWarp;
+  assign_count_kernel<GROUPS><<<(p.pieces + of_cta - 1) / of_cta, kPieceThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_behind_append(assign_pieces_kernel<GROUPS>, p.pieces, kPieceThreads, 0, s, p);
+}
+
 int fail(const char* msg) { return set_error(MTP_INVALID_ARG, msg); }
 
 int check_assign(const mtp_block_assign_args* a) {
@@ -336,7 +377,8 @@ extern "C" {
 
 size_t mtp_block_assign_workspace_size(int32_t B, int32_t T) {
   if (B < 0 || T < 0 || B > (1 << 20)) return 0;
-  return (((size_t)mtp::pieces_of(B, T) + 1) * sizeof(int32_t) + 255) / 256 * 256;
+  const size_t pieces = mtp::pieces_of(B, T);
+  return ((1 + pieces + pieces / mtp::kGroup + 1) * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 int kv_block_assign(const mtp_block_assign_args* a, void* stream) {
@@ -361,19 +403,20 @@ int kv_block_assign(const mtp_block_assign_args* a, void* stream) {
   p.max_blocks = a->max_blocks;
   p.capacity = a->free_capacity;
   p.pieces = mtp::pieces_of(a->B, a->T);
+  p.sums = p.counts + 1 + p.pieces;
   p.err = err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (a->T <= 16 * a->B && a->T <= 16384) {
+  // (us in one CTA and by pieces: 256 requests of 16 tokens 5.0, 6.4, of 48 11.2, 7.4; 1024 of 16 11.7, 11.9; 4096 of 16
+  // 42, 34, of 4 16.4, 33.8; 16384 of 4 60, 130. Up to 65536 tokens, since one long request may be among them, and a warp
+  // walks it alone.)
+  if ((a->T <= 16 * (long long)a->B && a->T <= 16384) || (a->T <= 8 * (long long)a->B && a->T <= 65536)) {
     mtp::assign_step_kernel<<<1, mtp::kStepThreads, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return mtp::set_cuda_error(e, "block assign launch");
     mtp::set_launch_count(1);
     return MTP_OK;
   }
-  const int warps = mtp::kPieceThreads / mtp::kWarp;
-  mtp::assign_count_kernel<<<(p.pieces + warps - 1) / warps, mtp::kPieceThreads, 0, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return mtp::set_cuda_error(e, "block assign launch");
-  e = mtp::launch_behind_append(mtp::assign_pieces_kernel, p.pieces, mtp::kPieceThreads, 0, s, p);
+  e = p.pieces > mtp::kManyPieces ? mtp::launch_pieces<true>(p, s) : mtp::launch_pieces<false>(p, s);
   if (e != cudaSuccess) return mtp::set_cuda_error(e, "block assign launch");
   mtp::set_launch_count(2);
   return MTP_OK;

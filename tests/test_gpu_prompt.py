@@ -81,6 +81,17 @@ def test_assign_to_the_last_entry(name, share):
     pool.check(pool.call())
 
 
+@pytest.mark.parametrize("n", [[3, 8, 0, 21], [40, 0, 9, 300]])
+@pytest.mark.parametrize("share", [1.0, 0.6])
+def test_assign_for_more_requests_than_a_batch_has(n, share):
+    """Steps of many requests by one CTA, and longer appends by more pieces than are summed one by one."""
+    B = 9001
+    lens, n = [(37 * b) % 500 for b in range(B)], [n[b % 4] for b in range(B)]
+    want = sum(max(0, -(-(a + m) // 64) - -(-a // 64)) for a, m in zip(lens, n))
+    pool = Pool(lens, n, free=int(want * share), head=1)
+    pool.check(pool.call())
+
+
 @pytest.mark.parametrize("n", [[3, 10, 2, 16], [300, 10, 4000, 129]])
 def test_assign_keeps_blocks_that_are_there(n):
     """Blocks handed out before, gaps among them, and a refused request asked again."""
