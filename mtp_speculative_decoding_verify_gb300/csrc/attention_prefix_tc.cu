@@ -25,6 +25,10 @@
 // passes it by 2^8 (O is then rescaled in TMEM, a rare branch): P and l stay
 // relative to it, and fp32 and bf16 have the room.
 //
+// A unit (256 rows x 128 keys) takes 1.70 us at 128 dims, which is 1.5 PFLOP/s on
+// all SMs; its products without the softmax 1.52, at 64 dims 1.41 and 1.11. 4096
+// rows of 8 KV heads behind 8192 tokens: 116 us, tensor pipe 55 % of the time.
+//
 // Warps: 0 TMA (Q by boxes of whole tokens, K and V pages in a ring of tiles),
 // 1 MMA, 4-7 and 8-11 softmax.
 #include <cuda.h>
