@@ -692,6 +692,8 @@ def mtp_kv_append(k_new, v_new, slot_map, k_cache, v_cache, *, stream=None):
         k_new = k_new.unsqueeze(1)
     T, Hkv, d = shape = k_new.shape
     nb, dt, index = k_cache.shape[0], k_new.dtype, _cuda_index(k_new, "k_new")
+    if T > 2 ** 31 - 1:              # (the struct's field would take it modulo 2^32, and rows would be left out unsaid)
+        raise ValueError("k_new: more than 2^31 - 1 tokens")
     k_stride = _token_rows(k_new, "k_new", index, dt, shape)
     if v_new is not None and v_cache is not None:
         d_v = v_new.shape[-1]
