@@ -336,9 +336,10 @@ __global__ void __launch_bounds__(kPieceThreads) assign_pieces_kernel(const Assi
     if (own != 0) atomicMin(p.free_count, free0 - (int)end);
   }
   __syncthreads();
-  const int p0 = max(r.L, i0 * kBlock), p1 = min(r.L + r.n, (i0 + kPieceBlocks) * kBlock);
-  for (int pos = p0 + tid; pos < p1; pos += kPieceThreads)
-    p.slots[r.s0 + pos - r.L] = slot_of(s_id[pos / kBlock - i0], pos);
+  // Positions count from the piece's first: a refused request may have up to 2^31 - 1 tokens, and the piece's end is then
+  // beyond 31 bits.
+  const int at = i0 * kBlock, x0 = max(r.L - at, 0), x1 = min(r.L + r.n - at, kPieceTokens);
+  for (int x = x0 + tid; x < x1; x += kPieceThreads) p.slots[r.s0 + (at - r.L) + x] = slot_of(s_id[x / kBlock], x);
 }
 
 int pieces_of(int B, int T) { return T / kPieceTokens + 2 * B; }
