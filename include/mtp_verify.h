@@ -557,8 +557,10 @@ int kv_window_release(const mtp_window_release_args* args, void* stream);
  * taken[b] is -1 and all else stays as it was. *free_count outside [0,
  * free_capacity] sets MTP_ERR_FREE_LIST and counts as 0. An entry < 0 of the
  * free list sets MTP_ERR_BLOCK_ID; it goes into the table, with slots of -1.
- * seq_lens is read only (advance it once the tokens are in the cache). No
- * two requests' ranges of new blocks may share a table row.
+ * seq_lens is read only (advance it once the tokens are in the cache). A
+ * refused request must not be in the step that follows: the attention calls
+ * report its missing blocks, and kv_rollback would put their entries, -1, on
+ * the free list.
  *   block_table [B, max_blocks] int32 (in/out); seq_lens [B] int32
  *   starts [B+1] int32; free_list [free_capacity] int32; free_count [1] int32 (in/out)
  *   slot_map [T] int64 (out); taken [B] int32 (out)
@@ -585,7 +587,9 @@ int kv_block_assign(const mtp_block_assign_args* args, void* stream);
  * Token t's K and V rows are copied to slot slot_map[t] of the cache (block
  * slot / 64, offset slot % 64). A slot < 0 is skipped (a padded token, a
  * refused request); one beyond the cache sets MTP_ERR_BLOCK_ID and is skipped.
- * Two tokens with the same slot leave that slot's values undefined.
+ * Two tokens with the same slot leave that slot's values undefined. The 8-bit
+ * cache has no append by slot, since a block's scale goes by all that it holds:
+ * mtp_kv8_append finds the slots in the table.
  *   k_new [T, Hkv, d_qk], v_new [T, Hkv, d_v] dtype, the tokens k_stride and
  *         v_stride elements apart (>= Hkv d; a view of a fused projection's
  *         output will do), a token's values contiguous
@@ -618,7 +622,14 @@ int mtp_kv_append(const mtp_kv_append_args* args, void* stream);
  * lengths. A prefix ends with a full block (a prompt's last tokens that fill
  * none are each request's own). Groups may be empty, have one request or no
  * prefix; requests in no group attend all by themselves. G = 0: no groups.
- * Own blocks of a request must not be other requests' (they are written).
+ * Own blocks of a request must not be other requests' (they are written), and
+ * kv_window_release is not for tables that share blocks (it would give one back
+ * once a request). With bf16 rows sharing pays from about four requests a
+ * group and a thousand shared tokens on; for less mtp_verify_attention is faster
+ * (fp32 rows: this call). The workspace has room for partial results of 256 rows (fp32:
+ * of 16 or 64) wherever a group's rows of a KV head begin as many: 133 KB each
+ * at d = 128, which many small groups feel (1024 groups of one request, 8 KV
+ * heads: 1.7 GB; of 512 pairs 0.9).
  * Sums and softmax statistics are fp32; with bf16 rows a probability is
  * rounded to bf16, as in mtp_verify_attention. Infinities and NaN act as in
  * mtp_verify_attention_window.
@@ -638,7 +649,9 @@ int mtp_kv_append(const mtp_kv_append_args* args, void* stream);
  * mtp_verify_attention. A block with a bad id sets
  * MTP_ERR_BLOCK_ID and takes no part; a row that sees nothing else is 0. MLA
  * is not provided: its 128 query heads share one latent row a token, so
- * products bound it, not the read. */
+ * products bound it, not the read. Nor are the 8-bit cache and windows:
+ * mtp_verify_attention_kv8 and mtp_verify_attention_window take tables that
+ * share full blocks, and read them once a request. */
 typedef struct {
   const void* q;
   const void* k_new;

@@ -13,7 +13,11 @@ constexpr int kJoinThreads = 128;
 // 32 dims of a row a warp from 1024 rows on (2496 rows of trees: 21.0 us with 16,
 // 19.5 us so; 256 rows with 17 results: 15.0 us with 16, and 17.2 with those in
 // batches of 8), 64 from 4096 on (7808 rows: 101.5 us with 32, 105.0 with 128, 99.7
-// so; 24576 rows: 50.2 with 128, 48.7 so); calls in a graph.
+// so; 24576 rows: 50.2 with 128, 48.7 so); calls in a graph. Where they cross goes by
+// the number of results, too: D = 3, 32/8 x 128, 2048 shared tokens, up to 200 own, us
+// with 16, 32 and 64: 512 rows 15.2, 17.6, 23.0; 1024 16.8, 18.4, 23.6; 1536 21.6, 20.7,
+// 25.3; 2048 22.2, 20.1, 24.2; 4096 31.8, 26.0, 26.5; 6144 38.2, 27.8, 27.3; 8192 45.7,
+// 33.2, 30.4.
 constexpr unsigned kSomeRows = 1024, kManyRows = 4096;
 
 __device__ __forceinline__ float ex2(float x) {

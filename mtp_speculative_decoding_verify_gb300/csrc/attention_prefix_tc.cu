@@ -27,7 +27,9 @@
 //
 // A unit (256 rows x 128 keys) takes 1.70 us at 128 dims, which is 1.5 PFLOP/s on
 // all SMs; its products without the softmax 1.52, at 64 dims 1.41 and 1.11. 4096
-// rows of 8 KV heads behind 8192 tokens: 116 us, tensor pipe 55 % of the time.
+// rows of 8 KV heads behind 8192 tokens are 92 us of all SMs by that; the whole call
+// takes 131 (256 requests with one own page each, append and join), and a profile
+// of this kernel, with cold caches, 116, tensor pipe 55 % of the time.
 //
 // Warps: 0 TMA (Q by boxes of whole tokens, K and V pages in a ring of tiles),
 // 1 MMA, 4-7 and 8-11 softmax.
@@ -598,8 +600,10 @@ void lay_out(const mtp_prefix_attn_args& a, OwnPlan* pl) {
   // As many teams as there are warps for, with two stages each at least. Stages of 64 keys where that takes no team away: a
   // warp then waits, and goes through a softmax, half as often, which is most of what it does (128 requests of 48 rows,
   // 1000 own tokens: 147 us with 32, 128 so; 48 rows of 64 dims: 53 and 46; of 100 tokens: 42.9 and 43.2, 21.5 and 21.4).
-  // Or one team of eight where there is work for all (16 rows of 64 dims, 1024 items of 1000 tokens: 65.0 and 54.4 us; 64
-  // items of 8000: 33.4 and 36.5).
+  // Or one team of eight where there is work for all: without a prefix (16 rows of 64 dims, us with 32 keys and with 64) 1024
+  // items of 1000 tokens 65.2, 54.5, of 500 to 1500 69.6, 68.5; 512 of 1000 37.8, 33.9; 64 of 8000 36.1, 38.3, of 500 to 1500
+  // 17.7, 18.0. Behind a prefix it can lose, since the SMs are shared out by costs that do not know the stages: 1024 items of
+  // 1000 behind 2048 tokens 69.5, 87.3; 2048 of 250 behind 4096 68.9, 74.6, of 1000 144.7, 143.6.
   constexpr int kStages = Smem<D>::kOwnStages, kManyItems = 1024;
   const int teams = std::min(own::kWarps / pl->row_warps, kStages / 2), fewer = std::min(teams, kStages / 4);
   const bool many = (long long)a.B * a.Hkv * pl->row_tiles >= kManyItems;

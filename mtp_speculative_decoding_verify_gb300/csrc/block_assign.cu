@@ -16,7 +16,9 @@
 // requests of 500-1500 tokens: 5.8 us, 32 of 5000-65000: 8.5). Where there are
 // many pieces, so that each piece's sum would take as long as the rest, the first
 // launch also counts by groups of pieces, and a sum is of those and of a part of
-// one group (65536 requests: 1754 -> 508 us; with 3000 pieces it loses: 12 us, 33 so).
+// one group. A CTA then counts 256 pieces, not 8, which costs more until there are
+// some 14000 (us one by one and by groups: 2056 pieces 12, 32; 8200 39, 52; 16420 89,
+// 75; 32840 244, 124; 131200 2970, 474).
 #include <algorithm>
 
 #include "attention_window.h"
@@ -408,9 +410,10 @@ int kv_block_assign(const mtp_block_assign_args* a, void* stream) {
   p.err = err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  // (us in one CTA and by pieces: 256 requests of 16 tokens 5.0, 6.4, of 48 11.2, 7.4; 1024 of 16 11.7, 11.9; 4096 of 16
-  // 42, 34, of 4 16.4, 33.8; 16384 of 4 60, 130. Up to 65536 tokens, since one long request may be among them, and a warp
-  // walks it alone.)
+  // (us in one CTA and by pieces: 256 requests of 16 tokens 5.4, 6.4, of 48 10.9, 6.5; 1024 of 16 12.2, 11.5; 4096 of 16
+  // 44.5, 38.5, of 4 16.5, 38.8; 16384 of 4 61, 122. Up to 65536 tokens, since one long request may be among them, and a
+  // warp walks it alone, which the rule does not see: 256 requests, 255 of one token and one of 3841, 11.1, 6.2; 1024, one
+  // of 15361, 36, 12; 8192, one of 8000, 38, 74, one of 30000 83, 74, one of 57000 143, 74.)
   if ((a->T <= 16 * (long long)a->B && a->T <= 16384) || (a->T <= 8 * (long long)a->B && a->T <= 65536)) {
     mtp::assign_step_kernel<<<1, mtp::kStepThreads, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return mtp::set_cuda_error(e, "block assign launch");

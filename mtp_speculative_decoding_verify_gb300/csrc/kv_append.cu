@@ -123,8 +123,10 @@ extern "C" int mtp_kv_append(const mtp_kv_append_args* a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int most = std::max(p.k_vecs, p.v_vecs);
   // Lanes a token: 8 for short rows, and for many tokens of middling ones, since warps cost more than loads there (us with 8
-  // and with 32 lanes: 65536 tokens of 128 bytes 5.5, 13.7; of 1152 bytes 26.1, 29.9; 8192 of them 3.7, 3.9; but 1024 of them
-  // 2.9, 2.2, and 65536 of 2 KB 82.9, 79.3).
+  // and with 32 lanes, K alone: 65536 tokens of 128 bytes 5.5, 13.7; of 1152 bytes 26.1, 29.5; 8192 of them 3.7, 3.8, 4096
+  // 3.1, 2.7, 1024 2.9, 2.0. 1024 bytes cross between 4096 tokens (2.8, 2.9) and 2048 (2.9, 2.2), 1536 at 8192 (4.2, 4.2;
+  // 65536 32.2, 34.3), 512 at 4096 (2.3, 2.5; 2048 2.3, 2.2). Close below 2 KB 32 lanes would be the better ones: 2032 bytes,
+  // 8192 tokens 5.3, 4.7, 65536 42.8, 41.5).
   const bool few = most <= 16 || (p.T >= 8192 && most < 128);
   const cudaError_t e = few ? mtp::launch<8>(p, s) : mtp::launch<32>(p, s);
   if (e != cudaSuccess) return mtp::set_cuda_error(e, "kv append launch");
